@@ -79,7 +79,12 @@ typedef struct moe_problem {
 
 /* Rows of the permuted buffers: R = T*K + S*T (routed rows, then T shared rows). */
 
-enum { MOE_CALL_ROUTE = 0, MOE_CALL_PERMUTE = 1, MOE_CALL_EXPERT_FFN = 2 };
+enum {
+  MOE_CALL_ROUTE = 0,
+  MOE_CALL_PERMUTE = 1,
+  MOE_CALL_EXPERT_FFN = 2,
+  MOE_CALL_ROUTER_BACKWARD_DENSE = 3
+};
 
 /* Workspace bytes a call needs for problem p (0 if none).  Returns 0 and sets the
  * last error for an invalid problem or call id. */
@@ -403,6 +408,113 @@ moe_status moe_unpermute_sum(const moe_problem* p, const void* dx_sorted,
  * code = RNE-saturating E4M3 of w/scale. */
 moe_status moe_quantize_weights_fp8(const void* w_bf16, void* w_fp8, float* scale,
                                     int64_t batch, int32_t rows, int32_t cols, void* stream);
+
+/* ---------------- sequence-wise balance loss ----------------
+ * The sequence-level balance term that goes with the bias rule (mpbf.cn section 2.2 names it
+ * and gives it no formula; this one is the usual product of load fraction and mean affinity
+ * share).  Sequence q holds tokens seq_offsets[q] .. seq_offsets[q+1]-1, L of them; with
+ * s = sigmoid(clamp(z, +-80)) and n[q,e] its choices of expert e in topk_idx,
+ *   f[q,e] = E/(K L) n[q,e],   P[q,e] = 1/L sum_t s[t,e] / sum_j s[t,j],
+ *   seq_loss[q] = sum_e f[q,e] P[q,e]      (1 when the loads or the shares are uniform).
+ * Weights (a small factor, the mean over sequences) are the caller's: they go into
+ * dseq_loss of the backward.
+ *   logits      [T,E] fp32 from moe_route;  topk_idx [T,K] int32 from moe_route
+ *   seq_offsets [n_seq+1] int32, 0 <= seq_offsets[0] <= ... <= seq_offsets[n_seq] <= T: empty
+ *               sequences are allowed, tokens before the first and behind the last one
+ *               (padding) belong to none
+ *   seq_counts  [n_seq,E] int32 out: n;  seq_prob [n_seq,E] fp32 out: P;
+ *   seq_loss    [n_seq] fp32 out (an empty sequence gets zeros in all three)
+ *   ws          >= moe_balance_loss_workspace_bytes(p, n_seq) bytes, 16-byte aligned
+ * fp32 sums in a fixed order (bit-for-bit reproducible).  Limits (checked): 1 <= n_seq <=
+ * 2^24, n_seq*E < 2^31.  Offsets that break the ordering, or indices outside [0,E) (not
+ * counted), give unspecified values but every write stays inside the outputs. */
+size_t moe_balance_loss_workspace_bytes(const moe_problem* p, int32_t n_seq);
+moe_status moe_balance_loss(const moe_problem* p, const float* logits, const int32_t* topk_idx,
+                            const int32_t* seq_offsets, int32_t n_seq, int32_t* seq_counts,
+                            float* seq_prob, float* seq_loss, void* ws, size_t ws_bytes,
+                            void* stream);
+
+/* Gradient of sum_q dseq_loss[q] seq_loss[q] in the logits.  The counts are piecewise constant
+ * and take none: with c[e] = dseq_loss[q] f[q,e]/L, S = sum_j s[t,j] for token t of sequence q,
+ *   dlogits[t,e] = (c[e] - sum_j c[j] s[t,j]/S)/S s(1-s),   0 where |z| > 80.
+ * dgate != NULL joins the gradient of the gates, dz of moe_router_backward, at the chosen
+ * experts (then topk_idx and topk_gate are read; a token in no sequence gets this part alone,
+ * or zeros).
+ *   seq_counts [n_seq,E] from moe_balance_loss; dseq_loss [n_seq] fp32;
+ *   dgate [T,K] fp32 from moe_combine_backward, or NULL;  dlogits [T,E] fp32 out. */
+moe_status moe_balance_loss_backward(const moe_problem* p, const float* logits,
+                                     const int32_t* seq_offsets, int32_t n_seq,
+                                     const int32_t* seq_counts, const float* dseq_loss,
+                                     const int32_t* topk_idx, const float* topk_gate,
+                                     const float* dgate, float* dlogits, void* stream);
+
+/* Router backward for a gradient of every logit, in place of moe_router_backward's chosen ones:
+ *   dx_router[t] = sum_e dlogits[t,e] W_r[e]   [T,H] fp32 out,
+ *   dw_router[e] = sum_t dlogits[t,e] x[t]     [E,H] fp32 out   (fp32, a fixed order).
+ *   dlogits [T,E] fp32, e.g. from moe_balance_loss_backward with dgate
+ *   ws      >= moe_workspace_bytes(p, MOE_CALL_ROUTER_BACKWARD_DENSE) bytes, 16-byte aligned */
+moe_status moe_router_backward_dense(const moe_problem* p, const void* x, const float* w_router,
+                                     const float* dlogits, float* dx_router, float* dw_router,
+                                     void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------- 8-bit activation checkpoints (bf16 and fp32 paths) ----------------
+ * The pre-activations au [R,2I] that the backward needs, kept as E4M3 codes with one fp32 scale
+ * per (row, 128 columns), amax/448 (1 for an all-zero block): 1.03 bytes an element in place of
+ * 2 or 4, and h [R,I] is not kept at all (the backward forms it again).  One au (and h) buffer
+ * can then serve every layer of a model.  A kept value is off by at most 2^-4 of itself, or
+ * 2^-10 scale where it is below 2^-6 scale.
+ *   au_q [R,2I] codes, au_scale [R,2I/128] fp32. */
+moe_status moe_checkpoint_save(const moe_problem* p, const void* au, void* au_q, float* au_scale,
+                               void* stream);
+
+/* The kept pre-activations again, code * scale rounded to act_dtype, for the calls that read
+ * au; and h = silu(a) u of them.  au [R,2I] act out or NULL; h [R,I] act out or NULL. */
+moe_status moe_checkpoint_restore(const moe_problem* p, const void* au_q, const float* au_scale,
+                                  void* au, void* h, void* stream);
+
+/* moe_expert_ffn_backward_input_packed straight from the kept codes (bf16 only): the results of
+ * moe_checkpoint_restore followed by that call, bit for bit, without au in memory; h [R,I] bf16
+ * out is the h that moe_expert_ffn_backward_weight reads.  Rows outside every group are not
+ * written.  The other arguments as moe_expert_ffn_backward_input_packed. */
+moe_status moe_expert_ffn_backward_input_checkpoint(const moe_problem* p, const int32_t* offsets,
+                                                    const void* w13t_packed,
+                                                    const void* w2t_packed, const void* au_q,
+                                                    const float* au_scale,
+                                                    const void* dy_sorted, void* dau, void* h,
+                                                    void* dx_sorted, void* stream);
+
+/* ---------------- block-scaled FP8 matrix product ----------------
+ * E4M3 quantisation of x [rows, cols] (dtype MOE_BF16 or MOE_F32, row stride ldx elements), one
+ * fp32 scale per 128 elements: scale = amax/448 (1 if that is 0), code = RNE-saturating E4M3 of
+ * x/scale.
+ *   q  [rows, ldq]  codes, scale   [rows, ceil(cols/128)]: blocks along a row; or both NULL
+ *   qt [cols, ldqt] codes, scale_t [cols, ceil(rows/128)]: the transpose, blocks along a column
+ *      of x; or both NULL (one of the two forms is required; both come from one read of x)
+ * Limits (checked): rows, cols >= 1; ldx >= cols; ldq >= cols and ldqt >= rows, multiples of 16;
+ * q, qt 16-byte aligned, x aligned to its element.  Bytes of a row past its codes are not
+ * written. */
+moe_status moe_quantize_fp8(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ldx,
+                            void* q, int64_t ldq, float* scale, void* qt, int64_t ldqt,
+                            float* scale_t, void* stream);
+
+/* C = A B^T over E4M3 codes with a scale for each block of 128 along k, fp32 accumulation: each
+ * block's partial sum of code products is scaled by the two block scales and added in fp32
+ * (mpbf.cn section 3.1), rounded once at the end.
+ *   a [M, lda] codes, a_scale [M, ceil(K/128)]
+ *   b [N, ldb] codes, b_scale [N, ceil(K/128)] (b_rows = 1) or [ceil(N/128), ceil(K/128)]
+ *     (b_rows = 128, as moe_quantize_weights_fp8 writes it)
+ *   c [M, ldc] out, c_dtype MOE_BF16 or MOE_F32; accumulate = 1 (MOE_F32 only): C += A B^T
+ *   ws >= moe_gemm_fp8_workspace_bytes(M, N, K) bytes, 16-byte aligned (may be NULL if that is 0)
+ * A linear layer y = x W^T: a = x by rows, b = W; its gradients: dx = dy W with a = dy by rows,
+ * b = W^T; dW = dy^T x with a = dy, b = x, both by columns (moe_quantize_fp8's transposes).
+ * Any M, N, K >= 1.  Code bytes past K in a row are ignored.  Limits (checked): lda, ldb
+ * multiples of 16, >= K and at most 2^22; ldc >= N; M, N < 2^31; a, b, c 16-byte aligned, c
+ * apart from a and b; at most 2^31 - 1 tiles of 64 x 64. */
+size_t moe_gemm_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K);
+moe_status moe_gemm_fp8(int64_t M, int64_t N, int64_t K, const void* a, int64_t lda,
+                        const float* a_scale, const void* b, int64_t ldb, const float* b_scale,
+                        int32_t b_rows, void* c, int64_t ldc, int32_t c_dtype, int32_t accumulate,
+                        void* ws, size_t ws_bytes, void* stream);
 
 /* Text of a status code, and the last error message of the calling thread. */
 const char* moe_status_str(moe_status s);

@@ -16,6 +16,7 @@ LIB_PATH = os.path.join(_PKG, "libmoe.so")
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = 0, -1, -2, -3, -4
 MOE_F32, MOE_BF16, MOE_FP8_E4M3 = 0, 1, 2
 MOE_CALL_ROUTE, MOE_CALL_PERMUTE, MOE_CALL_EXPERT_FFN = 0, 1, 2
+MOE_CALL_ROUTER_BACKWARD_DENSE = 3
 
 EXPORTS = ("moe_route", "moe_permute", "moe_expert_ffn", "moe_expert_ffn_up",
            "moe_expert_ffn_up_gather", "moe_quantize_act_fp8", "moe_expert_ffn_down",
@@ -26,7 +27,11 @@ EXPORTS = ("moe_route", "moe_permute", "moe_expert_ffn", "moe_expert_ffn_up",
            "moe_count_invalid_ids",
            "moe_seq_load_stats", "moe_pack_expert_weights", "moe_expert_ffn_up_packed",
            "moe_expert_ffn_down_packed", "moe_pack_expert_weights_transposed",
-           "moe_expert_ffn_backward_input_packed")
+           "moe_expert_ffn_backward_input_packed", "moe_balance_loss_workspace_bytes",
+           "moe_balance_loss", "moe_balance_loss_backward", "moe_router_backward_dense",
+           "moe_checkpoint_save", "moe_checkpoint_restore",
+           "moe_expert_ffn_backward_input_checkpoint", "moe_quantize_fp8",
+           "moe_gemm_fp8_workspace_bytes", "moe_gemm_fp8")
 
 
 class MoeError(RuntimeError):
@@ -84,6 +89,20 @@ def lib():
         L.moe_combine.argtypes = [pp, vp, vp, vp, vp, vp]
         L.moe_bias_update.argtypes = [pp, vp, f32, vp, vp]
         L.moe_quantize_weights_fp8.argtypes = [vp, vp, vp, i64, i32, i32, vp]
+        L.moe_balance_loss.argtypes = [pp, vp, vp, vp, i32, vp, vp, vp, vp, sz, vp]
+        L.moe_balance_loss_backward.argtypes = [pp, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp]
+        L.moe_router_backward_dense.argtypes = [pp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.moe_checkpoint_save.argtypes = [pp, vp, vp, vp, vp]
+        L.moe_checkpoint_restore.argtypes = [pp, vp, vp, vp, vp, vp]
+        L.moe_expert_ffn_backward_input_checkpoint.argtypes = [pp, vp, vp, vp, vp, vp, vp, vp, vp,
+                                                               vp, vp]
+        L.moe_quantize_fp8.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, vp, i64, vp, vp]
+        L.moe_gemm_fp8.argtypes = [i64, i64, i64, vp, i64, vp, vp, i64, vp, i32, vp, i64, i32, i32,
+                                   vp, sz, vp]
+        L.moe_balance_loss_workspace_bytes.argtypes = [pp, i32]
+        L.moe_balance_loss_workspace_bytes.restype = sz
+        L.moe_gemm_fp8_workspace_bytes.argtypes = [i64, i64, i64]
+        L.moe_gemm_fp8_workspace_bytes.restype = sz
         L.moe_workspace_bytes.argtypes = [pp, i32]
         L.moe_workspace_bytes.restype = sz
         L.moe_status_str.argtypes = [i32]
@@ -99,7 +118,11 @@ def lib():
                   "moe_seq_load_stats",
                   "moe_pack_expert_weights", "moe_expert_ffn_up_packed",
                   "moe_expert_ffn_down_packed", "moe_pack_expert_weights_transposed",
-                  "moe_expert_ffn_backward_input_packed"):
+                  "moe_expert_ffn_backward_input_packed", "moe_balance_loss",
+                  "moe_balance_loss_backward", "moe_router_backward_dense",
+                  "moe_checkpoint_save", "moe_checkpoint_restore",
+                  "moe_expert_ffn_backward_input_checkpoint", "moe_quantize_fp8",
+                  "moe_gemm_fp8"):
             getattr(L, n).restype = i32
         _lib = L
     return _lib
@@ -115,6 +138,29 @@ def _ptr(t):
     if isinstance(t, int):
         return t
     return t.data_ptr()
+
+
+def _ptrs(call, *tensors):
+    """Device pointers of tensors (None and addresses as they are).  A tensor in host memory or
+    on another device than the current one is refused: its address would fault the kernel, or
+    the stream would be another device's."""
+    import torch
+    here, out = None, []
+    for t in tensors:
+        if t is None or isinstance(t, int):
+            out.append(t)
+            continue
+        at = t.get_device()  # -1: host memory
+        if here is None and at >= 0:
+            here = torch.cuda.current_device()
+        if at < 0 or at != here:
+            raise MoeError(MOE_ERR_INVALID_ARG, call, "a tensor is in host memory" if at < 0 else
+                           f"a tensor is on device {at}, the current device is {here}")
+        if not t.is_contiguous():
+            raise MoeError(MOE_ERR_INVALID_ARG, call, "a tensor is not contiguous (pass the row "
+                           "stride of the whole buffer where the call takes one)")
+        out.append(t.data_ptr())
+    return out
 
 
 def _stream(stream):
@@ -304,3 +350,72 @@ def moe_unpermute_sum(p, dx_sorted, inv_perm, dx_router, dx, stream=None):
     _check(lib().moe_unpermute_sum(ctypes.byref(p), _ptr(dx_sorted), _ptr(inv_perm),
                                    _ptr(dx_router), _ptr(dx), _stream(stream)),
            "moe_unpermute_sum")
+
+
+def moe_balance_loss_workspace_bytes(p, n_seq) -> int:
+    n = lib().moe_balance_loss_workspace_bytes(ctypes.byref(p), n_seq)
+    if n == 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, "moe_balance_loss_workspace_bytes", last_error())
+    return n
+
+
+def moe_balance_loss(p, logits, topk_idx, seq_offsets, n_seq, seq_counts, seq_prob, seq_loss, ws,
+                     ws_bytes, stream=None):
+    z, i, o, c, q, l, w = _ptrs("moe_balance_loss", logits, topk_idx, seq_offsets, seq_counts,
+                                seq_prob, seq_loss, ws)
+    _check(lib().moe_balance_loss(ctypes.byref(p), z, i, o, n_seq, c, q, l, w, ws_bytes,
+                                  _stream(stream)), "moe_balance_loss")
+
+
+def moe_balance_loss_backward(p, logits, seq_offsets, n_seq, seq_counts, dseq_loss, topk_idx,
+                              topk_gate, dgate, dlogits, stream=None):
+    z, o, c, dl, i, g, dg, dz = _ptrs("moe_balance_loss_backward", logits, seq_offsets,
+                                      seq_counts, dseq_loss, topk_idx, topk_gate, dgate, dlogits)
+    _check(lib().moe_balance_loss_backward(ctypes.byref(p), z, o, n_seq, c, dl, i, g, dg, dz,
+                                           _stream(stream)), "moe_balance_loss_backward")
+
+
+def moe_router_backward_dense(p, x, w_router, dlogits, dx_router, dw_router, ws, ws_bytes,
+                              stream=None):
+    x, w, d, dx, dw, s = _ptrs("moe_router_backward_dense", x, w_router, dlogits, dx_router,
+                               dw_router, ws)
+    _check(lib().moe_router_backward_dense(ctypes.byref(p), x, w, d, dx, dw, s, ws_bytes,
+                                           _stream(stream)), "moe_router_backward_dense")
+
+
+def moe_checkpoint_save(p, au, au_q, au_scale, stream=None):
+    au, q, s = _ptrs("moe_checkpoint_save", au, au_q, au_scale)
+    _check(lib().moe_checkpoint_save(ctypes.byref(p), au, q, s, _stream(stream)),
+           "moe_checkpoint_save")
+
+
+def moe_checkpoint_restore(p, au_q, au_scale, au, h, stream=None):
+    q, s, au, h = _ptrs("moe_checkpoint_restore", au_q, au_scale, au, h)
+    _check(lib().moe_checkpoint_restore(ctypes.byref(p), q, s, au, h, _stream(stream)),
+           "moe_checkpoint_restore")
+
+
+def moe_expert_ffn_backward_input_checkpoint(p, offsets, w13t_packed, w2t_packed, au_q, au_scale,
+                                             dy_sorted, dau, h, dx_sorted, stream=None):
+    a = _ptrs("moe_expert_ffn_backward_input_checkpoint", offsets, w13t_packed, w2t_packed, au_q,
+              au_scale, dy_sorted, dau, h, dx_sorted)
+    _check(lib().moe_expert_ffn_backward_input_checkpoint(ctypes.byref(p), *a, _stream(stream)),
+           "moe_expert_ffn_backward_input_checkpoint")
+
+
+def moe_quantize_fp8(x, dtype, rows, cols, ldx, q, ldq, scale, qt=None, ldqt=0, scale_t=None,
+                     stream=None):
+    x, q, s, qt, st = _ptrs("moe_quantize_fp8", x, q, scale, qt, scale_t)
+    _check(lib().moe_quantize_fp8(x, dtype, rows, cols, ldx, q, ldq, s, qt, ldqt, st,
+                                  _stream(stream)), "moe_quantize_fp8")
+
+
+def moe_gemm_fp8_workspace_bytes(M, N, K) -> int:
+    return lib().moe_gemm_fp8_workspace_bytes(M, N, K)
+
+
+def moe_gemm_fp8(M, N, K, a, lda, a_scale, b, ldb, b_scale, b_rows, c, ldc, c_dtype=MOE_BF16,
+                 accumulate=0, ws=None, ws_bytes=0, stream=None):
+    a, sa, b, sb, c, w = _ptrs("moe_gemm_fp8", a, a_scale, b, b_scale, c, ws)
+    _check(lib().moe_gemm_fp8(M, N, K, a, lda, sa, b, ldb, sb, b_rows, c, ldc, c_dtype,
+                              accumulate, w, ws_bytes, _stream(stream)), "moe_gemm_fp8")

@@ -126,6 +126,7 @@ size_t moe_workspace_bytes(const moe_problem* p, int32_t which_call) {
     case MOE_CALL_ROUTE: return route_ws_bytes(d);
     case MOE_CALL_PERMUTE: return permute_ws_bytes(d);
     case MOE_CALL_EXPERT_FFN: return ffn_ws_bytes(d);
+    case MOE_CALL_ROUTER_BACKWARD_DENSE: return router_dense_ws_bytes(d);
   }
   fail(MOE_ERR_INVALID_ARG, "unknown call id %d", which_call);
   return 0;
@@ -659,6 +660,232 @@ moe_status moe_quantize_weights_fp8(const void* w_bf16, void* w_fp8, float* scal
                                          static_cast<uint8_t*>(w_fp8), scale, batch, rows, cols,
                                          static_cast<hipStream_t>(stream));
   return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_quantize_weights_fp8 launch");
+}
+
+static moe_status check_sequences(const Dims& d, int32_t n_seq) {
+  if (n_seq < 1 || n_seq > (1 << 24) || (int64_t)n_seq * d.E >= ((int64_t)1 << 31))
+    return fail(MOE_ERR_INVALID_ARG, "n_seq=%d must be in [1, 2^24] with n_seq*E < 2^31", n_seq);
+  return MOE_OK;
+}
+
+static moe_status check_ws(const char* call, const void* ws, size_t got, size_t need) {
+  if (need && (!ws || got < need || !aligned16(ws)))
+    return fail(MOE_ERR_WORKSPACE, "%s needs %zu workspace bytes, 16-byte aligned, got %zu", call,
+                need, ws ? got : (size_t)0);
+  return MOE_OK;
+}
+
+size_t moe_balance_loss_workspace_bytes(const moe_problem* p, int32_t n_seq) {
+  Dims d;
+  if (validate(p, &d) != MOE_OK || check_sequences(d, n_seq) != MOE_OK) return 0;
+  return balance_ws_bytes(d, n_seq);
+}
+
+moe_status moe_balance_loss(const moe_problem* p, const float* logits, const int32_t* topk_idx,
+                            const int32_t* seq_offsets, int32_t n_seq, int32_t* seq_counts,
+                            float* seq_prob, float* seq_loss, void* ws, size_t ws_bytes,
+                            void* stream) {
+  Dims d;
+  moe_status s = validate(p, &d);
+  if (s != MOE_OK) return s;
+  if ((s = check_sequences(d, n_seq)) != MOE_OK) return s;
+  REQUIRE_PTR(logits);
+  REQUIRE_PTR(topk_idx);
+  REQUIRE_PTR(seq_counts);
+  REQUIRE_PTR(seq_prob);
+  if (!seq_offsets || !seq_loss)
+    return fail(MOE_ERR_INVALID_ARG, "seq_offsets and seq_loss are required");
+  if ((s = check_ws("moe_balance_loss", ws, ws_bytes, balance_ws_bytes(d, n_seq))) != MOE_OK)
+    return s;
+  if ((s = check_device(nullptr)) != MOE_OK) return s;
+  const hipError_t e = launch_balance_loss(d, logits, topk_idx, seq_offsets, n_seq, seq_counts,
+                                           seq_prob, seq_loss, ws,
+                                           static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_balance_loss launch");
+}
+
+moe_status moe_balance_loss_backward(const moe_problem* p, const float* logits,
+                                     const int32_t* seq_offsets, int32_t n_seq,
+                                     const int32_t* seq_counts, const float* dseq_loss,
+                                     const int32_t* topk_idx, const float* topk_gate,
+                                     const float* dgate, float* dlogits, void* stream) {
+  Dims d;
+  moe_status s = validate(p, &d);
+  if (s != MOE_OK) return s;
+  if ((s = check_sequences(d, n_seq)) != MOE_OK) return s;
+  REQUIRE_PTR(logits);
+  REQUIRE_PTR(seq_counts);
+  REQUIRE_PTR(dlogits);
+  if (!seq_offsets || !dseq_loss)
+    return fail(MOE_ERR_INVALID_ARG, "seq_offsets and dseq_loss are required");
+  if (dgate && (!topk_idx || !topk_gate))
+    return fail(MOE_ERR_INVALID_ARG, "dgate needs topk_idx and topk_gate");
+  if (dlogits == logits)
+    return fail(MOE_ERR_INVALID_ARG, "dlogits cannot be written over logits");
+  if ((s = check_device(nullptr)) != MOE_OK) return s;
+  const hipError_t e = launch_balance_bwd(d, logits, seq_offsets, n_seq, seq_counts, dseq_loss,
+                                          topk_idx, topk_gate, dgate, dlogits,
+                                          static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_balance_loss_backward launch");
+}
+
+moe_status moe_router_backward_dense(const moe_problem* p, const void* x, const float* w_router,
+                                     const float* dlogits, float* dx_router, float* dw_router,
+                                     void* ws, size_t ws_bytes, void* stream) {
+  Dims d;
+  moe_status s = validate(p, &d);
+  if (s != MOE_OK) return s;
+  REQUIRE_PTR(x);
+  REQUIRE_PTR(w_router);
+  REQUIRE_PTR(dlogits);
+  REQUIRE_PTR(dx_router);
+  REQUIRE_PTR(dw_router);
+  if ((s = check_ws("moe_router_backward_dense", ws, ws_bytes, router_dense_ws_bytes(d))) != MOE_OK)
+    return s;
+  if ((s = check_device(nullptr)) != MOE_OK) return s;
+  const hipError_t e = launch_router_dense_bwd(d, x, w_router, dlogits, dx_router, dw_router, ws,
+                                               static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_router_backward_dense launch");
+}
+
+moe_status moe_checkpoint_save(const moe_problem* p, const void* au, void* au_q, float* au_scale,
+                               void* stream) {
+  Dims d;
+  moe_status s = validate(p, &d);
+  if (s != MOE_OK) return s;
+  if ((s = require_no_fp8(d, "moe_checkpoint_save")) != MOE_OK) return s;
+  REQUIRE_PTR(au);
+  REQUIRE_PTR(au_q);
+  if (!au_scale) return fail(MOE_ERR_INVALID_ARG, "au_scale is NULL");
+  if (au == au_q) return fail(MOE_ERR_INVALID_ARG, "the codes cannot be written over au");
+  if ((s = check_device(nullptr)) != MOE_OK) return s;
+  const hipError_t e =
+      launch_quantize_fp8(au, d.act, d.R(), 2 * (int64_t)d.I, 2 * (int64_t)d.I,
+                          static_cast<uint8_t*>(au_q), 2 * (int64_t)d.I, au_scale, nullptr, 0,
+                          nullptr, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_checkpoint_save launch");
+}
+
+moe_status moe_checkpoint_restore(const moe_problem* p, const void* au_q, const float* au_scale,
+                                  void* au, void* h, void* stream) {
+  Dims d;
+  moe_status s = validate(p, &d);
+  if (s != MOE_OK) return s;
+  if ((s = require_no_fp8(d, "moe_checkpoint_restore")) != MOE_OK) return s;
+  REQUIRE_PTR(au_q);
+  if (!au_scale) return fail(MOE_ERR_INVALID_ARG, "au_scale is NULL");
+  if (!au && !h) return fail(MOE_ERR_INVALID_ARG, "au and h are both NULL");
+  if (!aligned16(au) || !aligned16(h))
+    return fail(MOE_ERR_INVALID_ARG, "au or h is not 16-byte aligned");
+  if (au == au_q || h == au_q || (au && au == h))
+    return fail(MOE_ERR_INVALID_ARG, "au, h and au_q must be buffers of their own");
+  if ((s = check_device(nullptr)) != MOE_OK) return s;
+  const hipError_t e = launch_ckpt_restore(d, static_cast<const uint8_t*>(au_q), au_scale, au, h,
+                                           static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_checkpoint_restore launch");
+}
+
+moe_status moe_expert_ffn_backward_input_checkpoint(const moe_problem* p, const int32_t* offsets,
+                                                    const void* w13t_packed,
+                                                    const void* w2t_packed, const void* au_q,
+                                                    const float* au_scale,
+                                                    const void* dy_sorted, void* dau, void* h,
+                                                    void* dx_sorted, void* stream) {
+  Dims d;
+  moe_status s = validate(p, &d);
+  if (s != MOE_OK) return s;
+  if ((s = require_bf16_pair(d, "moe_expert_ffn_backward_input_checkpoint")) != MOE_OK) return s;
+  REQUIRE_PTR(w13t_packed);
+  REQUIRE_PTR(w2t_packed);
+  REQUIRE_PTR(au_q);
+  REQUIRE_PTR(dy_sorted);
+  REQUIRE_PTR(dau);
+  REQUIRE_PTR(h);
+  REQUIRE_PTR(dx_sorted);
+  if (!offsets || !au_scale)
+    return fail(MOE_ERR_INVALID_ARG, "offsets and au_scale are required");
+  if ((s = check_bwd_rows(d)) != MOE_OK) return s;
+  if ((s = check_device(nullptr)) != MOE_OK) return s;
+  const hipError_t e = launch_ffn_bwd_input_packed(
+      d, offsets, w13t_packed, w2t_packed, nullptr, dy_sorted, dau, dx_sorted,
+      static_cast<hipStream_t>(stream), static_cast<const uint8_t*>(au_q), au_scale, h);
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_expert_ffn_backward_input_checkpoint launch");
+}
+
+moe_status moe_quantize_fp8(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ldx,
+                            void* q, int64_t ldq, float* scale, void* qt, int64_t ldqt,
+                            float* scale_t, void* stream) {
+  if (dtype != MOE_BF16 && dtype != MOE_F32)
+    return fail(MOE_ERR_INVALID_ARG, "dtype=%d must be MOE_BF16 or MOE_F32", dtype);
+  constexpr int64_t kMost = (int64_t)1 << 40;
+  if (rows < 1 || cols < 1 || rows > kMost || cols > kMost)
+    return fail(MOE_ERR_INVALID_ARG, "rows and cols must be in [1, 2^40]");
+  if (((rows + 127) / 128) * (double)((cols + 127) / 128) >= 2147483648.0)
+    return fail(MOE_ERR_INVALID_ARG, "too many 128x128 blocks");
+  if (ldx < cols) return fail(MOE_ERR_INVALID_ARG, "ldx=%lld < cols", (long long)ldx);
+  if (!x || (reinterpret_cast<uintptr_t>(x) & (dtype == MOE_F32 ? 3 : 1)))
+    return fail(MOE_ERR_INVALID_ARG, "x is NULL or not aligned to its element");
+  if (!q && !qt) return fail(MOE_ERR_INVALID_ARG, "q and qt are both NULL");
+  if (q && (!aligned16(q) || !scale || ldq < cols || ldq % 16))
+    return fail(MOE_ERR_INVALID_ARG,
+                "q needs 16-byte alignment, scale and ldq >= cols, a multiple of 16");
+  if (qt && (!aligned16(qt) || !scale_t || ldqt < rows || ldqt % 16))
+    return fail(MOE_ERR_INVALID_ARG,
+                "qt needs 16-byte alignment, scale_t and ldqt >= rows, a multiple of 16");
+  if (x == q || x == qt || (q && q == qt))
+    return fail(MOE_ERR_INVALID_ARG, "x, q and qt must be buffers of their own");
+  moe_status s = check_device(nullptr);
+  if (s != MOE_OK) return s;
+  const hipError_t e = launch_quantize_fp8(x, dtype, rows, cols, ldx, static_cast<uint8_t*>(q),
+                                           ldq, scale, static_cast<uint8_t*>(qt), ldqt, scale_t,
+                                           static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_quantize_fp8 launch");
+}
+
+static moe_status check_gemm_fp8(int64_t M, int64_t N, int64_t K) {
+  constexpr int64_t kMost = ((int64_t)1 << 31) - 1;
+  if (M < 1 || N < 1 || K < 1 || M > kMost || N > kMost || K > ((int64_t)1 << 22))
+    return fail(MOE_ERR_INVALID_ARG, "M, N must be in [1, 2^31) and K in [1, 2^22]");
+  if (((M + 63) / 64) * ((N + 63) / 64) > kMost)
+    return fail(MOE_ERR_INVALID_ARG, "more than 2^31 - 1 tiles of 64 x 64");
+  return MOE_OK;
+}
+
+size_t moe_gemm_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (check_gemm_fp8(M, N, K) != MOE_OK) return 0;
+  return gemm_fp8_ws_bytes(M, N, K);
+}
+
+moe_status moe_gemm_fp8(int64_t M, int64_t N, int64_t K, const void* a, int64_t lda,
+                        const float* a_scale, const void* b, int64_t ldb, const float* b_scale,
+                        int32_t b_rows, void* c, int64_t ldc, int32_t c_dtype, int32_t accumulate,
+                        void* ws, size_t ws_bytes, void* stream) {
+  moe_status s = check_gemm_fp8(M, N, K);
+  if (s != MOE_OK) return s;
+  REQUIRE_PTR(a);
+  REQUIRE_PTR(b);
+  REQUIRE_PTR(c);
+  if (!a_scale || !b_scale)
+    return fail(MOE_ERR_INVALID_ARG, "a_scale and b_scale are required");
+  constexpr int64_t kMostLd = (int64_t)1 << 22;
+  if (lda < K || ldb < K || lda % 16 || ldb % 16 || lda > kMostLd || ldb > kMostLd)
+    return fail(MOE_ERR_INVALID_ARG,
+                "lda and ldb must be multiples of 16, at least K and at most 2^22");
+  if (ldc < N) return fail(MOE_ERR_INVALID_ARG, "ldc=%lld < N", (long long)ldc);
+  if (b_rows != 1 && b_rows != 128)
+    return fail(MOE_ERR_INVALID_ARG, "b_rows=%d must be 1 or 128", b_rows);
+  if (c_dtype != MOE_BF16 && c_dtype != MOE_F32)
+    return fail(MOE_ERR_INVALID_ARG, "c_dtype=%d must be MOE_BF16 or MOE_F32", c_dtype);
+  if (accumulate != 0 && (accumulate != 1 || c_dtype != MOE_F32))
+    return fail(MOE_ERR_INVALID_ARG, "accumulate must be 0, or 1 with c_dtype MOE_F32");
+  if (c == a || c == b) return fail(MOE_ERR_INVALID_ARG, "c cannot be written over a or b");
+  if ((s = check_ws("moe_gemm_fp8", ws, ws_bytes, gemm_fp8_ws_bytes(M, N, K))) != MOE_OK) return s;
+  if ((s = check_device(nullptr)) != MOE_OK) return s;
+  const hipError_t e = launch_gemm_fp8(
+      M, N, K, static_cast<const uint8_t*>(a), lda, a_scale, static_cast<const uint8_t*>(b), ldb,
+      b_scale, b_rows, c, ldc, c_dtype == MOE_F32, accumulate, ws,
+      static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_gemm_fp8 launch");
 }
 
 }  // extern "C"

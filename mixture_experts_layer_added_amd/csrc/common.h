@@ -251,7 +251,11 @@ hipError_t launch_pack_weights_t(const Dims& d, const void* w13, const void* w2,
                                  void* p2t, hipStream_t st);
 hipError_t launch_ffn_bwd_input_packed(const Dims& d, const int32_t* offsets, const void* p13t,
                                        const void* p2t, const void* au, const void* dys,
-                                       void* dau, void* dxs, hipStream_t st);
+                                       void* dau, void* dxs, hipStream_t st,
+                                       const uint8_t* ckq = nullptr, const float* cks = nullptr,
+                                       void* ckh = nullptr);
+// ... and from 8-bit checkpoints of au: codes ckq [R, 2I] and scales cks [R, 2I/128] in its
+// place, h [R, I] written to ckh
 // FP8 expert GEMMs over packed weight codes (gemm_packed_fp8.hip)
 hipError_t launch_pack_weights_fp8(const Dims& d, const void* w13, const void* w2, void* p13,
                                    void* p2, hipStream_t st);
@@ -296,6 +300,36 @@ hipError_t launch_ffn_bwd_input(const Dims& d, const int32_t* offsets, const voi
 hipError_t launch_ffn_bwd_weight(const Dims& d, const void* x, const int32_t* gather,
                                  const int32_t* offsets, const void* h, const void* dys,
                                  const void* dau, float* dw13, float* dw2, hipStream_t st);
+
+// sequence-wise balance loss (balance.hip)
+size_t balance_ws_bytes(const Dims& d, int n_seq);
+hipError_t launch_balance_loss(const Dims& d, const float* z, const int32_t* idx,
+                               const int32_t* off, int n_seq, int32_t* counts, float* prob,
+                               float* loss, void* ws, hipStream_t st);
+// dgate == nullptr: the balance loss's part alone
+hipError_t launch_balance_bwd(const Dims& d, const float* z, const int32_t* off, int n_seq,
+                              const int32_t* counts, const float* dloss, const int32_t* idx,
+                              const float* gate, const float* dgate, float* dz, hipStream_t st);
+
+// router backward for a dense logit gradient (router_dense.hip)
+size_t router_dense_ws_bytes(const Dims& d);
+hipError_t launch_router_dense_bwd(const Dims& d, const void* x, const float* w, const float* dz,
+                                   float* dx, float* dw, void* ws, hipStream_t st);
+
+// E4M3 quantisation along rows (q) and columns (qt, transposed), either may be nullptr, and
+// the restoring of 8-bit checkpoints (quant.hip)
+hipError_t launch_quantize_fp8(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ldx,
+                               uint8_t* q, int64_t ldq, float* scale, uint8_t* qt, int64_t ldqt,
+                               float* scale_t, hipStream_t st);
+hipError_t launch_ckpt_restore(const Dims& d, const uint8_t* q, const float* scale, void* au,
+                               void* h, hipStream_t st);
+
+// block-scaled FP8 matrix product (gemm_fp8_block.hip)
+size_t gemm_fp8_ws_bytes(int64_t M, int64_t N, int64_t K);
+hipError_t launch_gemm_fp8(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda,
+                           const float* sa, const uint8_t* b, int64_t ldb, const float* sb,
+                           int b_rows, void* c, int64_t ldc, int c_f32, int accumulate, void* ws,
+                           hipStream_t st);
 
 int device_cu_count();
 

@@ -46,8 +46,17 @@ constexpr int kPkStep = 4096;       // elements of one (block, k step)
 constexpr int kASlot = PBM * 128;   // bytes of one activation step at 192 rows
 constexpr int kPRing = 3 * kASlot;  // 72 KiB
 constexpr int kPStg = 32 * 128;     // down epilogue staging per wave: 32 rows x 128 bytes
+                                    // (mode 3: of 256 bytes)
 
 __device__ __forceinline__ float silu(float a) { return a / (1.0f + __expf(-a)); }
+
+// the values of 4 codes under one scale, rounded to bf16
+__device__ __forceinline__ void from_codes4(uint32_t w, float s, float* v) {
+  v[0] = bf16_bits_to_f32(f32_to_bf16_bits(__builtin_amdgcn_cvt_f32_fp8((int)w, 0) * s));
+  v[1] = bf16_bits_to_f32(f32_to_bf16_bits(__builtin_amdgcn_cvt_f32_fp8((int)w, 1) * s));
+  v[2] = bf16_bits_to_f32(f32_to_bf16_bits(__builtin_amdgcn_cvt_f32_fp8((int)w, 2) * s));
+  v[3] = bf16_bits_to_f32(f32_to_bf16_bits(__builtin_amdgcn_cvt_f32_fp8((int)w, 3) * s));
+}
 
 // ---------------------------------------------------------------------------
 // pack: one thread per 16-byte chunk of the packed output
@@ -108,14 +117,20 @@ __global__ void k_pack_bf16_t(const uint16_t* __restrict__ w, uint4* __restrict_
 // NULL).  Mode 1: down (C = Y [rows, Nout]).  Mode 2: the backward's dh, a down-form
 // product over packed W2^T, whose epilogue turns dh into da = dh u silu'(a) and
 // du = dh silu(a) with a = au[r][c], u = au[r][I + c] (I = Nout) and writes both into
-// C = [da|du] [rows, 2I].
+// C = [da|du] [rows, 2I].  Mode 3: mode 2 with the pre-activations as 8-bit checkpoints, E4M3
+// codes ckq [rows, 2I] with one scale per (row, 128 columns) in cks; the values are rounded to
+// bf16 as if they had been restored first, and h = silu(a) u, which is not kept, is written
+// to ckh [rows, I] for the weight gradients.
 template <int Mode, int MS, int D>
 __device__ __forceinline__ void pk_tile(const uint16_t* __restrict__ A,
                                         const int32_t* __restrict__ gather, int a_rows,
                                         const uint16_t* __restrict__ Bw, bool w_on,
                                         uint16_t* __restrict__ C, uint16_t* __restrict__ au,
                                         int Kd, int Nout, int col0, int64_t grow0, int m_rows,
-                                        char* smem, uint32_t lds0, char* stg) {
+                                        char* smem, uint32_t lds0, char* stg,
+                                        const uint8_t* ckq,
+                                        const float* cks,
+                                        uint16_t* __restrict__ ckh) {
   constexpr bool kSwiglu = Mode == 0;
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -315,6 +330,57 @@ __device__ __forceinline__ void pk_tile(const uint16_t* __restrict__ A,
         }
       }
     }
+  } else if constexpr (Mode == 3) {
+    // dh of a subtile goes through the wave's LDS in fp32 (rows of 256 bytes), and a lane takes
+    // 8 columns of 4 rows: its kept codes come as 8 adjacent bytes, da, du and h leave as
+    // whole lines.  (Working on the accumulators in place, as mode 2 does, spilled them in
+    // the six-subtile form.)
+    const int I = Nout, j = lane & 7;
+#pragma unroll
+    for (int m = 0; m < MS; ++m) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<float4*>(stg + stg256_off(lane & 31, 8 * n + 2 * q + (lane >> 5))) =
+              make_float4(acc[m][n][4 * q], acc[m][n][4 * q + 1], acc[m][n][4 * q + 2],
+                          acc[m][n][4 * q + 3]);
+      const int nrows = min(32, m_rows - 32 * m);
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const int fr = 8 * p + (lane >> 3);
+        if (fr >= nrows) continue;
+        const int64_t row = grow0 + 32 * m + fr;
+        const int col = col0 + 8 * j;
+        const uint2 aq = *reinterpret_cast<const uint2*>(ckq + row * 2 * I + col);
+        const uint2 uq = *reinterpret_cast<const uint2*>(ckq + row * 2 * I + I + col);
+        const float* sp = cks + row * (2 * I / 128) + col0 / 128;
+        const float sca = sp[0], scu = sp[I / 128];
+        const float4 d0 = *reinterpret_cast<const float4*>(stg + stg256_off(fr, 2 * j));
+        const float4 d1 = *reinterpret_cast<const float4*>(stg + stg256_off(fr, 2 * j + 1));
+        const float dh[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
+        float a[8], u[8], da[8], du[8], h[8];
+        from_codes4(aq.x, sca, a);
+        from_codes4(aq.y, sca, a + 4);
+        from_codes4(uq.x, scu, u);
+        from_codes4(uq.y, scu, u + 4);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          const float sg = 1.0f / (1.0f + __expf(-a[t]));
+          da[t] = dh[t] * u[t] * (sg * (1.0f + a[t] * (1.0f - sg)));
+          du[t] = dh[t] * (a[t] * sg);
+          h[t] = silu(a[t]) * u[t];
+        }
+        auto put8 = [](const float* v, uint16_t* o) {
+          const uint2 x = pack4_bf16(v[0], v[1], v[2], v[3]), y = pack4_bf16(v[4], v[5], v[6], v[7]);
+          const u32x4 w = {x.x, x.y, y.x, y.y};
+          __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(o));
+        };
+        put8(da, C + row * 2 * I + col);
+        put8(du, C + row * 2 * I + I + col);
+        put8(h, ckh + row * I + col);
+      }
+    }
   } else {
     // lane: row 32m + l%32, columns col0 + 32n + 8q + 4(l/32) .. +3 (4 per group q of
     // four elements).  Each 32-row subtile is staged in the wave's own 4 KiB of LDS
@@ -348,6 +414,7 @@ __device__ __forceinline__ void pk_tile(const uint16_t* __restrict__ A,
 // gather != nullptr: row r of the permuted order is row gather[r] of A (a_rows rows).
 // Mode 0: Nout = I (h columns), Bp = packed W13.  Mode 1: Nout = H, Bp = packed W2.
 // Mode 2: Nout = I, Bp = packed W2^T, A = dY, au the saved pre-activations (read).
+// Mode 3: as mode 2 with ckq, cks in place of au, and h written to ckh.
 template <int Mode>
 __global__ __launch_bounds__(256, 1) void k_gemm_packed(const uint16_t* __restrict__ A,
                                                         const uint16_t* __restrict__ Bp,
@@ -355,9 +422,12 @@ __global__ __launch_bounds__(256, 1) void k_gemm_packed(const uint16_t* __restri
                                                         const int32_t* __restrict__ offsets,
                                                         const int32_t* __restrict__ gather,
                                                         uint16_t* __restrict__ au, int a_rows,
-                                                        int NG, int Kd, int Nout) {
+                                                        int NG, int Kd, int Nout,
+                                                        const uint8_t* ckq,
+                                                        const float* cks,
+                                                        uint16_t* __restrict__ ckh) {
   constexpr bool kSwiglu = Mode == 0;
-  __shared__ __attribute__((aligned(1024))) char smem[kPRing + 4 * kPStg];
+  __shared__ __attribute__((aligned(1024))) char smem[kPRing + 4 * (Mode == 3 ? 2 : 1) * kPStg];
   __shared__ int mt_start[kMaxGroups + 1];
   // the cost prefix is only needed for the XCD split below, before the first tile's
   // loads overwrite the ring (they follow a barrier), so it borrows the ring's memory
@@ -374,7 +444,7 @@ __global__ __launch_bounds__(256, 1) void k_gemm_packed(const uint16_t* __restri
   // accumulators of up to 4 sub-tiles in the SwiGLU and dh epilogues, of all 6 in down
   const bool deep = (nk & 3) == 0;
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(smem));
-  char* stg = smem + kPRing + wv * kPStg;
+  char* stg = smem + kPRing + wv * (Mode == 3 ? 2 : 1) * kPStg;
 
   const int P = gridDim.x, per_xcd = P / kXcds;
   const int xcd = blockIdx.x % kXcds, slot = blockIdx.x / kXcds;
@@ -402,10 +472,10 @@ __global__ __launch_bounds__(256, 1) void k_gemm_packed(const uint16_t* __restri
   case MSV:                                                                               \
     if (deep && (MSV <= 4 || Mode == 1))                                                 \
       pk_tile<Mode, MSV, 3>(A, gather, a_rows, Bw, w_on, C, au, Kd, Nout, col0, grow0,    \
-                               m_rows, smem, lds0, stg);                                  \
+                               m_rows, smem, lds0, stg, ckq, cks, ckh);                                  \
     else                                                                                  \
       pk_tile<Mode, MSV, 1>(A, gather, a_rows, Bw, w_on, C, au, Kd, Nout, col0, grow0,    \
-                               m_rows, smem, lds0, stg);                                  \
+                               m_rows, smem, lds0, stg, ckq, cks, ckh);                                  \
     break;
     switch (ms) {
       PK_CASE(1)
@@ -474,7 +544,7 @@ hipError_t launch_ffn_up_packed(const Dims& d, const void* xs, const int32_t* of
   hipLaunchKernelGGL(k_gemm_packed<0>, dim3(pk_grid()), dim3(256), 0, st,
                      static_cast<const uint16_t*>(xs), static_cast<const uint16_t*>(p13),
                      static_cast<uint16_t*>(h), offsets, gather, static_cast<uint16_t*>(au),
-                     (int)d.T, ng, d.H, d.I);
+                     (int)d.T, ng, d.H, d.I, nullptr, nullptr, nullptr);
   return hipGetLastError();
 }
 
@@ -483,7 +553,7 @@ hipError_t launch_ffn_down_packed(const Dims& d, const void* h, const int32_t* o
   hipLaunchKernelGGL(k_gemm_packed<1>, dim3(pk_grid()), dim3(256), 0, st,
                      static_cast<const uint16_t*>(h), static_cast<const uint16_t*>(p2),
                      static_cast<uint16_t*>(ys), offsets, nullptr, nullptr, 0, d.E + d.S, d.I,
-                     d.H);
+                     d.H, nullptr, nullptr, nullptr);
   return hipGetLastError();
 }
 
@@ -511,20 +581,22 @@ hipError_t launch_pack_weights_t(const Dims& d, const void* w13, const void* w2,
 
 hipError_t launch_ffn_bwd_input_packed(const Dims& d, const int32_t* offsets, const void* p13t,
                                        const void* p2t, const void* au, const void* dys,
-                                       void* dau, void* dxs, hipStream_t st) {
+                                       void* dau, void* dxs, hipStream_t st, const uint8_t* ckq,
+                                       const float* cks, void* ckh) {
   const int NG = d.E + d.S;
   // dh = dY W2 (k over H) -> [da|du]
-  hipLaunchKernelGGL(k_gemm_packed<2>, dim3(pk_grid()), dim3(256), 0, st,
-                     static_cast<const uint16_t*>(dys), static_cast<const uint16_t*>(p2t),
-                     static_cast<uint16_t*>(dau), offsets, nullptr,
-                     const_cast<uint16_t*>(static_cast<const uint16_t*>(au)), 0, NG, d.H, d.I);
+  auto dh = ckq ? k_gemm_packed<3> : k_gemm_packed<2>;
+  hipLaunchKernelGGL(dh, dim3(pk_grid()), dim3(256), 0, st, static_cast<const uint16_t*>(dys),
+                     static_cast<const uint16_t*>(p2t), static_cast<uint16_t*>(dau), offsets,
+                     nullptr, const_cast<uint16_t*>(static_cast<const uint16_t*>(au)), 0, NG, d.H,
+                     d.I, ckq, cks, static_cast<uint16_t*>(ckh));
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   // dx_sorted = [da|du] W13 (k over 2I)
   hipLaunchKernelGGL(k_gemm_packed<1>, dim3(pk_grid()), dim3(256), 0, st,
                      static_cast<const uint16_t*>(dau), static_cast<const uint16_t*>(p13t),
                      static_cast<uint16_t*>(dxs), offsets, nullptr, nullptr, 0, NG, 2 * d.I,
-                     d.H);
+                     d.H, nullptr, nullptr, nullptr);
   return hipGetLastError();
 }
 

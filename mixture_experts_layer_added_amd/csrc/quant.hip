@@ -1,0 +1,263 @@
+// E4M3 quantisation of matrices of any size with one fp32 scale per 128 elements, along the
+// rows, along the columns (written transposed), or both from one read of the matrix; and the
+// 8-bit activation checkpoints of the expert backward, which are the row form.
+//   scale = amax/448 over the block (1 where that is 0), code = RNE-saturating E4M3 of
+//   x/scale (IEEE division)
+// A code's relative rounding error is at most 2^-4 for values above 2^-6 scale; smaller ones
+// round to multiples of 2^-9 scale.
+// All kernels here are bound by memory: each element is read once and each code written once.
+//   k_quant_rows: 16 lanes take one block of 128 columns, 8 elements a lane.
+//   k_quant_tile: a workgroup takes 128 x 128 elements through LDS, so that the transposed
+//     codes leave as whole 128-byte lines as well.
+//   k_ckpt_restore: 8 columns of h a lane from the gate and the up codes.
+#include "common.h"
+
+namespace moe {
+namespace {
+
+constexpr int kQB = 128;  // elements under one scale
+
+__device__ __forceinline__ float block_scale(float amax) {
+  const float s = amax / 448.0f;
+  return s > 0.0f ? s : 1.0f;  // 0 as well where amax is so small that the quotient is 0
+}
+
+// 8 elements from p, zeros from the n-th on
+template <bool kVec>
+__device__ __forceinline__ void read8(const uint16_t* __restrict__ p, int n, float* v) {
+  if (kVec && n >= 8) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? bf16_bits_to_f32(p[i]) : 0.0f;
+  }
+}
+template <bool kVec>
+__device__ __forceinline__ void read8(const float* __restrict__ p, int n, float* v) {
+  if (kVec && n >= 8) {
+    const float4 a = *reinterpret_cast<const float4*>(p);
+    const float4 b = *reinterpret_cast<const float4*>(p + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : 0.0f;
+  }
+}
+
+__device__ __forceinline__ float amax8(const float* v) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = __builtin_fmaxf(m, __builtin_fabsf(v[i]));
+  return m;
+}
+
+// the codes of v/s to q, whose first n bytes are the row's
+__device__ __forceinline__ void write8(uint8_t* __restrict__ q, int n, const float* v, float s) {
+  const uint32_t a = pack4_e4m3(v[0] / s, v[1] / s, v[2] / s, v[3] / s);
+  const uint32_t b = pack4_e4m3(v[4] / s, v[5] / s, v[6] / s, v[7] / s);
+  if (n >= 8) {
+    *reinterpret_cast<uint2*>(q) = make_uint2(a, b);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) q[i] = (uint8_t)((i < 4 ? a : b) >> (8 * (i & 3)));
+  }
+}
+
+template <typename T, bool kVec>
+__global__ __launch_bounds__(256) void k_quant_rows(const T* __restrict__ x, int64_t rows,
+                                                    int64_t cols, int64_t ldx,
+                                                    uint8_t* __restrict__ q, int64_t ldq,
+                                                    float* __restrict__ scale, int64_t kb) {
+  const int l = threadIdx.x & 15;
+  const int64_t stride = (int64_t)gridDim.x * 16;
+  for (int64_t g = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4); g < rows * kb; g += stride) {
+    const int64_t r = g / kb, b = g - r * kb;
+    const int64_t c = b * kQB + 8 * l;
+    const int n = (int)max((int64_t)0, min((int64_t)8, cols - c));
+    float v[8];
+    read8<kVec>(x + r * ldx + c, n, v);
+    float m = amax8(v);
+#pragma unroll
+    for (int o = 8; o >= 1; o >>= 1) m = __builtin_fmaxf(m, __shfl_xor(m, o));
+    const float s = block_scale(m);
+    write8(q + r * ldq + c, n, v, s);
+    if (l == 0) scale[r * kb + b] = s;
+  }
+}
+
+// 128 x 128 elements a workgroup.  Rows: 16 lanes a row, 8 elements a lane.  Columns: 8 lanes
+// a column, 16 rows a lane, read from LDS.
+constexpr int kTileLd = kQB + 1;
+template <typename T, bool kVec>
+__global__ __launch_bounds__(256) void k_quant_tile(const T* __restrict__ x, int64_t rows,
+                                                    int64_t cols, int64_t ldx,
+                                                    uint8_t* __restrict__ q, int64_t ldq,
+                                                    float* __restrict__ scale, int64_t kb,
+                                                    uint8_t* __restrict__ qt, int64_t ldqt,
+                                                    float* __restrict__ scale_t, int64_t kbt) {
+  __shared__ float tile[kQB * kTileLd];
+  const int tid = threadIdx.x, l = tid & 15;
+  const int64_t rb = blockIdx.x / kb, cb = blockIdx.x - rb * kb;
+  const int64_t r0 = rb * kQB, c0 = cb * kQB;
+  const int n = (int)max((int64_t)0, min((int64_t)8, cols - c0 - 8 * l));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int rr = 16 * i + (tid >> 4);
+    const int64_t r = r0 + rr;
+    float v[8];
+    read8<kVec>(x + r * ldx + c0 + 8 * l, r < rows ? n : 0, v);
+    if (q) {
+      float m = amax8(v);
+#pragma unroll
+      for (int o = 8; o >= 1; o >>= 1) m = __builtin_fmaxf(m, __shfl_xor(m, o));
+      const float s = block_scale(m);
+      if (r < rows) {
+        write8(q + r * ldq + c0 + 8 * l, n, v, s);
+        if (l == 0) scale[r * kb + cb] = s;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) tile[rr * kTileLd + 8 * l + k] = v[k];
+  }
+  __syncthreads();
+  const int g = tid & 7;
+  const int nr = (int)max((int64_t)0, min((int64_t)16, rows - r0 - 16 * g));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int cc = 32 * i + (tid >> 3);
+    float v[16], m = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      v[k] = tile[(16 * g + k) * kTileLd + cc];
+      m = __builtin_fmaxf(m, __builtin_fabsf(v[k]));
+    }
+#pragma unroll
+    for (int o = 4; o >= 1; o >>= 1) m = __builtin_fmaxf(m, __shfl_xor(m, o));
+    const float s = block_scale(m);
+    const int64_t c = c0 + cc;
+    if (c >= cols) continue;
+    uint8_t* p = qt + c * ldqt + r0 + 16 * g;
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      w[k] = pack4_e4m3(v[4 * k] / s, v[4 * k + 1] / s, v[4 * k + 2] / s, v[4 * k + 3] / s);
+    if (nr == 16) {
+      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        if (k < nr) p[k] = (uint8_t)(w[k >> 2] >> (8 * (k & 3)));
+    }
+    if (g == 0) scale_t[c * kbt + rb] = s;
+  }
+}
+
+// value of each of 4 codes times its scale, rounded to T (the width that the backward reads)
+__device__ __forceinline__ void from_codes(uint32_t w, float s, float* v, const uint16_t*) {
+  v[0] = __builtin_amdgcn_cvt_f32_fp8((int)w, 0) * s;
+  v[1] = __builtin_amdgcn_cvt_f32_fp8((int)w, 1) * s;
+  v[2] = __builtin_amdgcn_cvt_f32_fp8((int)w, 2) * s;
+  v[3] = __builtin_amdgcn_cvt_f32_fp8((int)w, 3) * s;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = bf16_bits_to_f32(f32_to_bf16_bits(v[i]));
+}
+__device__ __forceinline__ void from_codes(uint32_t w, float s, float* v, const float*) {
+  v[0] = __builtin_amdgcn_cvt_f32_fp8((int)w, 0) * s;
+  v[1] = __builtin_amdgcn_cvt_f32_fp8((int)w, 1) * s;
+  v[2] = __builtin_amdgcn_cvt_f32_fp8((int)w, 2) * s;
+  v[3] = __builtin_amdgcn_cvt_f32_fp8((int)w, 3) * s;
+}
+__device__ __forceinline__ void put8(uint16_t* __restrict__ p, const float* v) {
+  const uint2 a = pack4_bf16(v[0], v[1], v[2], v[3]), b = pack4_bf16(v[4], v[5], v[6], v[7]);
+  *reinterpret_cast<uint4*>(p) = make_uint4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ void put8(float* __restrict__ p, const float* v) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void k_ckpt_restore(const uint8_t* __restrict__ q,
+                                                      const float* __restrict__ scale, int64_t R,
+                                                      int I, T* __restrict__ au,
+                                                      T* __restrict__ h) {
+  const int per = I / 8, kb = 2 * I / kQB;
+  const int64_t n = R * per, stride = (int64_t)gridDim.x * 256;
+  for (int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x; g < n; g += stride) {
+    const int64_t r = g / per;
+    const int c = (int)(g - r * per) * 8;
+    const uint8_t* p = q + r * 2 * I + c;
+    const uint2 aq = *reinterpret_cast<const uint2*>(p);
+    const uint2 uq = *reinterpret_cast<const uint2*>(p + I);
+    const float as = scale[r * kb + c / kQB], us = scale[r * kb + (I + c) / kQB];
+    float a[8], u[8];
+    from_codes(aq.x, as, a, au);
+    from_codes(aq.y, as, a + 4, au);
+    from_codes(uq.x, us, u, au);
+    from_codes(uq.y, us, u + 4, au);
+    if (au) {
+      put8(au + r * 2 * I + c, a);
+      put8(au + r * 2 * I + I + c, u);
+    }
+    if (h) {
+      float hv[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) hv[i] = a[i] / (1.0f + __expf(-a[i])) * u[i];
+      put8(h + r * I + c, hv);
+    }
+  }
+}
+
+template <typename T>
+hipError_t quantize(const T* x, int64_t rows, int64_t cols, int64_t ldx, uint8_t* q, int64_t ldq,
+                    float* scale, uint8_t* qt, int64_t ldqt, float* scale_t, hipStream_t st) {
+  const int64_t kb = (cols + kQB - 1) / kQB, kbt = (rows + kQB - 1) / kQB;
+  // 16-byte loads need every row to start at a multiple of 16 bytes
+  const bool vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && ldx * sizeof(T) % 16 == 0;
+  if (qt) {
+    auto k = vec ? k_quant_tile<T, true> : k_quant_tile<T, false>;
+    hipLaunchKernelGGL(k, dim3((unsigned)(kb * kbt)), dim3(256), 0, st, x, rows, cols, ldx, q,
+                       ldq, scale, kb, qt, ldqt, scale_t, kbt);
+  } else {
+    auto k = vec ? k_quant_rows<T, true> : k_quant_rows<T, false>;
+    const int64_t blocks = (rows * kb + 15) / 16;
+    hipLaunchKernelGGL(k, dim3((unsigned)(blocks < (1 << 20) ? blocks : (1 << 20))), dim3(256), 0,
+                       st, x, rows, cols, ldx, q, ldq, scale, kb);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_quantize_fp8(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ldx,
+                               uint8_t* q, int64_t ldq, float* scale, uint8_t* qt, int64_t ldqt,
+                               float* scale_t, hipStream_t st) {
+  if (dtype == MOE_BF16)
+    return quantize(static_cast<const uint16_t*>(x), rows, cols, ldx, q, ldq, scale, qt, ldqt,
+                    scale_t, st);
+  return quantize(static_cast<const float*>(x), rows, cols, ldx, q, ldq, scale, qt, ldqt, scale_t,
+                  st);
+}
+
+hipError_t launch_ckpt_restore(const Dims& d, const uint8_t* q, const float* scale, void* au,
+                               void* h, hipStream_t st) {
+  const int64_t blocks = (d.R() * (d.I / 8) + 255) / 256;
+  const dim3 g((unsigned)(blocks < (1 << 20) ? blocks : (1 << 20)));
+  if (d.act == MOE_BF16)
+    hipLaunchKernelGGL(k_ckpt_restore<uint16_t>, g, dim3(256), 0, st, q, scale, d.R(), d.I,
+                       static_cast<uint16_t*>(au), static_cast<uint16_t*>(h));
+  else
+    hipLaunchKernelGGL(k_ckpt_restore<float>, g, dim3(256), 0, st, q, scale, d.R(), d.I,
+                       static_cast<float*>(au), static_cast<float*>(h));
+  return hipGetLastError();
+}
+
+}  // namespace moe

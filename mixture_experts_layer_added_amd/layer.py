@@ -47,6 +47,78 @@ def quantize_weights_fp8(w: torch.Tensor, stream=None):
     return q, s
 
 
+def quantize_fp8(x: torch.Tensor, rows=True, cols=False):
+    """fp32 or bf16 [n, m] (rows may be strided) -> E4M3 codes (uint8, row length padded to 16)
+    and fp32 scales per 128: (q [n, .], scale [n, ceil(m/128)]) along the rows, (qt [m, .],
+    scale_t [m, ceil(n/128)]) of the transpose; None for a form not asked for.  On the current
+    stream."""
+    assert x.dim() == 2 and x.stride(1) == 1 and x.stride(0) >= x.shape[1]
+    assert x.dtype in (torch.bfloat16, torch.float32)
+    n, m = x.shape
+
+    def out(r, c):
+        return (torch.empty((r, -(-c // 16) * 16), dtype=torch.uint8, device=x.device),
+                torch.empty((r, -(-c // 128)), dtype=torch.float32, device=x.device))
+    q, scale = out(n, m) if rows else (None, None)
+    qt, scale_t = out(m, n) if cols else (None, None)
+    L._ptrs("moe_quantize_fp8", x.as_strided((1,), (1,)))  # its device; its rows may be strided
+    L.moe_quantize_fp8(x.data_ptr(), L.MOE_F32 if x.dtype == torch.float32 else L.MOE_BF16, n, m,
+                       x.stride(0), q, q.shape[1] if rows else 0, scale, qt,
+                       qt.shape[1] if cols else 0, scale_t)
+    return q, scale, qt, scale_t
+
+
+class Fp8Linear:
+    """y = x W^T in block-scaled FP8 with its gradients: W [N, K] bf16 (N, K multiples of 128)
+    is kept as E4M3 codes with a scale per 128 x 128 block, in both orders; x and dy are
+    quantised per 128 along the dimension that each product sums over.
+
+    forward(x [M, K] bf16) -> y [M, N] bf16; backward(dy [M, N] bf16) -> dx [M, K] bf16 and adds
+    dy^T x to self.dw [N, K] fp32 (zero_grad clears it).  Both run on the current stream.
+    """
+
+    def __init__(self, w: torch.Tensor, train=False):
+        self.N, self.K = w.shape
+        self.train = train
+        q, scale = quantize_weights_fp8(w[None])
+        self.w_q, self.w_scale = q[0], scale[0]
+        self.dw = None
+        if train:
+            self.wt_q, self.wt_scale = self.w_q.t().contiguous(), self.w_scale.t().contiguous()
+            self.dw = torch.zeros((self.N, self.K), dtype=torch.float32, device=w.device)
+        self._x = None
+
+    @staticmethod
+    def _gemm(a, a_scale, b, b_scale, b_rows, M, N, K, out, accumulate=0):
+        n = L.moe_gemm_fp8_workspace_bytes(M, N, K)
+        ws = torch.empty((n,), dtype=torch.uint8, device=a.device) if n else None
+        L.moe_gemm_fp8(M, N, K, a, a.shape[1], a_scale, b, b.shape[1], b_scale, b_rows, out,
+                       out.shape[1], L.MOE_F32 if out.dtype == torch.float32 else L.MOE_BF16,
+                       accumulate, ws, n)
+        return out
+
+    def forward(self, x):
+        M = x.shape[0]
+        assert x.dtype == torch.bfloat16 and x.shape == (M, self.K)
+        q, scale, qt, scale_t = quantize_fp8(x, True, self.train)
+        self._x = (M, qt, scale_t)
+        y = torch.empty((M, self.N), dtype=torch.bfloat16, device=x.device)
+        return self._gemm(q, scale, self.w_q, self.w_scale, 128, M, self.N, self.K, y)
+
+    def backward(self, dy):
+        assert self.train, "construct the layer with train=True"
+        M, xt, xt_scale = self._x
+        assert dy.dtype == torch.bfloat16 and dy.shape == (M, self.N)
+        q, scale, qt, scale_t = quantize_fp8(dy, True, True)
+        dx = torch.empty((M, self.K), dtype=torch.bfloat16, device=dy.device)
+        self._gemm(q, scale, self.wt_q, self.wt_scale, 128, M, self.K, self.N, dx)
+        self._gemm(qt, scale_t, xt, xt_scale, 1, self.N, self.K, M, self.dw, 1)
+        return dx
+
+    def zero_grad(self):
+        self.dw.zero_()
+
+
 # batches up to this mean load per routed expert use the packed-weight GEMMs by default
 PACKED_MAX_MEAN_ROWS = 160
 
@@ -71,10 +143,19 @@ class MoELayer:
     mean load per routed expert, T*K/E, is at most PACKED_MAX_MEAN_ROWS -- the packed
     kernels take at most 192 rows of an expert per tile (a larger expert streams its
     weights once per tile), the natural-layout kernels 256.
+    checkpoint8 (with train): the pre-activations are kept between forward and backward as
+    8-bit checkpoints (au_q, au_scale) and h is not kept; share: another such layer of the same
+    shape whose au, h, dau, dy_sorted and dx_sorted buffers this one uses too (they hold nothing
+    between calls; layers that share them must not run at the same time).
     """
 
     def __init__(self, shape: Shape, w_router, bias, w13, w2, w13_scale=None, w2_scale=None,
-                 device="cuda", gather=False, train=False, packed=None):
+                 device="cuda", gather=False, train=False, packed=None, checkpoint8=False,
+                 share=None):
+        assert not checkpoint8 or train, "checkpoint8 is for training"
+        assert share is None or (checkpoint8 and share.checkpoint8 and share.shape == shape)
+        self.checkpoint8 = checkpoint8
+        self._balance = None
         self.shape = shape
         self.gather = gather
         self.train = train
@@ -120,21 +201,26 @@ class MoELayer:
             self.h = torch.empty((R, shape.I), dtype=torch.uint8, device=dev)
             self.h_scale = torch.empty((R, shape.I // 128), dtype=torch.float32, device=dev)
         else:
-            self.h = torch.empty((R, shape.I), dtype=act, device=dev)
+            self.h = share.h if share else torch.empty((R, shape.I), dtype=act, device=dev)
             self.h_scale = None
         self.y_sorted = torch.empty((R, H), dtype=act, device=dev)
         self.y = torch.empty((T, H), dtype=act, device=dev)
         if train:
             assert shape.expert != "e4m3", "the backward is built for the bf16 and fp32 paths"
             NG, I, f32 = E + shape.S, shape.I, torch.float32
-            self.au = torch.empty((R, 2 * I), dtype=act, device=dev)
-            self.dy_sorted = torch.empty((R, H), dtype=act, device=dev)
+            self.au = share.au if share else torch.empty((R, 2 * I), dtype=act, device=dev)
+            if checkpoint8:
+                self.au_q = torch.empty((R, 2 * I), dtype=torch.uint8, device=dev)
+                self.au_scale = torch.empty((R, 2 * I // 128), dtype=f32, device=dev)
+            self.dy_sorted = share.dy_sorted if share else torch.empty((R, H), dtype=act,
+                                                                       device=dev)
             self.dgate = torch.empty((T, K), dtype=f32, device=dev)
             self.dz = torch.empty((T, K), dtype=f32, device=dev)
             self.dx_router = torch.empty((T, H), dtype=f32, device=dev)
             self.dw_router = torch.empty((E, H), dtype=f32, device=dev)
-            self.dau = torch.empty((R, 2 * I), dtype=act, device=dev)
-            self.dx_sorted = torch.empty((R, H), dtype=act, device=dev)
+            self.dau = share.dau if share else torch.empty((R, 2 * I), dtype=act, device=dev)
+            self.dx_sorted = share.dx_sorted if share else torch.empty((R, H), dtype=act,
+                                                                       device=dev)
             self.dw13 = torch.empty((NG, 2 * I, H), dtype=f32, device=dev)
             self.dw2 = torch.empty((NG, H, I), dtype=f32, device=dev)
             self.dx = torch.empty((T, H), dtype=act, device=dev)
@@ -209,6 +295,8 @@ class MoELayer:
         self.route(x, stream)
         self.permute(x, stream)
         self.expert_ffn(stream)
+        if self.checkpoint8:
+            L.moe_checkpoint_save(self.p, self.au, self.au_q, self.au_scale, stream)
         self.combine(stream)
         return self.y
 
@@ -216,7 +304,50 @@ class MoELayer:
         """Aux-loss-free bias update from this batch's expert counts (in place)."""
         L.moe_bias_update(self.p, self.counts, gamma, self.bias, stream)
 
+    def balance_loss(self, seq_offsets, stream=None):
+        """Sequence-wise balance loss of the last forward's routing: seq_offsets [n_seq+1] int32
+        on the device -> [n_seq] fp32 (overwritten by the next call with as many sequences).
+        Also kept: counts per (sequence, expert) and mean affinity shares in self.seq_counts,
+        self.seq_prob.  Its gradient joins the next backward(dy, dseq_loss=...)."""
+        n, E = seq_offsets.numel() - 1, self.shape.E
+        if self._balance is None or self._balance[0] != n:
+            dev, f32 = self.logits.device, torch.float32
+            self._balance = (n, torch.empty((n,), dtype=f32, device=dev), torch.empty(
+                (L.moe_balance_loss_workspace_bytes(self.p, n),), dtype=torch.uint8, device=dev))
+            self.seq_counts = torch.empty((n, E), dtype=torch.int32, device=dev)
+            self.seq_prob = torch.empty((n, E), dtype=f32, device=dev)
+        self._seq_offsets = seq_offsets
+        _, loss, ws = self._balance
+        L.moe_balance_loss(self.p, self.logits, self.topk_idx, seq_offsets, n, self.seq_counts,
+                           self.seq_prob, loss, ws, ws.numel(), stream)
+        return loss
+
+    def router_backward_dense(self, dseq_loss, stream=None):
+        """The router's backward with the balance loss's gradient (dseq_loss [n_seq] fp32, the
+        gradient of the sequences' losses) joined to the gates'."""
+        assert self._balance is not None, "call balance_loss first"
+        T, E = self.shape.T, self.shape.E
+        if not hasattr(self, "dlogits"):
+            self.dlogits = torch.empty((T, E), dtype=torch.float32, device=self.logits.device)
+            n = L.moe_workspace_bytes(self.p, L.MOE_CALL_ROUTER_BACKWARD_DENSE)
+            self.ws[L.MOE_CALL_ROUTER_BACKWARD_DENSE] = torch.empty(
+                (n,), dtype=torch.uint8, device=self.logits.device)
+        L.moe_balance_loss_backward(self.p, self.logits, self._seq_offsets, self._balance[0],
+                                    self.seq_counts, dseq_loss, self.topk_idx, self.topk_gate,
+                                    self.dgate, self.dlogits, stream)
+        x = self._x if self.gather else self._xin
+        ws, n = self._ws(L.MOE_CALL_ROUTER_BACKWARD_DENSE)
+        L.moe_router_backward_dense(self.p, x, self.w_router, self.dlogits, self.dx_router,
+                                    self.dw_router, ws, n, stream)
+
     def expert_ffn_backward_input(self, stream=None):
+        if self.checkpoint8 and self.w13tp is not None:
+            L.moe_expert_ffn_backward_input_checkpoint(
+                self.p, self.offsets, self.w13tp, self.w2tp, self.au_q, self.au_scale,
+                self.dy_sorted, self.dau, self.h, self.dx_sorted, stream)
+            return
+        if self.checkpoint8:
+            L.moe_checkpoint_restore(self.p, self.au_q, self.au_scale, self.au, self.h, stream)
         if self.w13tp is not None:
             L.moe_expert_ffn_backward_input_packed(self.p, self.offsets, self.w13tp, self.w2tp,
                                                    self.au, self.dy_sorted, self.dau,
@@ -244,12 +375,16 @@ class MoELayer:
         L.moe_unpermute_sum(self.p, self.dx_sorted, self.inv_perm, self.dx_router, self.dx,
                             stream)
 
-    def backward(self, dy, stream=None):
-        """Gradients of sum(dy * y) for the last forward (train=True): returns self.dx and
+    def backward(self, dy, stream=None, dseq_loss=None):
+        """Gradients of sum(dy * y) for the last forward (train=True), plus those of
+        sum(dseq_loss * balance_loss(...)) where dseq_loss is given: returns self.dx and
         fills dw_router, dw13, dw2 (fp32).  The routing bias has no gradient."""
         assert self.train, "construct the layer with train=True"
         self.combine_backward(dy, stream)
-        self.router_backward(stream)
+        if dseq_loss is None:
+            self.router_backward(stream)
+        else:
+            self.router_backward_dense(dseq_loss, stream)
         self.expert_ffn_backward_input(stream)
         self.expert_ffn_backward_weight(stream)
         self.unpermute_sum(stream)

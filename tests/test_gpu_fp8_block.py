@@ -1,0 +1,250 @@
+"""The block-scaled FP8 product and its quantiser, of any size, against their definitions.
+
+Tolerances: the quantiser's codes and scales bit for bit (fp32 quotients, torch's cast).  The
+product: code products are exact, a block's sum of 128 of them and the sum over nb blocks are
+taken in fp32, each addition rounded or truncated (2^-23 of the running magnitude), the promotion
+two more: (128 + nb + 8) 2^-23 of sum |a b| with the scales.  A bf16 output has half a step more,
+and its products are formed by the FP8 matrix instruction, which aligns the 8 products of
+adjacent k to the largest and drops what lies more than 13 bits below its leading bit (of 2^16 and
+2^e in one group, e = 3 stays and e = 2 is lost; in two groups 24 bits stay).  With m the group's
+largest |a b|, each of the 7 others loses less than 2^-13 m, so a group is off by less than
+7 2^-13 m, at most 7 2^-13 of its sum |a b|: 7 2^-13 sum |a b| more."""
+import pytest
+
+from gpu_cases import log
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+F8 = torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from mixture_experts_layer_added_amd import _lib
+    _lib.lib()
+
+
+def up(n, m):
+    return -(-n // m) * m
+
+
+def codes_of(x):
+    n, m = x.shape
+    w = torch.nn.functional.pad(x.float(), (0, up(m, 128) - m)).view(n, -1, 128)
+    amax = w.abs().amax(2)
+    scale = amax / 448
+    scale = torch.where(scale > 0, scale, torch.ones_like(scale))
+    q = (w / scale[:, :, None]).clamp(-448, 448).to(F8).view(torch.uint8).reshape(n, -1)
+    return q[:, :m], scale
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols,pad", [(1, 1, 0), (1, 8, 0), (3, 7, 1), (16, 128, 0),
+                                           (17, 129, 0), (128, 128, 8), (129, 255, 1),
+                                           (200, 640, 24), (1, 4099, 0), (4099, 1, 0),
+                                           (300, 264, 0)])
+def test_quantize(rows, cols, pad, dtype):
+    from mixture_experts_layer_added_amd import _lib as L
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    g = torch.Generator().manual_seed(rows * 7 + cols)
+    x = torch.randn((rows, cols + pad), generator=g)
+    x *= 10.0 ** torch.randint(-5, 4, (rows, 1), generator=g)
+    x[rows // 2] = 0
+    x = x.to(dt)
+    x[:, cols:] = float("nan")  # behind the row: never read into a scale
+    ldq, ldt = up(cols, 16) + 16, up(rows, 16) + 32
+    ref = codes_of(x[:, :cols]), codes_of(x[:, :cols].t())
+    for form in ("rows", "cols", "both"):
+        q = torch.full((rows, ldq), 0x55, dtype=torch.uint8, device="cuda")
+        qt = torch.full((cols, ldt), 0x55, dtype=torch.uint8, device="cuda")
+        s = torch.full((rows, up(cols, 128) // 128), -1.0, device="cuda")
+        st = torch.full((cols, up(rows, 128) // 128), -1.0, device="cuda")
+        L.moe_quantize_fp8(x.cuda(), L.MOE_F32 if dtype == "f32" else L.MOE_BF16, rows, cols,
+                           cols + pad, q if form != "cols" else None, ldq,
+                           s if form != "cols" else None, qt if form != "rows" else None, ldt,
+                           st if form != "rows" else None)
+        torch.cuda.synchronize()
+        if form != "cols":
+            assert torch.equal(q[:, :cols].cpu(), ref[0][0]) and torch.equal(s.cpu(), ref[0][1])
+        if form != "rows":
+            assert torch.equal(qt[:, :rows].cpu(), ref[1][0])
+            assert torch.equal(st.cpu(), ref[1][1])
+        assert bool((q[:, cols if form != "cols" else 0:] == 0x55).all())
+        assert bool((qt[:, rows if form != "rows" else 0:] == 0x55).all())
+
+
+def test_quantize_small_values():
+    """Blocks whose largest value is so small that amax/448 is not a normal number, or zero."""
+    from mixture_experts_layer_added_amd import _lib as L
+    x = torch.zeros((4, 128))
+    x[0, 3], x[1, 5], x[2, 7] = 1e-45, 3e-39, 448 * 1.2e-38
+    q = torch.empty((4, 128), dtype=torch.uint8, device="cuda")
+    s = torch.empty((4, 1), device="cuda")
+    L.moe_quantize_fp8(x.cuda(), L.MOE_F32, 4, 128, 128, q, 128, s)
+    torch.cuda.synchronize()
+    v = q.cpu().view(F8).float() * s.cpu()
+    assert bool(v.isfinite().all())
+    assert bool(((v - x).abs() <= 2 ** -4 * x + 1e-44).all())
+
+
+def operand(rows, cols, across, g, ld=None, wild=True):
+    """Random codes (finite ones), the pad filled with NaN codes, and scales."""
+    ld = up(cols, 16) if ld is None else ld
+    q = torch.randint(0, 256, (rows, ld), generator=g, dtype=torch.uint8)
+    q[(q & 0x7f) == 0x7f] = 0x3a
+    q[:, cols:] = 0x7f
+    s = torch.rand((-(-rows // across), up(cols, 128) // 128), generator=g) + 0.5
+    if wild:
+        s = s * 10.0 ** torch.randint(-3, 3, s.shape, generator=g)
+    return q, s
+
+
+def wide(q, s, cols, across):
+    r = torch.arange(q.shape[0])[:, None] // across
+    return q[:, :cols].view(F8).double() * s.double()[r, torch.arange(cols)[None] // 128]
+
+
+def run(M, N, K, a, sa, b, sb, b_rows, out, c0=None, ldc=None, stream=None):
+    from mixture_experts_layer_added_amd import _lib as L
+    ldc = N if ldc is None else ldc
+    dt = torch.float32 if out == "f32" else torch.bfloat16
+    c = torch.full((M + 1, ldc), float("nan"), dtype=dt, device="cuda")
+    if c0 is not None:
+        c[:M, :N] = c0.cuda()
+    n = L.moe_gemm_fp8_workspace_bytes(M, N, K)
+    ws = torch.full((n + 256,), 0x7f, dtype=torch.uint8, device="cuda")
+    L.moe_gemm_fp8(M, N, K, a.cuda(), a.shape[1], sa.cuda(), b.cuda(), b.shape[1], sb.cuda(),
+                   b_rows, c, ldc, L.MOE_F32 if out == "f32" else L.MOE_BF16, int(c0 is not None),
+                   ws if n else None, n, stream)
+    torch.cuda.synchronize()
+    assert bool(c[M:].isnan().all()) and bool(c[:M, N:].isnan().all()), "a write behind C"
+    assert bool((ws[n:] == 0x7f).all()), "a write behind the workspace"
+    return c[:M, :N].cpu()
+
+
+def near(c, A, B, out, c0=None):
+    K = A.shape[1]
+    ref, mag = A @ B.t(), A.abs() @ B.abs().t()
+    if c0 is not None:
+        ref, mag = ref + c0.double(), mag + c0.double().abs()
+    tol = (128 + up(K, 128) // 128 + 8) * 2.0 ** -23 * mag
+    if out == "bf16":
+        tol = tol + 7 * 2.0 ** -13 * mag
+        tol = tol + 2.0 ** -8 * (ref.abs() + tol)
+    err = (c.double() - ref).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
+    return float((err / mag).max() * 2 ** 23)
+
+
+SIZES = [(1, 1, 1), (1, 128, 128), (3, 5, 7), (1, 200, 500), (16, 64, 16), (17, 33, 130),
+         (31, 129, 257), (32, 512, 1024), (33, 256, 384), (64, 64, 4099), (65, 300, 640),
+         (100, 1000, 129), (128, 128, 128), (129, 260, 1025), (200, 513, 300), (256, 256, 2048),
+         (257, 511, 777), (300, 1024, 256), (1000, 77, 130), (520, 770, 515)]
+
+
+@pytest.mark.parametrize("M,N,K", SIZES)
+@pytest.mark.parametrize("b_rows", [1, 128])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_product(M, N, K, b_rows, out):
+    g = torch.Generator().manual_seed(M + 3 * N + 5 * K)
+    a, sa = operand(M, K, 1, g)
+    b, sb = operand(N, K, b_rows, g)
+    c = run(M, N, K, a, sa, b, sb, b_rows, out)
+    e = near(c, wide(a, sa, K, 1), wide(b, sb, K, b_rows), out)
+    if out == "f32":
+        log(f"    {M}x{N}x{K}, b_rows {b_rows}: within {e:.2f} of 2^-23 sum |ab|")
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 65, 300), (40, 260, 1000), (300, 520, 515),
+                                   (600, 1030, 400)])
+def test_strides_and_accumulation(M, N, K):
+    """Rows longer than their codes, an output row stride that is not a multiple of 4, and
+    C += A B^T."""
+    g = torch.Generator().manual_seed(K)
+    a, sa = operand(M, K, 1, g, ld=up(K, 16) + 48)
+    b, sb = operand(N, K, 1, g, ld=up(K, 16) + 16)
+    c0 = torch.randn((M, N), generator=g)
+    A, B = wide(a, sa, K, 1), wide(b, sb, K, 1)
+    near(run(M, N, K, a, sa, b, sb, 1, "f32", c0=c0, ldc=N + 3), A, B, "f32", c0)
+    near(run(M, N, K, a, sa, b, sb, 1, "bf16", ldc=N + 5), A, B, "bf16")
+
+
+def test_largest_codes():
+    """Sums of products of the largest codes, 448 x 448, of one sign: nothing overflows before
+    its scale."""
+    M, N, K = 70, 300, 1500
+    a, b = (torch.full((r, up(K, 16)), 0x7e, dtype=torch.uint8) for r in (M, N))
+    sa, sb = torch.full((M, 12), 2.0 ** -20), torch.full((N, 12), 2.0 ** 3)
+    near(run(M, N, K, a, sa, b, sb, 1, "f32"), wide(a, sa, K, 1), wide(b, sb, K, 1), "f32")
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 512, 1024), (90, 384, 2000), (600, 520, 515)])
+def test_repeats_streams_and_graphs(M, N, K):
+    """The same bits on another stream and from a graph replayed with new operands."""
+    from mixture_experts_layer_added_amd import _lib as L
+    g = torch.Generator().manual_seed(1)
+    a, sa = operand(M, K, 1, g)
+    b, sb = operand(N, K, 128, g)
+    c = run(M, N, K, a, sa, b, sb, 128, "bf16")
+    assert torch.equal(c, run(M, N, K, a, sa, b, sb, 128, "bf16", stream=torch.cuda.Stream()))
+    n = L.moe_gemm_fp8_workspace_bytes(M, N, K)
+    ws = torch.empty((max(n, 16),), dtype=torch.uint8, device="cuda")
+    ad, sad, bd, sbd = a.cuda(), sa.cuda(), b.cuda(), sb.cuda()
+    out = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+
+    def call():
+        L.moe_gemm_fp8(M, N, K, ad, ad.shape[1], sad, bd, bd.shape[1], sbd, 128, out, N,
+                       L.MOE_BF16, 0, ws, n)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        call()
+    for i in range(3):
+        a2, sa2 = operand(M, K, 1, g)
+        ad.copy_(a2)
+        sad.copy_(sa2)
+        out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out.cpu(), run(M, N, K, a2, sa2, b, sb, 128, "bf16")), i
+
+
+@pytest.mark.parametrize("M", [1, 37, 300])
+def test_linear_layer(M):
+    """Fp8Linear as a training program runs it: forward, backward, a second batch added into
+    dw; against the products of its quantised operands in 64 bits."""
+    from mixture_experts_layer_added_amd.layer import Fp8Linear, quantize_fp8
+    N, K = 384, 256
+    g = torch.Generator().manual_seed(M)
+    w = (torch.randn((N, K), generator=g) * 0.05).bfloat16()
+    lin = Fp8Linear(w.cuda(), train=True)
+    W = wide(lin.w_q.cpu(), lin.w_scale.cpu(), K, 128)
+    assert bool(((W - w.double()).abs() <= 2.0 ** -4 * w.double().abs() +
+                 lin.w_scale.max().cpu() * 2.0 ** -10).all())
+    dw = torch.zeros((N, K), dtype=torch.float64)
+    mag = torch.zeros_like(dw)
+    for _ in range(2):
+        x = torch.randn((M, K), generator=g).bfloat16()
+        dy = torch.randn((M, N), generator=g).bfloat16()
+        y = lin.forward(x.cuda())
+        dx = lin.backward(dy.cuda())
+        torch.cuda.synchronize()
+        xq, xs, xt, xts = [t.cpu() for t in quantize_fp8(x.cuda(), True, True)]
+        dq, ds, dt, dts = [t.cpu() for t in quantize_fp8(dy.cuda(), True, True)]
+        near(y.cpu(), wide(xq, xs, K, 1), W, "bf16")
+        near(dx.cpu(), wide(dq, ds, N, 1), W.t(), "bf16")
+        A, B = wide(dt, dts, M, 1), wide(xt, xts, M, 1)
+        dw, mag = dw + A @ B.t(), mag + A.abs() @ B.abs().t()
+    tol = (128 + 3 + 16) * 2.0 ** -23
+    assert bool(((lin.dw.cpu().double() - dw).abs() <= tol * mag).all())
+    lin.zero_grad()
+    assert not lin.dw.any()
+    # a strided view of rows is quantised as its dense copy
+    v = torch.randn((M, K + 64), generator=g).bfloat16().cuda()[:, 64:]
+    for p, q in zip(quantize_fp8(v, True, True), quantize_fp8(v.contiguous(), True, True)):
+        m = min(p.shape[1], M if p.shape[0] == K else K) if p.dtype == torch.uint8 else None
+        assert torch.equal(p[:, :m], q[:, :m])
