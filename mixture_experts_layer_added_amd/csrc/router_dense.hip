@@ -1,75 +1,494 @@
 // Router backward for a dense gradient of the logits, dz [T, E] (the balance loss gives every
 // expert's logit one, not the chosen ones alone):
 //   dx[t] = sum_e dz[t,e] W_r[e]      dW_r[e] = sum_t dz[t,e] x[t]
-// both in fp32, summed in a fixed order.
+// in fp32 on the 16-bit matrix instructions (2.5 PFLOP/s against 0.16 for fp32 operands): each
+// fp32 operand is split once into 16-bit parts whose sum it is, and the products of the parts
+// are added in fp32, in a fixed order.
+//   dx:  two fp16 parts of dz and of W_r.  A row of dz and a column of W_r are first scaled by
+//     a power of two that brings their largest value to [2^14, 2^15): hi = fp16(v), lo =
+//     fp16(v - hi) then hold 22 bits of every value within 2^-17 of the largest, and an error
+//     under 2^-40 of the largest of smaller ones.  hi hi + lo hi + hi lo leaves out 2^-22 of a
+//     product; three products.
+//   dW:  bf16 x is taken as it is, dz in three bf16 parts (24 bits, any exponent): three
+//     products.  fp32 x in three parts as well, and the six products above 2^-24.
+//   k_rd_split: the parts of dz (both kinds) and of W_r, transposed, with their exponents.
+//   k_rd_split_x: the parts of an fp32 x.
+//   k_rd_dx: 128 (or 64) tokens x 128 columns a workgroup; both operands have k innermost, so a
+//     step is 64 of k (128-byte rows, as in the FP8 product), 3 Ep / 64 steps.
+//   k_rd_dw: 128 (or 64) experts x 128 columns, 32 tokens a step; both operands have k outermost
+//     and are read with ds_read_b64_tr_b16 (gemm_bwd.hip).  Split over the tokens; k_rd_join
+//     adds the parts in order.
+#include <type_traits>
+
 #include "common.h"
 
 namespace moe {
 namespace {
 
-__device__ __forceinline__ float val(const float* p) { return *p; }
-__device__ __forceinline__ float val(const uint16_t* p) { return bf16_bits_to_f32(*p); }
+typedef short v4i16 __attribute__((ext_vector_type(4)));
+typedef __attribute__((__vector_size__(8 * sizeof(_Float16)))) _Float16 f16x8;
 
-// C[m,n] = sum_k A(m,k) B(k,n), 64 x 64 a workgroup, 4 x 4 a thread, 16 of k a step; A(m,k) at
-// m * am + k * ak, B(k,n) at k * ldb + n
-template <typename TB>
-__global__ __launch_bounds__(256) void k_rd_tile(const float* __restrict__ A, int64_t am,
-                                                 int64_t ak, const TB* __restrict__ B,
-                                                 int64_t ldb, float* __restrict__ C, int64_t M,
-                                                 int64_t N, int64_t K, int64_t mt) {
-  __shared__ float as[16][65], bs[16][65];
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int64_t m0 = (blockIdx.x % mt) * 64, n0 = (blockIdx.x / mt) * 64;
-  float acc[4][4] = {};
-  for (int64_t k0 = 0; k0 < K; k0 += 16) {
+constexpr int DBN = 128;   // columns of a tile
+constexpr int kWStep = 32; // tokens of a k_rd_dw step
+
+__device__ __forceinline__ uint16_t f16_bits(_Float16 v) {
+  return __builtin_bit_cast(uint16_t, v);
+}
+// exponent that brings |v| < 2^127 to [2^14, 2^15); 0 for 0
+__device__ __forceinline__ int lift(float amax) {
+  return amax > 0.0f ? 15 - __builtin_amdgcn_frexp_expf(amax) : 0;
+}
+// the three bf16 parts of v: each the rounding of what is left
+__device__ __forceinline__ void parts3(float v, uint16_t* p) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    p[i] = f32_to_bf16_bits(v);
+    v -= bf16_bits_to_f32(p[i]);
+  }
+}
+
+// Blocks 0 .. zb-1: 4 rows of dz each, one a wave.  The rest: 32 columns of W_r each.
+__global__ __launch_bounds__(256) void k_rd_split(
+    const float* __restrict__ dz, const float* __restrict__ w, int64_t T, int H, int E, int Ep,
+    int64_t zb, uint16_t* __restrict__ zh, uint16_t* __restrict__ zp, int32_t* __restrict__ ze,
+    uint16_t* __restrict__ wh, int32_t* __restrict__ we) {
+  const int tid = threadIdx.x;
+  if (blockIdx.x < zb) {
+    const int lane = tid & 63;
+    const int64_t t = (int64_t)blockIdx.x * 4 + (tid >> 6);
+    if (t >= T) return;
+    constexpr int kMost = 8;  // Ep <= 512
+    float v[kMost], m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+      const int e = 64 * i + lane;
+      v[i] = e < E ? dz[t * E + e] : 0.0f;
+      m = __builtin_fmaxf(m, __builtin_fabsf(v[i]));
+    }
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) m = __builtin_fmaxf(m, __shfl_xor(m, o));
+    const int ex = lift(m);
+    if (lane == 0) ze[t] = ex;
+    const int64_t plane = T * Ep;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+      const int e = 64 * i + lane;
+      if (e >= Ep) break;
+      const float s = __builtin_ldexpf(v[i], ex);
+      const _Float16 hi = (_Float16)s;
+      uint16_t p[3];
+      parts3(v[i], p);
+      uint16_t* q = zh + t * Ep + e;
+      q[0] = f16_bits(hi);
+      q[plane] = f16_bits((_Float16)(s - (float)hi));
+      q = zp + t * Ep + e;
+      q[0] = p[0];
+      q[plane] = p[1];
+      q[2 * plane] = p[2];
+    }
+    return;
+  }
+  __shared__ float s_m[8][32];
+  __shared__ uint32_t s_t[32][65];  // hi | lo << 16 of 32 columns x 64 experts
+  const int c = tid & 31, g = tid >> 5;
+  const int h0 = (int)(blockIdx.x - zb) * 32;
+  float m = 0.0f;
+  for (int e = g; e < E; e += 8) m = __builtin_fmaxf(m, __builtin_fabsf(w[(int64_t)e * H + h0 + c]));
+  s_m[g][c] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = __builtin_fmaxf(m, s_m[i][c]);
+  const int ex = lift(m);
+  if (g == 0) we[h0 + c] = ex;
+  for (int e0 = 0; e0 < Ep; e0 += 64) {
     __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = e0 + 8 * i + g;
+      const float s = e < E ? __builtin_ldexpf(w[(int64_t)e * H + h0 + c], ex) : 0.0f;
+      const _Float16 hi = (_Float16)s;
+      s_t[c][8 * i + g] = f16_bits(hi) | (uint32_t)f16_bits((_Float16)(s - (float)hi)) << 16;
+    }
+    __syncthreads();
+    // column c2's 64 experts: 8 lanes x 8 of them, both parts
+    const int c2 = tid >> 3, l = tid & 7;
+    uint32_t hi[4], lo[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int e = tid + 256 * i;
-      const int kr = ak == 1 ? e & 15 : e >> 6, mr = ak == 1 ? e >> 4 : e & 63;
-      as[kr][mr] = m0 + mr < M && k0 + kr < K ? A[(m0 + mr) * am + (k0 + kr) * ak] : 0.0f;
-      const int kc = e >> 6, nc = e & 63;
-      bs[kc][nc] = n0 + nc < N && k0 + kc < K ? val(B + (k0 + kc) * ldb + n0 + nc) : 0.0f;
+      const uint32_t a = s_t[c2][8 * l + 2 * i], b = s_t[c2][8 * l + 2 * i + 1];
+      hi[i] = (a & 0xFFFFu) | b << 16;
+      lo[i] = a >> 16 | (b & 0xFFFF0000u);
     }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 16; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          acc[i][j] = __builtin_fmaf(as[k][ty + 16 * i], bs[k][tx + 16 * j], acc[i][j]);
+    uint16_t* q = wh + (int64_t)(h0 + c2) * Ep + e0 + 8 * l;
+    *reinterpret_cast<uint4*>(q) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(q + (int64_t)H * Ep) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
+}
+
+__global__ __launch_bounds__(256) void k_rd_split_x(const float* __restrict__ x, int64_t n,
+                                                    uint16_t* __restrict__ xp) {
+  const int64_t stride = (int64_t)gridDim.x * 256 * 4;
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n; i += stride) {
+    const float4 v = *reinterpret_cast<const float4*>(x + i);
+    uint16_t a[3], b[3], c[3], d[3];
+    parts3(v.x, a);
+    parts3(v.y, b);
+    parts3(v.z, c);
+    parts3(v.w, d);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+    for (int p = 0; p < 3; ++p)
+      *reinterpret_cast<uint2*>(xp + p * n + i) =
+          make_uint2(a[p] | (uint32_t)b[p] << 16, c[p] | (uint32_t)d[p] << 16);
+  }
+}
+
+// tile `work` of mt x nt in bands of 8 row tiles, column-major inside a band
+__device__ __forceinline__ void band_tile(int tile, int mt, int nt, int* m, int* n) {
+  constexpr int kBand = 8;
+  const int band = tile / (kBand * nt), within = tile % (kBand * nt);
+  const int rb = min(kBand, mt - band * kBand);
+  *m = band * kBand + within % rb;
+  *n = within / rb;
+}
+
+// 16-byte chunk c of a 128-byte row r
+__device__ __forceinline__ int at128(int r, int c) { return r * 128 + ((c ^ (r >> 1)) & 7) * 16; }
+
+// dx: k runs over 3 Ep: (hi, hi), (lo, hi), (hi, lo) of (dz, W_r).  4 waves of (BM/WM) x
+// (128/WN) outputs; the W_r part is the first operand, so a lane's results lie in one row.
+template <int BM, int WM, int WN>
+__global__ __launch_bounds__(256, 1) void k_rd_dx(const uint16_t* __restrict__ zh,
+                                                  const int32_t* __restrict__ ze,
+                                                  const uint16_t* __restrict__ wh,
+                                                  const int32_t* __restrict__ we,
+                                                  float* __restrict__ dx, int64_t T, int H, int Ep,
+                                                  int mt, int nt) {
+  constexpr int W = 4, NST = 2, SM = BM / WM / 32, SN = DBN / WN / 32;
+  constexpr int kStage = (BM + DBN) * 128, NA = BM / 8 / W, NB = DBN / 8 / W;
+  static_assert(W * 32 * (DBN / WN) * 4 <= NST * kStage, "output staging fits the ring");
+  __shared__ __attribute__((aligned(1024))) char smem[NST * kStage];
+  const int total = mt * nt, per = (total + kXcds - 1) / kXcds;
+  const int work = (blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
+  if (blockIdx.x / kXcds >= per || work >= total) return;
+  int mi, ni;
+  band_tile(work, mt, nt, &mi, &ni);
+  const int64_t m0 = (int64_t)mi * BM;
+  const int n0 = ni * DBN;
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wv / WN, wn = wv % WN, fr = lane & 31, kq = lane >> 5;
+  const int m_rows = (int)min((int64_t)BM, T - m0);
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(smem));
+  const uint32_t row_b = 2 * Ep;  // bytes of a row of either operand
+  const int lrow = 8 * wv + (lane >> 3);
+  const uint32_t lchunk = 16 * ((lane & 7) ^ ((4 * (wv & 1) + (lane >> 4)) & 7));
+  const int per_part = Ep / 64, nk = 3 * per_part;
+  auto stage = [&](int kt, int st) {
+    const int part = kt / per_part;
+    const uint32_t ko = (uint32_t)(kt - part * per_part) * 128;
+    // rows past T arrive as zeros
+    const i32x4 ar = buffer_rsrc(zh + (part == 1 ? T * Ep : 0) + m0 * Ep, m_rows * row_b);
+    const i32x4 br = buffer_rsrc(wh + (part == 2 ? (int64_t)H * Ep : 0) + (int64_t)n0 * Ep,
+                                 DBN * row_b);
+    const uint32_t dst = lds0 + st * kStage + 8 * wv * 128;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-      if (m < M && n < N) C[m * N + n] = acc[i][j];
+    for (int i = 0; i < NA; ++i)
+      load16_to_lds(ar, dst + i * 8 * W * 128, (8 * W * i + lrow) * row_b + lchunk + ko);
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+      load16_to_lds(br, dst + (BM + i * 8 * W) * 128, (8 * W * i + lrow) * row_b + lchunk + ko);
+  };
+  f32x16 acc[SM][SN];
+#pragma unroll
+  for (int m = 0; m < SM; ++m)
+#pragma unroll
+    for (int n = 0; n < SN; ++n)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[m][n][i] = 0.0f;
+  stage(0, 0);
+  for (int kt = 0; kt < nk; ++kt) {
+    wait_vm<0>();
+    __syncthreads();
+    if (kt + 1 < nk) stage(kt + 1, (kt + 1) & 1);
+    const char* as = smem + (kt & 1) * kStage;
+    const char* bs = as + BM * 128;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      f16x8 a[SM], b[SN];
+#pragma unroll
+      for (int m = 0; m < SM; ++m)
+        a[m] = *reinterpret_cast<const f16x8*>(as + at128(wm * (BM / WM) + 32 * m + fr, 2 * s + kq));
+#pragma unroll
+      for (int n = 0; n < SN; ++n)
+        b[n] = *reinterpret_cast<const f16x8*>(bs + at128(wn * (DBN / WN) + 32 * n + fr, 2 * s + kq));
+#pragma unroll
+      for (int m = 0; m < SM; ++m)
+#pragma unroll
+        for (int n = 0; n < SN; ++n)
+          acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(b[n], a[m], acc[m][n], 0, 0, 0);
     }
+  }
+  __syncthreads();  // every wave is done with the ring, which now stages the output
+  constexpr int kCols = DBN / WN, kChunks = kCols / 4, kMask = kChunks < 16 ? kChunks - 1 : 15;
+  char* stg = smem + wv * 32 * kCols * 4;
+  const int h0 = n0 + wn * kCols;
+#pragma unroll
+  for (int m = 0; m < SM; ++m) {
+    const int64_t row0 = m0 + wm * (BM / WM) + 32 * m;
+    const int er = row0 + fr < T ? ze[row0 + fr] : 0;
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+    for (int n = 0; n < SN; ++n)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int col = 32 * n + 8 * q + 4 * kq;
+        const int4 ec = *reinterpret_cast<const int4*>(we + h0 + col);
+        const f32x16& a = acc[m][n];
+        *reinterpret_cast<float4*>(stg + fr * kCols * 4 + (((col / 4) ^ (fr & kMask)) << 4)) =
+            make_float4(__builtin_ldexpf(a[4 * q], -er - ec.x),
+                        __builtin_ldexpf(a[4 * q + 1], -er - ec.y),
+                        __builtin_ldexpf(a[4 * q + 2], -er - ec.z),
+                        __builtin_ldexpf(a[4 * q + 3], -er - ec.w));
+      }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+    for (int e = lane; e < 32 * kChunks; e += 64) {
+      const int r = e / kChunks, ch = e % kChunks;
+      const u32x4 v =
+          *reinterpret_cast<const u32x4*>(stg + r * kCols * 4 + ((ch ^ (r & kMask)) << 4));
+      if (row0 + r < T)
+        __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(dx + (row0 + r) * H + h0 + 4 * ch));
+    }
+  }
+}
+
+// k-outer stages: rows (tokens) of 256 bytes, 16-byte chunk c of row r at slot c ^ 4 (r & 3).
+// A fragment read's lane offset for columns 32 p .. +31 (see gemm_bwd.hip, whose rows have 512
+// bytes): 8 consecutive k of a column per lane by two transposing reads.
+constexpr int kORow = 256;
+__device__ __forceinline__ uint32_t ko_off(int lane, int p) {
+  const int g = lane >> 4, j = lane & 15, i = j >> 2;
+  const int row = 8 * (g >> 1) + i;
+  const int c = 4 * p + 2 * (g & 1) + ((j & 3) >> 1);
+  return (uint32_t)(row * kORow + ((c ^ (4 * i)) << 4) + (j & 1) * 8);
+}
+__device__ __forceinline__ bf16x8 ko_frag(uint32_t addr) {
+  typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
+  const v4i16 both[2] = {
+      __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(uintptr_t)addr),
+      __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(uintptr_t)(addr + 4 * kORow))};
+  bf16x8 f;
+  __builtin_memcpy(&f, both, 16);
+  return f;
+}
+
+// dW partial sums over the tokens of part blockIdx.y: BM experts x 128 columns a workgroup, 4
+// waves as WM x WN.  XP parts of x: 1 (bf16 x itself) or 3.
+template <int BM, int WM, int WN, int XP>
+__global__ __launch_bounds__(256, 1) void k_rd_dw(const uint16_t* __restrict__ zp,
+                                                  const uint16_t* __restrict__ xp,
+                                                  float* __restrict__ out, int64_t T, int H, int E,
+                                                  int Ep, int64_t part_rows, int nt) {
+  constexpr int W = 4, NST = 2, SM = BM / WM / 32, SN = DBN / WN / 32;
+  constexpr int kZ = kWStep * kORow;       // a plane of a stage: 8 KiB (BM = 64: half used)
+  constexpr int kStage = (3 + XP) * kZ;
+  constexpr int kI = kWStep / 4 / W;       // load instructions of a plane and wave
+  __shared__ __attribute__((aligned(1024))) char smem[NST * kStage];
+  const int mi = blockIdx.x / nt, n0 = (blockIdx.x % nt) * DBN;
+  const int64_t t0 = (int64_t)blockIdx.y * part_rows, t1 = min(t0 + part_rows, T);
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wv / WN, wn = wv % WN;
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(smem));
+  // instruction i of wave wv fills rows 4 (i W + wv) .. +3; columns past the tile's BM
+  // experts (BM = 64) are not loaded
+  const int lr = lane >> 4, lc = (lane & 15) ^ (4 * lr);
+  auto stage = [&](int64_t t, int st) {
+    const int rows = (int)min((int64_t)kWStep, t1 - t);  // later ones arrive as zeros
+    const uint32_t dst = lds0 + st * kStage + 4 * wv * kORow;
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+      const i32x4 r = buffer_rsrc(zp + (p * T + t) * Ep, (uint32_t)(rows * Ep * 2));
+#pragma unroll
+      for (int i = 0; i < kI; ++i) {
+        const uint32_t o = (uint32_t)((4 * (i * W + wv) + lr) * Ep + mi * BM + 8 * lc) * 2;
+        load16_to_lds(r, dst + p * kZ + i * 4 * W * kORow, 8 * lc < BM ? o : 0x7ffffff0u);
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < XP; ++p) {
+      const i32x4 r = buffer_rsrc(xp + (p * T + t) * H, (uint32_t)(rows * H * 2));
+#pragma unroll
+      for (int i = 0; i < kI; ++i)
+        load16_to_lds(r, dst + (3 + p) * kZ + i * 4 * W * kORow,
+                      (uint32_t)((4 * (i * W + wv) + lr) * H + n0 + 8 * lc) * 2);
+    }
+  };
+  f32x16 acc[SM][SN];
+#pragma unroll
+  for (int m = 0; m < SM; ++m)
+#pragma unroll
+    for (int n = 0; n < SN; ++n)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[m][n][i] = 0.0f;
+  uint32_t oa[SM], ob[SN];
+#pragma unroll
+  for (int m = 0; m < SM; ++m) oa[m] = ko_off(lane, wm * SM + m);
+#pragma unroll
+  for (int n = 0; n < SN; ++n) ob[n] = ko_off(lane, wn * SN + n);
+  stage(t0, 0);
+  int st = 0;
+  for (int64_t t = t0; t < t1; t += kWStep, st ^= 1) {
+    wait_vm<0>();
+    __syncthreads();
+    if (t + kWStep < t1) stage(t + kWStep, st ^ 1);
+    const uint32_t zs = lds0 + st * kStage, xs = zs + 3 * kZ;
+#pragma unroll
+    for (int s = 0; s < kWStep / 16; ++s) {
+      bf16x8 a[3][SM], b[XP][SN];
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+#pragma unroll
+        for (int m = 0; m < SM; ++m) a[p][m] = ko_frag(zs + p * kZ + s * 16 * kORow + oa[m]);
+#pragma unroll
+      for (int p = 0; p < XP; ++p)
+#pragma unroll
+        for (int n = 0; n < SN; ++n) b[p][n] = ko_frag(xs + p * kZ + s * 16 * kORow + ob[n]);
+      // the smallest products first
+#pragma unroll
+      for (int sum = 2; sum >= 0; --sum)
+#pragma unroll
+        for (int p = 0; p <= sum; ++p) {
+          const int q = sum - p;  // part p of dz, part q of x
+          if (q >= XP) continue;
+#pragma unroll
+          for (int m = 0; m < SM; ++m)
+#pragma unroll
+            for (int n = 0; n < SN; ++n)
+              acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[p][m], b[q][n], acc[m][n], 0, 0, 0);
+        }
+    }
+  }
+  // element i of a lane: expert 8 (i/4) + 4 (lane/32) + i%4, column lane%32: 32 lanes store one
+  // 128-byte line
+#pragma unroll
+  for (int m = 0; m < SM; ++m)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int e = mi * BM + wm * (BM / WM) + 32 * m + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3);
+      if (e >= E) continue;
+      float* p = out + ((int64_t)blockIdx.y * E + e) * H + n0 + wn * (DBN / WN) + (lane & 31);
+#pragma unroll
+      for (int n = 0; n < SN; ++n) p[32 * n] = acc[m][n][i];
+    }
+}
+
+__global__ __launch_bounds__(256) void k_rd_join(const float* __restrict__ part, int parts,
+                                                 int64_t n, float* __restrict__ dw) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  float4 s = *reinterpret_cast<const float4*>(part + i);
+  for (int p = 1; p < parts; ++p) {
+    const float4 v = *reinterpret_cast<const float4*>(part + p * n + i);
+    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+  }
+  *reinterpret_cast<float4*>(dw + i) = s;
+}
+
+struct RdPlan {
+  int Ep, bm;         // experts padded to whole tiles, experts of a k_rd_dw tile
+  int parts;          // of the tokens
+  int64_t part_rows;
+  size_t zh, zp, ze, wh, we, xp, part, bytes;  // byte offsets in the workspace
+};
+
+RdPlan rd_plan(const Dims& d) {
+  RdPlan p;
+  p.bm = d.E <= 64 ? 64 : 128;
+  p.Ep = (d.E + p.bm - 1) / p.bm * p.bm;
+  // about two workgroups a CU, parts of at least 8 steps
+  const int64_t tiles = (int64_t)(p.Ep / p.bm) * (d.H / DBN);
+  const int64_t steps = (d.T + kWStep - 1) / kWStep;
+  int64_t s = 512 / tiles;
+  if (s > steps / 8) s = steps / 8;
+  if (s < 1) s = 1;
+  p.part_rows = (steps + s - 1) / s * kWStep;
+  p.parts = (int)((d.T + p.part_rows - 1) / p.part_rows);
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t o = at;
+    at += (n + 255) / 256 * 256;
+    return o;
+  };
+  const size_t TE = (size_t)d.T * p.Ep, HE = (size_t)d.H * p.Ep;
+  p.zh = take(TE * 4);
+  p.zp = take(TE * 6);
+  p.ze = take((size_t)d.T * 4);
+  p.wh = take(HE * 4);
+  p.we = take((size_t)d.H * 4);
+  p.xp = take(d.act == MOE_F32 ? (size_t)d.T * d.H * 6 : 0);
+  p.part = take(p.parts > 1 ? (size_t)p.parts * d.E * d.H * 4 : 0);
+  p.bytes = at;
+  return p;
+}
+
+template <int XP>
+void launch_dw(const RdPlan& p, const Dims& d, const uint16_t* zp, const uint16_t* xp, float* out,
+               hipStream_t st) {
+  const int nt = d.H / DBN;
+  const dim3 g((unsigned)(p.Ep / p.bm * nt), (unsigned)p.parts);
+  if (p.bm == 64)
+    hipLaunchKernelGGL((k_rd_dw<64, 2, 2, XP>), g, dim3(256), 0, st, zp, xp, out, d.T, d.H, d.E,
+                       p.Ep, p.part_rows, nt);
+  else
+    hipLaunchKernelGGL((k_rd_dw<128, 2, 2, XP>), g, dim3(256), 0, st, zp, xp, out, d.T, d.H, d.E,
+                       p.Ep, p.part_rows, nt);
 }
 
 }  // namespace
 
-size_t router_dense_ws_bytes(const Dims& d) { return 256; }
+size_t router_dense_ws_bytes(const Dims& d) { return rd_plan(d).bytes; }
 
 hipError_t launch_router_dense_bwd(const Dims& d, const void* x, const float* w, const float* dz,
                                    float* dx, float* dw, void* ws, hipStream_t st) {
-  const int64_t nt = (d.H + 63) / 64;
-  const int64_t mx = (d.T + 63) / 64, mw = (d.E + 63) / 64;
-  hipLaunchKernelGGL(k_rd_tile<float>, dim3((unsigned)(mx * nt)), dim3(256), 0, st, dz,
-                     (int64_t)d.E, (int64_t)1, w, (int64_t)d.H, dx, d.T, (int64_t)d.H,
-                     (int64_t)d.E, mx);
+  const RdPlan p = rd_plan(d);
+  char* b = static_cast<char*>(ws);
+  uint16_t* zh = reinterpret_cast<uint16_t*>(b + p.zh);
+  uint16_t* zp = reinterpret_cast<uint16_t*>(b + p.zp);
+  int32_t* ze = reinterpret_cast<int32_t*>(b + p.ze);
+  uint16_t* wh = reinterpret_cast<uint16_t*>(b + p.wh);
+  int32_t* we = reinterpret_cast<int32_t*>(b + p.we);
+  const int64_t zb = (d.T + 3) / 4;
+  hipLaunchKernelGGL(k_rd_split, dim3((unsigned)(zb + d.H / 32)), dim3(256), 0, st, dz, w, d.T,
+                     d.H, d.E, p.Ep, zb, zh, zp, ze, wh, we);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (d.act == MOE_BF16)
-    hipLaunchKernelGGL(k_rd_tile<uint16_t>, dim3((unsigned)(mw * nt)), dim3(256), 0, st, dz,
-                       (int64_t)1, (int64_t)d.E, static_cast<const uint16_t*>(x), (int64_t)d.H,
-                       dw, (int64_t)d.E, (int64_t)d.H, d.T, mw);
-  else
-    hipLaunchKernelGGL(k_rd_tile<float>, dim3((unsigned)(mw * nt)), dim3(256), 0, st, dz,
-                       (int64_t)1, (int64_t)d.E, static_cast<const float*>(x), (int64_t)d.H, dw,
-                       (int64_t)d.E, (int64_t)d.H, d.T, mw);
+  const int nt = d.H / DBN;
+  const int64_t mt128 = (d.T + 127) / 128;
+  if (mt128 * nt >= 256) {
+    const int per = (int)((mt128 * nt + kXcds - 1) / kXcds);
+    hipLaunchKernelGGL((k_rd_dx<128, 2, 2>), dim3(per * kXcds), dim3(256), 0, st, zh, ze, wh, we,
+                       dx, d.T, d.H, p.Ep, (int)mt128, nt);
+  } else {
+    const int mt = (int)((d.T + 63) / 64), per = (mt * nt + kXcds - 1) / kXcds;
+    hipLaunchKernelGGL((k_rd_dx<64, 2, 2>), dim3(per * kXcds), dim3(256), 0, st, zh, ze, wh, we,
+                       dx, d.T, d.H, p.Ep, mt, nt);
+  }
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  const uint16_t* xp = static_cast<const uint16_t*>(x);
+  if (d.act == MOE_F32) {
+    uint16_t* parts = reinterpret_cast<uint16_t*>(b + p.xp);
+    const int64_t n = d.T * d.H, blocks = (n / 4 + 255) / 256;
+    hipLaunchKernelGGL(k_rd_split_x, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256),
+                       0, st, static_cast<const float*>(x), n, parts);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    xp = parts;
+  }
+  float* out = p.parts > 1 ? reinterpret_cast<float*>(b + p.part) : dw;
+  if (d.act == MOE_F32) launch_dw<3>(p, d, zp, xp, out, st);
+  else launch_dw<1>(p, d, zp, xp, out, st);
+  if ((e = hipGetLastError()) != hipSuccess || p.parts == 1) return e;
+  const int64_t n = (int64_t)d.E * d.H;
+  hipLaunchKernelGGL(k_rd_join, dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0, st, out,
+                     p.parts, n, dw);
   return hipGetLastError();
 }
 
