@@ -22,6 +22,8 @@
 // N arrive as zeros by the descriptor's range check.  B is the matrix instruction's first
 // operand, so a lane's results lie in one row of C and take one activation scale.  Split over
 // k (few tiles): fp32 partial sums to the workspace, k_fp8_join adds them in order.
+#include <type_traits>
+
 #include "common.h"
 
 namespace moe {
@@ -102,6 +104,8 @@ struct Op<true> {
     return t;
   }
 };
+
+typedef const __attribute__((address_space(4))) float* ConstPtr;
 
 struct GemmArgs {
   const uint8_t *a, *b;
@@ -228,7 +232,10 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_fp8_tile(GemmArgs g) {
     }
   };
   // !kRowB: the scales of the wave's 128-row block (the last one where the wave is past N)
-  const float* sbp = g.sb + min((n0 + wn * (BN / WN)) / 128, (g.N - 1) / 128) * nk;
+  // read through the constant address space: as scalar loads they stay out of the count of
+  // vector loads in flight (as vector loads, each step waited for its own: 2 us a step)
+  const ConstPtr sbp =
+      (ConstPtr)(uintptr_t)(g.sb + min((n0 + wn * (BN / WN)) / 128, (g.N - 1) / 128) * nk);
 
   // this lane's chunks of its row, the same in every sub-tile (the swizzle repeats every 16
   // rows)
@@ -254,9 +261,9 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_fp8_tile(GemmArgs g) {
   for (int j = 0; j < NST - 1; ++j)
     if (k0 + j < k1) stage(k0 + j, j);
   int st = 0;
+  float sw_next = kRowB ? 1.0f : sbp[k0];
   for (int kt = k0; kt < k1; ++kt) {
-    float sw = 1.0f;
-    if (!kRowB) sw = sbp[kt];
+    const float sw = sw_next;
     if (k1 - kt >= NST - 1) wait_vm<(NST - 2) * kPer>();
     else wait_vm<0>();
     __syncthreads();
@@ -279,6 +286,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_fp8_tile(GemmArgs g) {
       }
       __syncthreads();
     }
+    if (!kRowB) sw_next = sbp[min(kt + 1, nk - 1)];
     // The sub-tiles in a software pipeline: while the matrix cores form sub-tile j's partial
     // sum, the vector unit promotes that of sub-tile j - kD + 1 and the codes of the next column
     // group come from LDS.  (Left to the compiler, each promotion waited for its own products
@@ -338,40 +346,182 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_fp8_tile(GemmArgs g) {
 
   // a wave's kT x (BN/WN) outputs of sub-tile row m in LDS (16-byte chunks swizzled by the
   // row), stored back 16 bytes a lane along the rows
-  const bool f32 = g.c_f32 || g.splits > 1;
-  const int es = f32 ? 4 : 2;
-  constexpr int kCols = BN / WN;
-  const int row_bytes = kCols * es, chunks = row_bytes / 16, mask = min(chunks, 16) - 1;
-  char* stg = smem + wv * kT * kCols * 4;
-  char* out = static_cast<char*>(g.c) + (g.splits > 1 ? (int64_t)part * g.M * g.ldc * 4 : 0);
-  const bool vec = g.ldc * es % 16 == 0;
-  const bool add = g.accumulate && g.splits == 1;
+  auto store = [&](auto is_f32) {
+    constexpr bool f32 = decltype(is_f32)::value;
+    constexpr int es = f32 ? 4 : 2, kCols = BN / WN, row_bytes = kCols * es;
+    constexpr int chunks = row_bytes / 16, mask = (chunks < 16 ? chunks : 16) - 1;
+    char* stg = smem + wv * kT * kCols * 4;
+    char* out = static_cast<char*>(g.c) + (g.splits > 1 ? (int64_t)part * g.M * g.ldc * 4 : 0);
+    const bool vec = g.ldc * es % 16 == 0;
+    const bool add = g.accumulate && g.splits == 1;
 #pragma unroll
-  for (int m = 0; m < SM; ++m) {
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    for (int m = 0; m < SM; ++m) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
-    for (int n = 0; n < SN; ++n)
+      for (int n = 0; n < SN; ++n)
 #pragma unroll
-      for (int q = 0; q < O::kR / 4; ++q) {
-        const auto& a = acc[m][n];
-        const int col = kT * n + O::col(lane, 4 * q);  // 4 adjacent columns
-        char* p = stg + fr * row_bytes + (((col * es / 16) ^ (fr & mask)) << 4);
-        if (f32)
-          *reinterpret_cast<float4*>(p) =
-              make_float4(a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]);
-        else
-          *reinterpret_cast<uint2*>(p + (col & 4) * 2) =
-              pack4_bf16(a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]);
+        for (int q = 0; q < O::kR / 4; ++q) {
+          const auto& a = acc[m][n];
+          const int col = kT * n + O::col(lane, 4 * q);  // 4 adjacent columns
+          char* p = stg + fr * row_bytes + (((col * es / 16) ^ (fr & mask)) << 4);
+          if (f32)
+            *reinterpret_cast<float4*>(p) =
+                make_float4(a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]);
+          else
+            *reinterpret_cast<uint2*>(p + (col & 4) * 2) =
+                pack4_bf16(a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]);
+        }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      const int64_t row0 = m0 + wm * (BM / WM) + kT * m;
+#pragma unroll
+      for (int e0 = 0; e0 < kT * chunks; e0 += 64) {
+        const int r = (e0 + lane) / chunks, ch = (e0 + lane) % chunks;
+        const int64_t n = n0 + wn * kCols + ch * (16 / es);
+        const uint4 v =
+            *reinterpret_cast<const uint4*>(stg + r * row_bytes + ((ch ^ (r & mask)) << 4));
+        if (row0 + r < g.M && n < g.N)
+          store16(out + ((row0 + r) * g.ldc + n) * es, v, (int)min((int64_t)8, g.N - n), f32, vec,
+                  add);
       }
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    const int64_t row0 = m0 + wm * (BM / WM) + kT * m;
-    for (int e = lane; e < kT * chunks; e += 64) {
-      const int r = e / chunks, ch = e % chunks;
-      const int64_t n = n0 + wn * kCols + ch * (16 / es);
-      const uint4 v = *reinterpret_cast<const uint4*>(stg + r * row_bytes + ((ch ^ (r & mask)) << 4));
-      if (row0 + r < g.M && n < g.N)
-        store16(out + ((row0 + r) * g.ldc + n) * es, v, (int)min((int64_t)8, g.N - n), f32, vec,
-                add);
+    }
+  };
+  if (kWide || g.splits > 1) store(std::true_type());
+  else store(std::false_type());
+}
+
+// Few rows: a workgroup takes 16 columns and every row of A, its 8 waves every 8th block of k
+// each, with the codes of kU blocks on their way from memory straight into registers, and they
+// add their sums in LDS, in order.  B is read once in all, A once a workgroup (from the L2): the
+// form is bound by B's bytes, or by latency, until A's rows weigh more.  B is the first
+// operand of the 16 x 16 products: a lane holds row l%16 of A and columns 4 (l/16) .. +3 of B,
+// and chunks l/16 and l/16 + 4 of a row's block of codes.
+template <bool kWide>
+__device__ __forceinline__ f32x4 mul16(const u32x4 (&b)[2], const u32x4 (&a)[2]) {
+  f32x4 t = {0.0f, 0.0f, 0.0f, 0.0f};
+  if constexpr (kWide) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+          widen8((int)b[i >> 1][2 * (i & 1)], (int)b[i >> 1][2 * (i & 1) + 1]),
+          widen8((int)a[i >> 1][2 * (i & 1)], (int)a[i >> 1][2 * (i & 1) + 1]), t, 0, 0, 0);
+  } else {
+    i32x8 x, y;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[i] = (int)b[i >> 2][i & 3];
+      y[i] = (int)a[i >> 2][i & 3];
+    }
+    t = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, t, 0, 0, 0, 127, 0, 127);
+  }
+  return t;
+}
+
+// 16 codes at k of a row of K, zeros past K
+__device__ __forceinline__ u32x4 codes_at(const uint8_t* __restrict__ row, int64_t k, int64_t K) {
+  u32x4 v = {0, 0, 0, 0};
+  if (k >= K) return v;
+  v = *reinterpret_cast<const u32x4*>(row + k);
+  const int n = (int)min((int64_t)16, K - k);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (n < 4 * i + 4) v[i] = n > 4 * i ? v[i] & ((1u << (8 * (n - 4 * i))) - 1u) : 0u;
+  return v;
+}
+
+template <int MG, int kU, bool kWide, bool kRowB>
+__global__ __launch_bounds__(512) void k_fp8_rows(GemmArgs g) {
+  constexpr int kW = 8, kM = 16 * MG;
+  __shared__ float s_sum[kW][kM][17];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, q = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int nk = (int)((g.K + GBK - 1) / GBK), whole = (int)(g.K / GBK);
+  // rows past M or N repeat the last one (their results are not stored)
+  const uint8_t* ap[MG];
+  const float *sap[MG], *sbp[4];
+#pragma unroll
+  for (int m = 0; m < MG; ++m) {
+    const int64_t row = min((int64_t)16 * m + r, g.M - 1);
+    ap[m] = g.a + row * g.lda + 16 * q;
+    sap[m] = g.sa + row * nk;
+  }
+  const uint8_t* bp = g.b + min(n0 + r, g.N - 1) * g.ldb + 16 * q;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sbp[i] = g.sb + min(n0 + 4 * q + i, g.N - 1) * (kRowB ? nk : 0);
+  const ConstPtr sbu = (ConstPtr)(uintptr_t)(g.sb + n0 / 128 * nk);  // !kRowB
+  struct Block {
+    u32x4 a[MG][2], b[2];
+    float sa[MG], sb[4];
+  };
+  auto scales = [&](Block& v, int blk) {
+#pragma unroll
+    for (int m = 0; m < MG; ++m) v.sa[m] = sap[m][blk];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v.sb[i] = kRowB ? sbp[i][blk] : i ? v.sb[0] : sbu[blk];
+  };
+  auto load = [&](Block& v, int blk) {  // a whole block
+    const int64_t k = (int64_t)blk * GBK;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      v.b[h] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(bp + k + 64 * h));
+#pragma unroll
+      for (int m = 0; m < MG; ++m) v.a[m][h] = *reinterpret_cast<const u32x4*>(ap[m] + k + 64 * h);
+    }
+    scales(v, blk);
+  };
+  f32x4 acc[MG];
+#pragma unroll
+  for (int m = 0; m < MG; ++m) acc[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  auto add = [&](const Block& v) {
+#pragma unroll
+    for (int m = 0; m < MG; ++m) {
+      const f32x4 t = mul16<kWide>(v.b, v.a[m]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        acc[m][i] = __builtin_fmaf(t[i], v.sa[m] * v.sb[i], acc[m][i]);
+    }
+  };
+  Block v[kU];
+#pragma unroll
+  for (int u = 0; u < kU; ++u)
+    if (wv + kW * u < whole) load(v[u], wv + kW * u);
+  for (int b = wv; b < whole; b += kW * kU)
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int blk = b + kW * u;
+      if (blk >= whole) break;
+      add(v[u]);
+      if (blk + kW * kU < whole) load(v[u], blk + kW * kU);
+    }
+  if (whole < nk && whole % kW == wv) {  // the last, partial block
+    const int64_t k = (int64_t)whole * GBK, left = g.K - k - 16 * q;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      v[0].b[h] = codes_at(bp + k, 64 * h, left);
+#pragma unroll
+      for (int m = 0; m < MG; ++m) v[0].a[m][h] = codes_at(ap[m] + k, 64 * h, left);
+    }
+    scales(v[0], whole);
+    add(v[0]);
+  }
+#pragma unroll
+  for (int m = 0; m < MG; ++m)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s_sum[wv][16 * m + r][4 * q + i] = acc[m][i];
+  __syncthreads();
+  for (int e = tid; e < kM * 16; e += 512) {
+    const int m = e >> 4, n = e & 15;
+    if (m >= g.M || n0 + n >= g.N) continue;
+    float s = s_sum[0][m][n];
+#pragma unroll
+    for (int w = 1; w < kW; ++w) s += s_sum[w][m][n];
+    const int64_t at = m * g.ldc + n0 + n;
+    if (g.c_f32) {
+      float* p = static_cast<float*>(g.c) + at;
+      *p = g.accumulate ? *p + s : s;
+    } else {
+      static_cast<uint16_t*>(g.c)[at] = f32_to_bf16_bits(s);
     }
   }
 }
@@ -420,6 +570,13 @@ int64_t up4(int64_t n) { return (n + 3) / 4 * 4; }
 Plan plan(int64_t M, int64_t N, int64_t K) {
   const int64_t nk = (K + GBK - 1) / GBK;
   Plan p;
+  if (M <= 16 || (M <= 32 && K <= 2048)) {  // k_fp8_rows
+    p.bm = M <= 16 ? 16 : 32;
+    p.bn = 16;
+    p.splits = 1;
+    p.steps = (int)nk;
+    return p;
+  }
   if (M <= 64) { p.bm = 64; p.bn = 128; }
   else if (((M + 255) / 256) * ((N + 255) / 256) >= 192) { p.bm = 256; p.bn = 256; }
   else { p.bm = 128; p.bn = 128; }
@@ -445,6 +602,18 @@ void launch_tile(GemmArgs g, bool row_b, hipStream_t st) {
                        dim3(64 * WM * WN), 0, st, g);
 }
 
+template <int MG, int kU, bool kWide>
+void launch_rows(const GemmArgs& g, bool row_b, hipStream_t st) {
+  const dim3 grid((unsigned)((g.N + 15) / 16));
+  if (row_b) hipLaunchKernelGGL((k_fp8_rows<MG, kU, kWide, true>), grid, dim3(512), 0, st, g);
+  else hipLaunchKernelGGL((k_fp8_rows<MG, kU, kWide, false>), grid, dim3(512), 0, st, g);
+}
+template <bool kWide>
+void launch_rows(const Plan& p, const GemmArgs& g, bool row_b, hipStream_t st) {
+  if (p.bm == 16) launch_rows<1, 4, kWide>(g, row_b, st);
+  else launch_rows<2, 4, kWide>(g, row_b, st);
+}
+
 }  // namespace
 
 size_t gemm_fp8_ws_bytes(int64_t M, int64_t N, int64_t K) {
@@ -463,12 +632,15 @@ hipError_t launch_gemm_fp8(int64_t M, int64_t N, int64_t K, const uint8_t* a, in
     g.ldc = up4(N);
   }
   const bool row_b = b_rows == 1;
-  if (p.bm == 64) {
-    if (c_f32) launch_tile<64, 128, 1, 4, 3, true>(g, row_b, st);
-    else launch_tile<64, 128, 1, 4, 3, false>(g, row_b, st);
+  if (p.bn == 16) {
+    if (c_f32) launch_rows<true>(p, g, row_b, st);
+    else launch_rows<false>(p, g, row_b, st);
+  } else if (p.bm == 64) {
+    if (c_f32) launch_tile<64, 128, 2, 4, 3, true>(g, row_b, st);
+    else launch_tile<64, 128, 2, 4, 3, false>(g, row_b, st);
   } else if (p.bm == 128) {
-    if (c_f32) launch_tile<128, 128, 2, 2, 2, true>(g, row_b, st);
-    else launch_tile<128, 128, 2, 2, 2, false>(g, row_b, st);
+    if (c_f32) launch_tile<128, 128, 4, 2, 2, true>(g, row_b, st);
+    else launch_tile<128, 128, 4, 2, 2, false>(g, row_b, st);
   } else {
     if (c_f32) launch_tile<256, 128, 4, 2, 3, true>(g, row_b, st);
     else launch_tile<256, 256, 4, 2, 2, false>(g, row_b, st);

@@ -6,10 +6,11 @@
 // A code's relative rounding error is at most 2^-4 for values above 2^-6 scale; smaller ones
 // round to multiples of 2^-9 scale.
 // All kernels here are bound by memory: each element is read once and each code written once.
-//   k_quant_rows: 16 lanes take one block of 128 columns, 8 elements a lane.
-//   k_quant_tile: a workgroup takes 128 x 128 elements through LDS, so that the transposed
-//     codes leave as whole 128-byte lines as well.
+//   k_quant_rows: 16 lanes take a block of 128 columns, 8 elements a lane.
+//   k_quant_tile: a workgroup takes 128 x 128 elements through LDS and writes both orders.
 //   k_ckpt_restore: 8 columns of h a lane from the gate and the up codes.
+#include <algorithm>
+
 #include "common.h"
 
 namespace moe {
@@ -58,10 +59,34 @@ __device__ __forceinline__ float amax8(const float* v) {
   return m;
 }
 
+// The rounded quotient v/s of |v| <= 448 s from r = 1/s, rounded: q0 = v r is within an ulp or so
+// of it, and the remainder v - q0 s, exact in one fused operation, corrects it to the nearest
+// (P. Markstein's theorem on division by a rounded reciprocal, IBM J. Res. Dev. 34, 1990).
+// 3 operations in place of the 10 of a division; s is kept away from the ends of the
+// exponent range, where r or the remainder would not be a normal number.
+struct Scale {
+  float s, r;
+  bool plain;
+  __device__ __forceinline__ explicit Scale(float amax) {
+    s = block_scale(amax);
+    r = 1.0f / s;
+    plain = !(s > 0x1p-100f && s < 0x1p100f);
+  }
+  __device__ __forceinline__ float of(float v) const {
+    const float q = v * r;
+    return __builtin_fmaf(__builtin_fmaf(-q, s, v), r, q);
+  }
+  __device__ __forceinline__ uint32_t codes(float a, float b, float c, float d) const {
+    if (plain) return pack4_e4m3(a / s, b / s, c / s, d / s);
+    return pack4_e4m3(of(a), of(b), of(c), of(d));
+  }
+};
+
 // the codes of v/s to q, whose first n bytes are the row's
-__device__ __forceinline__ void write8(uint8_t* __restrict__ q, int n, const float* v, float s) {
-  const uint32_t a = pack4_e4m3(v[0] / s, v[1] / s, v[2] / s, v[3] / s);
-  const uint32_t b = pack4_e4m3(v[4] / s, v[5] / s, v[6] / s, v[7] / s);
+__device__ __forceinline__ void write8(uint8_t* __restrict__ q, int n, const float* v,
+                                       const Scale& s) {
+  const uint32_t a = s.codes(v[0], v[1], v[2], v[3]);
+  const uint32_t b = s.codes(v[4], v[5], v[6], v[7]);
   if (n >= 8) {
     *reinterpret_cast<uint2*>(q) = make_uint2(a, b);
   } else {
@@ -71,31 +96,75 @@ __device__ __forceinline__ void write8(uint8_t* __restrict__ q, int n, const flo
   }
 }
 
-template <typename T, bool kVec>
+// kU adjacent blocks of 128 columns per 16 lanes and turn, their loads ahead of their codes
+template <typename T, bool kVec, int kU>
 __global__ __launch_bounds__(256) void k_quant_rows(const T* __restrict__ x, int64_t rows,
                                                     int64_t cols, int64_t ldx,
                                                     uint8_t* __restrict__ q, int64_t ldq,
                                                     float* __restrict__ scale, int64_t kb) {
   const int l = threadIdx.x & 15;
-  const int64_t stride = (int64_t)gridDim.x * 16;
-  for (int64_t g = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4); g < rows * kb; g += stride) {
-    const int64_t r = g / kb, b = g - r * kb;
-    const int64_t c = b * kQB + 8 * l;
-    const int n = (int)max((int64_t)0, min((int64_t)8, cols - c));
-    float v[8];
-    read8<kVec>(x + r * ldx + c, n, v);
-    float m = amax8(v);
+  const int64_t total = rows * kb, stride = (int64_t)gridDim.x * 16 * kU;
+  for (int64_t g0 = ((int64_t)blockIdx.x * 16 + (threadIdx.x >> 4)) * kU; g0 < total;
+       g0 += stride) {
+    float v[kU][8];
+    int64_t r[kU], b[kU];
+    int n[kU];
+    r[0] = (uint64_t)total >> 32 ? g0 / kb : (int64_t)((uint32_t)g0 / (uint32_t)kb);
+    b[0] = g0 - r[0] * kb;
 #pragma unroll
-    for (int o = 8; o >= 1; o >>= 1) m = __builtin_fmaxf(m, __shfl_xor(m, o));
-    const float s = block_scale(m);
-    write8(q + r * ldq + c, n, v, s);
-    if (l == 0) scale[r * kb + b] = s;
+    for (int u = 1; u < kU; ++u) {
+      const bool next = b[u - 1] + 1 == kb;
+      r[u] = r[u - 1] + (next ? 1 : 0);
+      b[u] = next ? 0 : b[u - 1] + 1;
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int64_t c = b[u] * kQB + 8 * l;
+      n[u] = r[u] < rows ? (int)max((int64_t)0, min((int64_t)8, cols - c)) : 0;
+      read8<kVec>(x + r[u] * ldx + c, n[u], v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      float m = amax8(v[u]);
+#pragma unroll
+      for (int o = 8; o >= 1; o >>= 1) m = __builtin_fmaxf(m, __shfl_xor(m, o));
+      const Scale s(m);
+      write8(q + r[u] * ldq + b[u] * kQB + 8 * l, n[u], v[u], s);
+      if (l == 0 && r[u] < rows) scale[r[u] * kb + b[u]] = s.s;
+    }
   }
 }
 
-// 128 x 128 elements a workgroup.  Rows: 16 lanes a row, 8 elements a lane.  Columns: 8 lanes
-// a column, 16 rows a lane, read from LDS.
-constexpr int kTileLd = kQB + 1;
+// 128 x 128 elements a workgroup.  Rows: 16 lanes a row, 8 elements a lane, which also go to
+// LDS as they are.  Columns: lane l of wave w takes columns 2 l and 2 l + 1 of rows 32 w .. +31
+// (a wave reads whole rows, without bank conflicts), and the waves' maxima meet in LDS.
+template <typename T>
+struct Pair;
+template <>
+struct Pair<uint16_t> {
+  typedef uint32_t type;
+  static __device__ __forceinline__ float lo(uint32_t p) { return __uint_as_float(p << 16); }
+  static __device__ __forceinline__ float hi(uint32_t p) { return __uint_as_float(p & 0xFFFF0000u); }
+};
+template <>
+struct Pair<float> {
+  typedef float2 type;
+  static __device__ __forceinline__ float lo(const float2& p) { return p.x; }
+  static __device__ __forceinline__ float hi(const float2& p) { return p.y; }
+};
+__device__ __forceinline__ void keep8(uint16_t* p, const float* v) {  // exact: v came as bf16
+  uint4 o;
+  uint32_t* w = reinterpret_cast<uint32_t*>(&o);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = __float_as_uint(v[2 * i]) >> 16 | (__float_as_uint(v[2 * i + 1]) & 0xFFFF0000u);
+  *reinterpret_cast<uint4*>(p) = o;
+}
+__device__ __forceinline__ void keep8(float* p, const float* v) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+
 template <typename T, bool kVec>
 __global__ __launch_bounds__(256) void k_quant_tile(const T* __restrict__ x, int64_t rows,
                                                     int64_t cols, int64_t ldx,
@@ -103,60 +172,72 @@ __global__ __launch_bounds__(256) void k_quant_tile(const T* __restrict__ x, int
                                                     float* __restrict__ scale, int64_t kb,
                                                     uint8_t* __restrict__ qt, int64_t ldqt,
                                                     float* __restrict__ scale_t, int64_t kbt) {
-  __shared__ float tile[kQB * kTileLd];
+  typedef Pair<T> P;
+  __shared__ __attribute__((aligned(16))) T tile[kQB * kQB];
+  __shared__ float s_m[4][kQB];
   const int tid = threadIdx.x, l = tid & 15;
   const int64_t rb = blockIdx.x / kb, cb = blockIdx.x - rb * kb;
   const int64_t r0 = rb * kQB, c0 = cb * kQB;
   const int n = (int)max((int64_t)0, min((int64_t)8, cols - c0 - 8 * l));
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int rr = 16 * i + (tid >> 4);
-    const int64_t r = r0 + rr;
-    float v[8];
-    read8<kVec>(x + r * ldx + c0 + 8 * l, r < rows ? n : 0, v);
-    if (q) {
-      float m = amax8(v);
+  for (int h = 0; h < 2; ++h) {
+    float v[4][8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t r = r0 + 64 * h + 16 * i + (tid >> 4);
+      read8<kVec>(x + r * ldx + c0 + 8 * l, r < rows ? n : 0, v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int rr = 64 * h + 16 * i + (tid >> 4);
+      const int64_t r = r0 + rr;
+      keep8(tile + rr * kQB + 8 * l, v[i]);
+      if (!q) continue;
+      float m = amax8(v[i]);
 #pragma unroll
       for (int o = 8; o >= 1; o >>= 1) m = __builtin_fmaxf(m, __shfl_xor(m, o));
-      const float s = block_scale(m);
       if (r < rows) {
-        write8(q + r * ldq + c0 + 8 * l, n, v, s);
-        if (l == 0) scale[r * kb + cb] = s;
+        const Scale s(m);
+        write8(q + r * ldq + c0 + 8 * l, n, v[i], s);
+        if (l == 0) scale[r * kb + cb] = s.s;
       }
     }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) tile[rr * kTileLd + 8 * l + k] = v[k];
   }
   __syncthreads();
-  const int g = tid & 7;
-  const int nr = (int)max((int64_t)0, min((int64_t)16, rows - r0 - 16 * g));
+  const int lane = tid & 63, wv = tid >> 6;
+  typename P::type v[32];
+  float m0 = 0.0f, m1 = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int cc = 32 * i + (tid >> 3);
-    float v[16], m = 0.0f;
+  for (int k = 0; k < 32; ++k) {
+    v[k] = *reinterpret_cast<const typename P::type*>(tile + (32 * wv + k) * kQB + 2 * lane);
+    m0 = __builtin_fmaxf(m0, __builtin_fabsf(P::lo(v[k])));
+    m1 = __builtin_fmaxf(m1, __builtin_fabsf(P::hi(v[k])));
+  }
+  *reinterpret_cast<float2*>(&s_m[wv][2 * lane]) = make_float2(m0, m1);
+  __syncthreads();
+  const int nr = (int)max((int64_t)0, min((int64_t)32, rows - r0 - 32 * wv));
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      v[k] = tile[(16 * g + k) * kTileLd + cc];
-      m = __builtin_fmaxf(m, __builtin_fabsf(v[k]));
-    }
-#pragma unroll
-    for (int o = 4; o >= 1; o >>= 1) m = __builtin_fmaxf(m, __shfl_xor(m, o));
-    const float s = block_scale(m);
+  for (int h = 0; h < 2; ++h) {
+    const int cc = 2 * lane + h;
     const int64_t c = c0 + cc;
     if (c >= cols) continue;
-    uint8_t* p = qt + c * ldqt + r0 + 16 * g;
-    uint32_t w[4];
+    const Scale s(__builtin_fmaxf(__builtin_fmaxf(s_m[0][cc], s_m[1][cc]),
+                                  __builtin_fmaxf(s_m[2][cc], s_m[3][cc])));
+    uint32_t w[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      w[k] = pack4_e4m3(v[4 * k] / s, v[4 * k + 1] / s, v[4 * k + 2] / s, v[4 * k + 3] / s);
-    if (nr == 16) {
-      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int k = 0; k < 8; ++k)
+      w[k] = h ? s.codes(P::hi(v[4 * k]), P::hi(v[4 * k + 1]), P::hi(v[4 * k + 2]), P::hi(v[4 * k + 3]))
+               : s.codes(P::lo(v[4 * k]), P::lo(v[4 * k + 1]), P::lo(v[4 * k + 2]), P::lo(v[4 * k + 3]));
+    uint8_t* p = qt + c * ldqt + r0 + 32 * wv;
+    if (nr == 32) {
+      reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
     } else {
 #pragma unroll
-      for (int k = 0; k < 16; ++k)
+      for (int k = 0; k < 32; ++k)
         if (k < nr) p[k] = (uint8_t)(w[k >> 2] >> (8 * (k & 3)));
     }
-    if (g == 0) scale_t[c * kbt + rb] = s;
+    if (wv == 0) scale_t[c * kbt + rb] = s.s;
   }
 }
 
@@ -227,10 +308,14 @@ hipError_t quantize(const T* x, int64_t rows, int64_t cols, int64_t ldx, uint8_t
     hipLaunchKernelGGL(k, dim3((unsigned)(kb * kbt)), dim3(256), 0, st, x, rows, cols, ldx, q,
                        ldq, scale, kb, qt, ldqt, scale_t, kbt);
   } else {
-    auto k = vec ? k_quant_rows<T, true> : k_quant_rows<T, false>;
-    const int64_t blocks = (rows * kb + 15) / 16;
-    hipLaunchKernelGGL(k, dim3((unsigned)(blocks < (1 << 20) ? blocks : (1 << 20))), dim3(256), 0,
-                       st, x, rows, cols, ldx, q, ldq, scale, kb);
+    // 4 blocks a turn once that leaves every CU 8 workgroups
+    const int64_t groups = (rows * kb + 15) / 16;
+    const bool four = groups > 4 * 2048;
+    const int64_t blocks = std::min<int64_t>(four ? (groups + 3) / 4 : groups, 1 << 20);
+    auto k = four ? (vec ? k_quant_rows<T, true, 4> : k_quant_rows<T, false, 4>)
+                  : (vec ? k_quant_rows<T, true, 1> : k_quant_rows<T, false, 1>);
+    hipLaunchKernelGGL(k, dim3((unsigned)blocks), dim3(256), 0, st, x, rows, cols, ldx, q, ldq,
+                       scale, kb);
   }
   return hipGetLastError();
 }

@@ -89,6 +89,42 @@ def test_quantize_small_values():
     assert bool(((v - x).abs() <= 2 ** -4 * x + 1e-44).all())
 
 
+def test_quantize_next_to_ties():
+    """Values whose quotient by the scale lies on or within two steps of the middle between two
+    codes: the codes are those of the correctly rounded quotient, as everywhere."""
+    from mixture_experts_layer_added_amd import _lib as L
+    codes = torch.arange(0, 0x7f, dtype=torch.uint8).view(F8).float()
+    ties = (codes[1:] + codes[:-1]) / 2  # exact: 5 significant bits
+    g = torch.Generator().manual_seed(1)
+    n = 20000
+    amax = (torch.rand((n, 1), generator=g) + 0.5) * 2.0 ** torch.randint(-60, 60, (n, 1),
+                                                                          generator=g)
+    pick = ties[torch.randint(0, len(ties), (n, 127), generator=g)]
+    x = (pick.double() * (amax / 448).double()).float()
+    for _ in range(2):
+        step = torch.randint(-1, 2, x.shape, generator=g)
+        x = torch.where(step < 0, torch.nextafter(x, torch.zeros(())),
+                        torch.where(step > 0, torch.nextafter(x, torch.full((), 3e38)), x))
+    x = torch.cat([amax, torch.minimum(x, amax)], 1)
+    x *= torch.where(torch.rand(x.shape, generator=g) < 0.5, -1.0, 1.0)
+    q = torch.empty((n, 128), dtype=torch.uint8, device="cuda")
+    s = torch.empty((n, 1), device="cuda")
+    qt = torch.empty((128, up(n, 16)), dtype=torch.uint8, device="cuda")
+    L.moe_quantize_fp8(x.cuda(), L.MOE_F32, n, 128, 128, q, 128, s)
+    torch.cuda.synchronize()
+    ref = codes_of(x)
+    assert torch.equal(s.cpu(), ref[1]) and torch.equal(q.cpu(), ref[0])
+    # the same values down the columns
+    y = x[:128 * (n // 128)].view(-1, 128, 128).transpose(1, 2).reshape(-1, 128).contiguous()
+    m = y.shape[0]
+    st = torch.empty((128, m // 128), device="cuda")
+    L.moe_quantize_fp8(y.cuda(), L.MOE_F32, m, 128, 128, None, 0, None, qt, qt.shape[1], st)
+    torch.cuda.synchronize()
+    ref = codes_of(y.t())
+    assert torch.equal(st.cpu(), ref[1])
+    assert torch.equal(qt[:, :m].cpu(), ref[0])
+
+
 def operand(rows, cols, across, g, ld=None, wild=True):
     """Random codes (finite ones), the pad filled with NaN codes, and scales."""
     ld = up(cols, 16) if ld is None else ld
