@@ -38,7 +38,7 @@ __device__ __forceinline__ float exp_neg(float z) {
 }
 
 __device__ __forceinline__ float clamp80(float z) {
-  return __builtin_fminf(__builtin_fmaxf(z, -80.0f), 80.0f);
+  return __builtin_amdgcn_fmed3f(z, -80.0f, 80.0f);
 }
 
 // first q in [0, n] with off[q + 1] > t (n: none)
@@ -75,14 +75,17 @@ __device__ __forceinline__ float seg_sum(float v) {
   return v;
 }
 
-// LP lanes a token, SL groups of 4 experts a lane (expert 256 j + 4 l + i)
-template <int LP, int SL, bool kVec>
+// LP lanes a token, SL groups of 4 experts a lane (expert 4 LP j + 4 l + i): 16 lanes up to 256
+// experts, so that 4 tokens share each step of a sum across lanes (with 64 lanes a token the
+// backward spent more on those than on its bytes: 146 us at 262,144 tokens and 256 experts)
+// kFull: E = 4 LP SL, no lane's expert is past E
+template <int LP, int SL, bool kVec, bool kFull>
 __global__ __launch_bounds__(256) void k_balance_part(
     const float* __restrict__ z, const int32_t* __restrict__ idx, const int32_t* __restrict__ off,
     int n_seq, int64_t T, int E, int E4, int K, int C, float* __restrict__ part_p,
     int32_t* __restrict__ part_n) {
   constexpr int TPW = 64 / LP, kWaves = 4, kStep = TPW * kWaves;
-  constexpr int U = 4;  // rows in flight per lane group
+  constexpr int U = SL < 4 ? 4 : 2;  // rows in flight per lane group
   __shared__ int hist[kBalMaxE];
   __shared__ float4 s_p[kWaves][LP * SL];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
@@ -114,7 +117,7 @@ __global__ __launch_bounds__(256) void k_balance_part(
         const int64_t tt = t + u * kStep;
 #pragma unroll
         for (int j = 0; j < SL; ++j)
-          v[u][j] = load_row4<kVec>(z + tt * E, 256 * j + 4 * l, tt < hi ? E : 0, -INFINITY);
+          v[u][j] = load_row4<kVec>(z + tt * E, 4 * (LP * j + l), tt < hi ? E : 0, -INFINITY);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -124,8 +127,8 @@ __global__ __launch_bounds__(256) void k_balance_part(
           const float w[4] = {v[u][j].x, v[u][j].y, v[u][j].z, v[u][j].w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            s[j][i] = w[i] == -INFINITY ? 0.0f
-                                        : __builtin_amdgcn_rcpf(1.0f + exp_neg(clamp80(w[i])));
+            s[j][i] = __builtin_amdgcn_rcpf(1.0f + exp_neg(clamp80(w[i])));
+            if (!kFull && w[i] == -INFINITY) s[j][i] = 0.0f;
             sum += s[j][i];
           }
         }
@@ -245,13 +248,13 @@ __global__ __launch_bounds__(1024) void k_balance_seq(
 
 // LP lanes a token as in the forward; a group takes TW consecutive tokens and looks its
 // sequence up once.  gates: dgate != nullptr.
-template <int LP, int SL, bool kVec>
+template <int LP, int SL, bool kVec, bool kFull>
 __global__ __launch_bounds__(256) void k_balance_bwd(
     const float* __restrict__ z, const int32_t* __restrict__ off, int n_seq,
     const int32_t* __restrict__ counts, const float* __restrict__ dloss,
     const int32_t* __restrict__ idx, const float* __restrict__ gate,
     const float* __restrict__ dgate, int64_t T, int E, int K, int TW, float* __restrict__ dz) {
-  constexpr int TPW = 64 / LP;
+  constexpr int TPW = 64 / LP, NK = (kBalMaxK + LP - 1) / LP;
   __shared__ float s_d[4][64 * 4 * SL];
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   const int seg = lane / LP, l = lane % LP;
@@ -264,9 +267,36 @@ __global__ __launch_bounds__(256) void k_balance_bwd(
   for (int j = 0; j < SL; ++j)
 #pragma unroll
     for (int i = 0; i < 4; ++i) cf[j][i] = 0.0f;
+  // the logits and choices of token first + w, loaded a turn ahead
+  float4 row[SL];
+  int ek[NK];
+  float gk[NK], dk[NK];
+  auto choices = [&](int64_t t, int n, int* e, float* g, float* dg) {
+    const int k = n * LP + l;
+    const bool on = t < T && k < K;
+    *e = on ? idx[t * K + k] : -1;
+    *g = on ? gate[t * K + k] : 0.0f;
+    *dg = on ? dgate[t * K + k] : 0.0f;
+  };
+#pragma unroll
+  for (int j = 0; j < SL; ++j)
+    row[j] = load_row4<kVec>(z + first * E, 4 * (LP * j + l), first < T ? E : 0, -INFINITY);
+  if (dgate)
+#pragma unroll
+    for (int n = 0; n < NK; ++n) choices(first, n, &ek[n], &gk[n], &dk[n]);
   for (int w = 0; w < TW; ++w) {
     const int64_t t = first + w;
     const bool live = t < T;
+    float4 next[SL];
+#pragma unroll
+    for (int j = 0; j < SL; ++j)
+      next[j] = load_row4<kVec>(z + (t + 1) * E, 4 * (LP * j + l),
+                                w + 1 < TW && t + 1 < T ? E : 0, -INFINITY);
+    int ek1[NK];
+    float gk1[NK], dk1[NK];
+    if (dgate)
+#pragma unroll
+      for (int n = 0; n < NK; ++n) choices(w + 1 < TW ? t + 1 : T, n, &ek1[n], &gk1[n], &dk1[n]);
     if (live && t >= q_hi && q < n_seq) {
       if (q_hi >= 0) q = seq_after(off, n_seq, t);
       if (q < n_seq) {
@@ -278,25 +308,22 @@ __global__ __launch_bounds__(256) void k_balance_bwd(
         for (int j = 0; j < SL; ++j)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int e = 256 * j + 4 * l + i;
+            const int e = 4 * (LP * j + l) + i;
             cf[j][i] = e < E ? (float)counts[(int64_t)q * E + e] * k : 0.0f;
           }
       }
     }
     const bool in = live && q < n_seq && t >= q_lo;
     float s[SL][4], o[SL][4], sum = 0.0f, dot = 0.0f;  // o = 1 - s, without cancellation
-    bool flat[SL][4];
 #pragma unroll
     for (int j = 0; j < SL; ++j) {
-      const float4 v = load_row4<kVec>(z + t * E, 256 * j + 4 * l, live ? E : 0, -INFINITY);
-      const float x[4] = {v.x, v.y, v.z, v.w};
+      const float x[4] = {row[j].x, row[j].y, row[j].z, row[j].w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float em = exp_neg(clamp80(x[i]));
-        flat[j][i] = x[i] > 80.0f || x[i] < -80.0f;
+        const float c = clamp80(x[i]), em = exp_neg(c);
         const float a = __builtin_amdgcn_rcpf(1.0f + em);
-        s[j][i] = x[i] == -INFINITY ? 0.0f : a;
-        o[j][i] = em * a;
+        s[j][i] = !kFull && x[i] == -INFINITY ? 0.0f : a;
+        o[j][i] = c == x[i] ? em * a : 0.0f;  // 0 where the clamp is flat
         sum += s[j][i];
         dot = __builtin_fmaf(cf[j][i], s[j][i], dot);
       }
@@ -310,59 +337,53 @@ __global__ __launch_bounds__(256) void k_balance_bwd(
     for (int j = 0; j < SL; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        d[j][i] = flat[j][i] || !in ? 0.0f : (cf[j][i] - mean) * inv * (s[j][i] * o[j][i]);
+        d[j][i] = (cf[j][i] - mean) * inv * (s[j][i] * o[j][i]);
     if (dgate) {
-      // the chosen gates' part, placed by expert through the group's LDS row
+      // the chosen gates' part: their logits come from, and their gradients are added to, the
+      // token's row in the group's LDS (LDS operations of a wave run in order)
+      auto put = [&](int j, float a, float b, float c, float e) {
+        *reinterpret_cast<float4*>(sd + 4 * (LP * j + l)) = make_float4(a, b, c, e);
+      };
 #pragma unroll
-      for (int j = 0; j < SL; ++j)
-        *reinterpret_cast<float4*>(sd + 4 * (LP * j + l)) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int j = 0; j < SL; ++j) put(j, row[j].x, row[j].y, row[j].z, row[j].w);
       __builtin_amdgcn_wave_barrier();
-      constexpr int NK = (kBalMaxK + LP - 1) / LP;
-      float a[NK], sl[NK], dg[NK], tot = 0.0f, gd = 0.0f;
-      int ek[NK];
+      float sl[NK], tot = 0.0f, gd = 0.0f;
 #pragma unroll
       for (int n = 0; n < NK; ++n) {
-        const int k = n * LP + l;
-        a[n] = sl[n] = dg[n] = 0.0f;
-        ek[n] = -1;
-        if (live && k < K) {
-          ek[n] = idx[t * K + k];
-          dg[n] = dgate[t * K + k];
-          if (ek[n] >= 0 && ek[n] < E) {
-            const float zz = z[t * E + ek[n]];
-            const float em = exp_neg(clamp80(zz));
-            a[n] = __builtin_amdgcn_rcpf(1.0f + em);
-            sl[n] = zz > 80.0f || zz < -80.0f ? 0.0f : a[n] * (em * a[n]);
-            gd = __builtin_fmaf(gate[t * K + k], dg[n], gd);
-            tot += a[n];
-          } else {
-            ek[n] = -1;
-          }
+        sl[n] = 0.0f;
+        if (ek[n] >= 0 && ek[n] < E) {
+          const float x = sd[ek[n]], c = clamp80(x), em = exp_neg(c);
+          const float a = __builtin_amdgcn_rcpf(1.0f + em);
+          sl[n] = c == x ? a * (em * a) : 0.0f;
+          gd = __builtin_fmaf(gk[n], dk[n], gd);
+          tot += a;
         }
       }
       tot = seg_sum<LP>(tot);
       gd = seg_sum<LP>(gd);
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int j = 0; j < SL; ++j) put(j, d[j][0], d[j][1], d[j][2], d[j][3]);
+      __builtin_amdgcn_wave_barrier();
 #pragma unroll
       for (int n = 0; n < NK; ++n)
-        if (ek[n] >= 0) {
-          const int e = ek[n], j = e >> 8;
-          atomicAdd(sd + 4 * LP * j + (e & 255), (dg[n] - gd) / tot * sl[n]);
-        }
+        if (ek[n] >= 0 && ek[n] < E) atomicAdd(sd + ek[n], (dk[n] - gd) / tot * sl[n]);
       __builtin_amdgcn_wave_barrier();
 #pragma unroll
       for (int j = 0; j < SL; ++j) {
         const float4 g = *reinterpret_cast<const float4*>(sd + 4 * (LP * j + l));
-        d[j][0] += g.x; d[j][1] += g.y; d[j][2] += g.z; d[j][3] += g.w;
+        d[j][0] = g.x; d[j][1] = g.y; d[j][2] = g.z; d[j][3] = g.w;
       }
       __builtin_amdgcn_wave_barrier();
     }
     if (live) {
 #pragma unroll
       for (int j = 0; j < SL; ++j) {
-        const int e = 256 * j + 4 * l;
+        const int e = 4 * (LP * j + l);
         float* p = dz + t * E + e;
         if (kVec) {
-          if (e < E) *reinterpret_cast<float4*>(p) = make_float4(d[j][0], d[j][1], d[j][2], d[j][3]);
+          const f32x4 v = {d[j][0], d[j][1], d[j][2], d[j][3]};
+          if (e < E) __builtin_nontemporal_store(v, reinterpret_cast<f32x4*>(p));
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -370,12 +391,21 @@ __global__ __launch_bounds__(256) void k_balance_bwd(
         }
       }
     }
+#pragma unroll
+    for (int j = 0; j < SL; ++j) row[j] = next[j];
+    if (dgate)
+#pragma unroll
+      for (int n = 0; n < NK; ++n) {
+        ek[n] = ek1[n];
+        gk[n] = gk1[n];
+        dk[n] = dk1[n];
+      }
   }
 }
 
-// tokens per chunk: about 1024 chunks of a large batch (4 per CU), at least 8 tokens
+// tokens per chunk: about 1024 chunks of a large batch (4 per CU), at least 16 tokens
 int chunk_tokens(int64_t T) {
-  int64_t c = 8;
+  int64_t c = 16;
   while (c * 1024 < T) c *= 2;
   return (int)c;
 }
@@ -388,18 +418,22 @@ size_t balance_ws_bytes(const Dims& d, int n_seq) {
   return slots * (size_t)((d.E + 3) / 4 * 4) * 8;
 }
 
-#define BAL_SHAPES(CALL)                        \
-  if (d.E % 4 == 0) {                           \
-    if (d.E <= 16) CALL(4, 1, true);            \
-    else if (d.E <= 32) CALL(8, 1, true);       \
-    else if (d.E <= 64) CALL(16, 1, true);      \
-    else if (d.E <= 128) CALL(32, 1, true);     \
-    else if (d.E <= 256) CALL(64, 1, true);     \
-    else CALL(64, 2, true);                     \
-  } else {                                      \
-    if (d.E <= 64) CALL(16, 1, false);          \
-    else if (d.E <= 256) CALL(64, 1, false);    \
-    else CALL(64, 2, false);                    \
+#define BAL_SHAPES(CALL)                                 \
+  if (d.E % 4 == 0) {                                    \
+    if (d.E <= 16) CALL(4, 1, true, false);              \
+    else if (d.E <= 32) CALL(8, 1, true, false);         \
+    else if (d.E == 64) CALL(16, 1, true, true);         \
+    else if (d.E <= 64) CALL(16, 1, true, false);        \
+    else if (d.E == 128) CALL(16, 2, true, true);        \
+    else if (d.E <= 128) CALL(16, 2, true, false);       \
+    else if (d.E == 256) CALL(16, 4, true, true);        \
+    else if (d.E <= 256) CALL(16, 4, true, false);       \
+    else if (d.E == 512) CALL(32, 4, true, true);        \
+    else CALL(32, 4, true, false);                       \
+  } else {                                               \
+    if (d.E <= 64) CALL(16, 1, false, false);            \
+    else if (d.E <= 256) CALL(16, 4, false, false);      \
+    else CALL(32, 4, false, false);                      \
   }
 
 hipError_t launch_balance_loss(const Dims& d, const float* z, const int32_t* idx,
@@ -409,9 +443,9 @@ hipError_t launch_balance_loss(const Dims& d, const float* z, const int32_t* idx
   const int64_t nch = (d.T + C - 1) / C;
   float* pp = static_cast<float*>(ws);
   int32_t* pn = reinterpret_cast<int32_t*>(pp + (nch + n_seq) * E4);
-#define BAL_PART(LP, SL, V)                                                                     \
-  hipLaunchKernelGGL((k_balance_part<LP, SL, V>), dim3((unsigned)nch), dim3(256), 0, st, z, idx, \
-                     off, n_seq, d.T, d.E, E4, d.K, C, pp, pn)
+#define BAL_PART(LP, SL, V, F)                                                                 \
+  hipLaunchKernelGGL((k_balance_part<LP, SL, V, F>), dim3((unsigned)nch), dim3(256), 0, st, z, \
+                     idx, off, n_seq, d.T, d.E, E4, d.K, C, pp, pn)
   BAL_SHAPES(BAL_PART)
 #undef BAL_PART
   const hipError_t e = hipGetLastError();
@@ -429,8 +463,8 @@ hipError_t launch_balance_bwd(const Dims& d, const float* z, const int32_t* off,
                               const float* gate, const float* dgate, float* dz, hipStream_t st) {
   // consecutive tokens of a lane group: 8 once that leaves every CU its waves
   const int TW = d.T >= 65536 ? 8 : d.T >= 16384 ? 2 : 1;
-#define BAL_BWD(LP, SL, V)                                                                    \
-  hipLaunchKernelGGL((k_balance_bwd<LP, SL, V>),                                              \
+#define BAL_BWD(LP, SL, V, F)                                                                 \
+  hipLaunchKernelGGL((k_balance_bwd<LP, SL, V, F>),                                            \
                      dim3((unsigned)((d.T + 256 / LP * TW - 1) / (256 / LP * TW))), dim3(256), \
                      0, st, z, off, n_seq, counts, dloss, idx, gate, dgate, d.T, d.E, d.K, TW, dz)
   BAL_SHAPES(BAL_BWD)

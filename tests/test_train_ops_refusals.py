@@ -40,8 +40,8 @@ def bad(L, rc, frag, status=None):
 def test_balance_loss(L):
     f = L.lib().moe_balance_loss
     need = L.lib().moe_balance_loss_workspace_bytes(P(L), 3)
-    # 32 chunks of 8 tokens + 3 sequences, 16 experts, two arrays of 4 bytes
-    assert need == (32 + 3) * 16 * 8
+    # 16 chunks of 16 tokens + 3 sequences, 16 experts, two arrays of 4 bytes
+    assert need == (16 + 3) * 16 * 8
     for n in (0, -1, (1 << 24) + 1):
         bad(L, f(P(L), A, A, A, n, A, A, A, A, need, None), "n_seq")
         assert L.lib().moe_balance_loss_workspace_bytes(P(L), n) == 0
