@@ -145,17 +145,17 @@ def _ptrs(call, *tensors):
     on another device than the current one is refused: its address would fault the kernel, or
     the stream would be another device's."""
     import torch
-    here, out = None, []
+    here, out = -1, []
     for t in tensors:
         if t is None or isinstance(t, int):
             out.append(t)
             continue
         at = t.get_device()  # -1: host memory
-        if here is None and at >= 0:
-            here = torch.cuda.current_device()
-        if at < 0 or at != here:
-            raise MoeError(MOE_ERR_INVALID_ARG, call, "a tensor is in host memory" if at < 0 else
-                           f"a tensor is on device {at}, the current device is {here}")
+        if at != here or at < 0:
+            here = torch.cuda.current_device() if at >= 0 else -1
+            if at < 0 or at != here:
+                raise MoeError(MOE_ERR_INVALID_ARG, call, "a tensor is in host memory" if at < 0
+                               else f"a tensor is on device {at}, the current one is {here}")
         if not t.is_contiguous():
             raise MoeError(MOE_ERR_INVALID_ARG, call, "a tensor is not contiguous (pass the row "
                            "stride of the whole buffer where the call takes one)")
@@ -166,7 +166,8 @@ def _ptrs(call, *tensors):
 def _stream(stream):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle without building a Stream object for it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

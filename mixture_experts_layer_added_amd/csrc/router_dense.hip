@@ -13,13 +13,12 @@
 //     products.  fp32 x in three parts as well, and the six products above 2^-24.
 //   k_rd_split: the parts of dz (both kinds) and of W_r, transposed, with their exponents.
 //   k_rd_split_x: the parts of an fp32 x.
-//   k_rd_dx: 128 (or 64) tokens x 128 columns a workgroup; both operands have k innermost, so a
-//     step is 64 of k (128-byte rows, as in the FP8 product), 3 Ep / 64 steps.
-//   k_rd_dw: 128 (or 64) experts x 128 columns, 32 tokens a step; both operands have k outermost
-//     and are read with ds_read_b64_tr_b16 (gemm_bwd.hip).  Split over the tokens; k_rd_join
-//     adds the parts in order.
-#include <type_traits>
-
+//   k_rd_products, 4 waves a workgroup:
+//     dx: 128 (or 64) tokens x 128 columns; both operands have k innermost, so a step is 64 of
+//       k (128-byte rows, as in the FP8 product), 3 Ep / 64 steps.
+//     dW: 128 (or 64) experts x 128 columns, 32 tokens a step (16 for fp32 x); both operands have
+//       k outermost and are read with ds_read_b64_tr_b16 (gemm_bwd.hip).  Split over the
+//       tokens; k_rd_join adds the parts in order.
 #include "common.h"
 
 namespace moe {
@@ -28,8 +27,17 @@ namespace {
 typedef short v4i16 __attribute__((ext_vector_type(4)));
 typedef __attribute__((__vector_size__(8 * sizeof(_Float16)))) _Float16 f16x8;
 
-constexpr int DBN = 128;   // columns of a tile
-constexpr int kWStep = 32; // tokens of a k_rd_dw step
+constexpr int DBN = 128;       // columns of a tile
+constexpr int kRdWaves = 4;    // of a workgroup, 2 x 2
+constexpr int kRdLds = 65536;  // a ring of two stages
+
+struct RdArgs {
+  const uint16_t *zh, *zp, *wh, *xp;
+  const int32_t *ze, *we;
+  float *dx, *dw;  // dw: dW or its partial sums [parts, E, H]
+  int64_t T, part_rows;
+  int H, E, Ep, mt, nt, dw_tiles, dw_blocks;
+};
 
 __device__ __forceinline__ uint16_t f16_bits(_Float16 v) {
   return __builtin_bit_cast(uint16_t, v);
@@ -47,7 +55,9 @@ __device__ __forceinline__ void parts3(float v, uint16_t* p) {
   }
 }
 
-// Blocks 0 .. zb-1: 4 rows of dz each, one a wave.  The rest: 32 columns of W_r each.
+// Blocks 0 .. zb-1: 4 rows of dz each, one a wave, a lane's experts 4 adjacent ones of each 256.
+// The rest: 32 columns of W_r each, 8 threads a column, kW experts a thread.
+template <int kW>
 __global__ __launch_bounds__(256) void k_rd_split(
     const float* __restrict__ dz, const float* __restrict__ w, int64_t T, int H, int E, int Ep,
     int64_t zb, uint16_t* __restrict__ zh, uint16_t* __restrict__ zp, int32_t* __restrict__ ze,
@@ -57,13 +67,21 @@ __global__ __launch_bounds__(256) void k_rd_split(
     const int lane = tid & 63;
     const int64_t t = (int64_t)blockIdx.x * 4 + (tid >> 6);
     if (t >= T) return;
-    constexpr int kMost = 8;  // Ep <= 512
-    float v[kMost], m = 0.0f;
+    constexpr int kG = kW / 32;  // groups of 256 experts
+    float v[kG][4], m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kMost; ++i) {
-      const int e = 64 * i + lane;
-      v[i] = e < E ? dz[t * E + e] : 0.0f;
-      m = __builtin_fmaxf(m, __builtin_fabsf(v[i]));
+    for (int j = 0; j < kG; ++j) {
+      const int e = 256 * j + 4 * lane;
+      if ((E & 3) == 0) {
+        float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (e < E) r = *reinterpret_cast<const float4*>(dz + t * E + e);
+        v[j][0] = r.x; v[j][1] = r.y; v[j][2] = r.z; v[j][3] = r.w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[j][i] = e + i < E ? dz[t * E + e + i] : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = __builtin_fmaxf(m, __builtin_fabsf(v[j][i]));
     }
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) m = __builtin_fmaxf(m, __shfl_xor(m, o));
@@ -71,20 +89,29 @@ __global__ __launch_bounds__(256) void k_rd_split(
     if (lane == 0) ze[t] = ex;
     const int64_t plane = T * Ep;
 #pragma unroll
-    for (int i = 0; i < kMost; ++i) {
-      const int e = 64 * i + lane;
+    for (int j = 0; j < kG; ++j) {
+      const int e = 256 * j + 4 * lane;
       if (e >= Ep) break;
-      const float s = __builtin_ldexpf(v[i], ex);
-      const _Float16 hi = (_Float16)s;
-      uint16_t p[3];
-      parts3(v[i], p);
-      uint16_t* q = zh + t * Ep + e;
-      q[0] = f16_bits(hi);
-      q[plane] = f16_bits((_Float16)(s - (float)hi));
-      q = zp + t * Ep + e;
-      q[0] = p[0];
-      q[plane] = p[1];
-      q[2 * plane] = p[2];
+      uint32_t hi[2], lo[2], b[3][2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float s = __builtin_ldexpf(v[j][i], ex);
+        const _Float16 h = (_Float16)s;
+        const uint32_t hb = f16_bits(h), lb = f16_bits((_Float16)(s - (float)h));
+        uint16_t p[3];
+        parts3(v[j][i], p);
+        const int k = i >> 1, sh = 16 * (i & 1);
+        hi[k] = i & 1 ? hi[k] | hb << sh : hb;
+        lo[k] = i & 1 ? lo[k] | lb << sh : lb;
+#pragma unroll
+        for (int n = 0; n < 3; ++n) b[n][k] = i & 1 ? b[n][k] | (uint32_t)p[n] << sh : p[n];
+      }
+      const int64_t at = t * Ep + e;
+      *reinterpret_cast<uint2*>(zh + at) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(zh + plane + at) = make_uint2(lo[0], lo[1]);
+#pragma unroll
+      for (int n = 0; n < 3; ++n)
+        *reinterpret_cast<uint2*>(zp + n * plane + at) = make_uint2(b[n][0], b[n][1]);
     }
     return;
   }
@@ -92,20 +119,24 @@ __global__ __launch_bounds__(256) void k_rd_split(
   __shared__ uint32_t s_t[32][65];  // hi | lo << 16 of 32 columns x 64 experts
   const int c = tid & 31, g = tid >> 5;
   const int h0 = (int)(blockIdx.x - zb) * 32;
-  float m = 0.0f;
-  for (int e = g; e < E; e += 8) m = __builtin_fmaxf(m, __builtin_fabsf(w[(int64_t)e * H + h0 + c]));
+  float v[kW], m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kW; ++i) v[i] = 8 * i + g < E ? w[(int64_t)(8 * i + g) * H + h0 + c] : 0.0f;
+#pragma unroll
+  for (int i = 0; i < kW; ++i) m = __builtin_fmaxf(m, __builtin_fabsf(v[i]));
   s_m[g][c] = m;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = __builtin_fmaxf(m, s_m[i][c]);
   const int ex = lift(m);
   if (g == 0) we[h0 + c] = ex;
-  for (int e0 = 0; e0 < Ep; e0 += 64) {
+#pragma unroll
+  for (int e0 = 0; e0 < 8 * kW; e0 += 64) {
+    if (e0 >= Ep) break;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int e = e0 + 8 * i + g;
-      const float s = e < E ? __builtin_ldexpf(w[(int64_t)e * H + h0 + c], ex) : 0.0f;
+      const float s = __builtin_ldexpf(v[e0 / 8 + i], ex);
       const _Float16 hi = (_Float16)s;
       s_t[c][8 * i + g] = f16_bits(hi) | (uint32_t)f16_bits((_Float16)(s - (float)hi)) << 16;
     }
@@ -154,22 +185,21 @@ __device__ __forceinline__ void band_tile(int tile, int mt, int nt, int* m, int*
 // 16-byte chunk c of a 128-byte row r
 __device__ __forceinline__ int at128(int r, int c) { return r * 128 + ((c ^ (r >> 1)) & 7) * 16; }
 
-// dx: k runs over 3 Ep: (hi, hi), (lo, hi), (hi, lo) of (dz, W_r).  4 waves of (BM/WM) x
-// (128/WN) outputs; the W_r part is the first operand, so a lane's results lie in one row.
-template <int BM, int WM, int WN>
-__global__ __launch_bounds__(256, 1) void k_rd_dx(const uint16_t* __restrict__ zh,
-                                                  const int32_t* __restrict__ ze,
-                                                  const uint16_t* __restrict__ wh,
-                                                  const int32_t* __restrict__ we,
-                                                  float* __restrict__ dx, int64_t T, int H, int Ep,
-                                                  int mt, int nt) {
-  constexpr int W = 4, NST = 2, SM = BM / WM / 32, SN = DBN / WN / 32;
+// dx: k runs over 3 Ep: (hi, hi), (lo, hi), (hi, lo) of (dz, W_r).  The W_r part is the first
+// operand, so a lane's results lie in one row.
+template <int BM>
+__device__ __forceinline__ void rd_dx(char* smem, int block, const uint16_t* __restrict__ zh,
+                                      const int32_t* __restrict__ ze,
+                                      const uint16_t* __restrict__ wh,
+                                      const int32_t* __restrict__ we, float* __restrict__ dx,
+                                      int64_t T, int H, int Ep, int mt, int nt) {
+  constexpr int W = kRdWaves, WM = 2, WN = 2, SM = BM / WM / 32, SN = DBN / WN / 32;
   constexpr int kStage = (BM + DBN) * 128, NA = BM / 8 / W, NB = DBN / 8 / W;
-  static_assert(W * 32 * (DBN / WN) * 4 <= NST * kStage, "output staging fits the ring");
-  __shared__ __attribute__((aligned(1024))) char smem[NST * kStage];
+  static_assert(2 * kStage <= kRdLds, "the ring fits");
+  static_assert(W * 32 * (DBN / WN) * 4 <= 2 * kStage, "output staging fits the ring");
   const int total = mt * nt, per = (total + kXcds - 1) / kXcds;
-  const int work = (blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
-  if (blockIdx.x / kXcds >= per || work >= total) return;
+  const int work = (block % kXcds) * per + block / kXcds;
+  if (block / kXcds >= per || work >= total) return;
   int mi, ni;
   band_tile(work, mt, nt, &mi, &ni);
   const int64_t m0 = (int64_t)mi * BM;
@@ -281,20 +311,21 @@ __device__ __forceinline__ bf16x8 ko_frag(uint32_t addr) {
   return f;
 }
 
-// dW partial sums over the tokens of part blockIdx.y: BM experts x 128 columns a workgroup, 4
-// waves as WM x WN.  XP parts of x: 1 (bf16 x itself) or 3.
-template <int BM, int WM, int WN, int XP>
-__global__ __launch_bounds__(256, 1) void k_rd_dw(const uint16_t* __restrict__ zp,
-                                                  const uint16_t* __restrict__ xp,
-                                                  float* __restrict__ out, int64_t T, int H, int E,
-                                                  int Ep, int64_t part_rows, int nt) {
-  constexpr int W = 4, NST = 2, SM = BM / WM / 32, SN = DBN / WN / 32;
-  constexpr int kZ = kWStep * kORow;       // a plane of a stage: 8 KiB (BM = 64: half used)
+// dW partial sums over the tokens of a part: BM experts x 128 columns a workgroup.  XP parts of
+// x: 1 (bf16 x itself) or 3.
+template <int BM, int XP>
+__device__ __forceinline__ void rd_dw(char* smem, int tile, int part,
+                                      const uint16_t* __restrict__ zp,
+                                      const uint16_t* __restrict__ xp, float* __restrict__ out,
+                                      int64_t T, int H, int E, int Ep, int64_t part_rows, int nt) {
+  constexpr int W = kRdWaves, WM = 2, WN = 2, SM = BM / WM / 32, SN = DBN / WN / 32;
+  constexpr int kWStep = XP == 1 ? 32 : 16;  // tokens of a step
+  constexpr int kZ = kWStep * kORow;         // a plane of a stage (BM = 64: half used)
   constexpr int kStage = (3 + XP) * kZ;
-  constexpr int kI = kWStep / 4 / W;       // load instructions of a plane and wave
-  __shared__ __attribute__((aligned(1024))) char smem[NST * kStage];
-  const int mi = blockIdx.x / nt, n0 = (blockIdx.x % nt) * DBN;
-  const int64_t t0 = (int64_t)blockIdx.y * part_rows, t1 = min(t0 + part_rows, T);
+  constexpr int kI = kWStep / 4 / W;         // load instructions of a plane and wave
+  static_assert(2 * kStage <= kRdLds, "the ring fits");
+  const int mi = tile / nt, n0 = (tile % nt) * DBN;
+  const int64_t t0 = (int64_t)part * part_rows, t1 = min(t0 + part_rows, T);
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wv / WN, wn = wv % WN;
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(smem));
@@ -375,10 +406,24 @@ __global__ __launch_bounds__(256, 1) void k_rd_dw(const uint16_t* __restrict__ z
     for (int i = 0; i < 16; ++i) {
       const int e = mi * BM + wm * (BM / WM) + 32 * m + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3);
       if (e >= E) continue;
-      float* p = out + ((int64_t)blockIdx.y * E + e) * H + n0 + wn * (DBN / WN) + (lane & 31);
+      float* p = out + ((int64_t)part * E + e) * H + n0 + wn * (DBN / WN) + (lane & 31);
 #pragma unroll
       for (int n = 0; n < SN; ++n) p[32 * n] = acc[m][n][i];
     }
+}
+
+// Both products in one launch, two workgroups a CU: the first dw_blocks workgroups take dW's
+// tiles and parts, the others dx's tiles, whose stores (most of the bytes) then overlap with
+// products of either.
+template <int BMX, int BMW, int XP>
+__global__ __launch_bounds__(64 * kRdWaves, 1) void k_rd_products(RdArgs g) {
+  __shared__ __attribute__((aligned(1024))) char smem[kRdLds];
+  if ((int)blockIdx.x < g.dw_blocks)
+    rd_dw<BMW, XP>(smem, blockIdx.x % g.dw_tiles, blockIdx.x / g.dw_tiles, g.zp, g.xp, g.dw, g.T,
+                   g.H, g.E, g.Ep, g.part_rows, g.nt);
+  else
+    rd_dx<BMX>(smem, blockIdx.x - g.dw_blocks, g.zh, g.ze, g.wh, g.we, g.dx, g.T, g.H, g.Ep, g.mt,
+               g.nt);
 }
 
 __global__ __launch_bounds__(256) void k_rd_join(const float* __restrict__ part, int parts,
@@ -404,13 +449,13 @@ RdPlan rd_plan(const Dims& d) {
   RdPlan p;
   p.bm = d.E <= 64 ? 64 : 128;
   p.Ep = (d.E + p.bm - 1) / p.bm * p.bm;
-  // about two workgroups a CU, parts of at least 8 steps
+  // about two workgroups a CU, parts of at least 256 tokens
   const int64_t tiles = (int64_t)(p.Ep / p.bm) * (d.H / DBN);
-  const int64_t steps = (d.T + kWStep - 1) / kWStep;
+  const int64_t steps = (d.T + 31) / 32;
   int64_t s = 512 / tiles;
   if (s > steps / 8) s = steps / 8;
   if (s < 1) s = 1;
-  p.part_rows = (steps + s - 1) / s * kWStep;
+  p.part_rows = (steps + s - 1) / s * 32;
   p.parts = (int)((d.T + p.part_rows - 1) / p.part_rows);
   size_t at = 0;
   auto take = [&](size_t n) {
@@ -430,17 +475,24 @@ RdPlan rd_plan(const Dims& d) {
   return p;
 }
 
-template <int XP>
-void launch_dw(const RdPlan& p, const Dims& d, const uint16_t* zp, const uint16_t* xp, float* out,
-               hipStream_t st) {
-  const int nt = d.H / DBN;
-  const dim3 g((unsigned)(p.Ep / p.bm * nt), (unsigned)p.parts);
-  if (p.bm == 64)
-    hipLaunchKernelGGL((k_rd_dw<64, 2, 2, XP>), g, dim3(256), 0, st, zp, xp, out, d.T, d.H, d.E,
-                       p.Ep, p.part_rows, nt);
-  else
-    hipLaunchKernelGGL((k_rd_dw<128, 2, 2, XP>), g, dim3(256), 0, st, zp, xp, out, d.T, d.H, d.E,
-                       p.Ep, p.part_rows, nt);
+template <int BMX, int BMW, int XP>
+void launch_products(RdArgs& g, int parts, hipStream_t st) {
+  g.mt = (int)((g.T + BMX - 1) / BMX);
+  g.dw_tiles = g.Ep / BMW * g.nt;
+  g.dw_blocks = g.dw_tiles * parts;
+  const int dx_blocks = (g.mt * g.nt + kXcds - 1) / kXcds * kXcds;
+  hipLaunchKernelGGL((k_rd_products<BMX, BMW, XP>), dim3(g.dw_blocks + dx_blocks),
+                     dim3(64 * kRdWaves), 0, st, g);
+}
+template <int BMX>
+void launch_products(RdArgs& g, const RdPlan& p, bool f32, hipStream_t st) {
+  if (p.bm == 64) {
+    if (f32) launch_products<BMX, 64, 3>(g, p.parts, st);
+    else launch_products<BMX, 64, 1>(g, p.parts, st);
+  } else {
+    if (f32) launch_products<BMX, 128, 3>(g, p.parts, st);
+    else launch_products<BMX, 128, 1>(g, p.parts, st);
+  }
 }
 
 }  // namespace
@@ -457,24 +509,14 @@ hipError_t launch_router_dense_bwd(const Dims& d, const void* x, const float* w,
   uint16_t* wh = reinterpret_cast<uint16_t*>(b + p.wh);
   int32_t* we = reinterpret_cast<int32_t*>(b + p.we);
   const int64_t zb = (d.T + 3) / 4;
-  hipLaunchKernelGGL(k_rd_split, dim3((unsigned)(zb + d.H / 32)), dim3(256), 0, st, dz, w, d.T,
+  auto split = d.E <= 256 ? k_rd_split<32> : k_rd_split<64>;
+  hipLaunchKernelGGL(split, dim3((unsigned)(zb + d.H / 32)), dim3(256), 0, st, dz, w, d.T,
                      d.H, d.E, p.Ep, zb, zh, zp, ze, wh, we);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int nt = d.H / DBN;
-  const int64_t mt128 = (d.T + 127) / 128;
-  if (mt128 * nt >= 256) {
-    const int per = (int)((mt128 * nt + kXcds - 1) / kXcds);
-    hipLaunchKernelGGL((k_rd_dx<128, 2, 2>), dim3(per * kXcds), dim3(256), 0, st, zh, ze, wh, we,
-                       dx, d.T, d.H, p.Ep, (int)mt128, nt);
-  } else {
-    const int mt = (int)((d.T + 63) / 64), per = (mt * nt + kXcds - 1) / kXcds;
-    hipLaunchKernelGGL((k_rd_dx<64, 2, 2>), dim3(per * kXcds), dim3(256), 0, st, zh, ze, wh, we,
-                       dx, d.T, d.H, p.Ep, mt, nt);
-  }
-  if ((e = hipGetLastError()) != hipSuccess) return e;
   const uint16_t* xp = static_cast<const uint16_t*>(x);
-  if (d.act == MOE_F32) {
+  const bool f32 = d.act == MOE_F32;
+  if (f32) {
     uint16_t* parts = reinterpret_cast<uint16_t*>(b + p.xp);
     const int64_t n = d.T * d.H, blocks = (n / 4 + 255) / 256;
     hipLaunchKernelGGL(k_rd_split_x, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256),
@@ -483,8 +525,10 @@ hipError_t launch_router_dense_bwd(const Dims& d, const void* x, const float* w,
     xp = parts;
   }
   float* out = p.parts > 1 ? reinterpret_cast<float*>(b + p.part) : dw;
-  if (d.act == MOE_F32) launch_dw<3>(p, d, zp, xp, out, st);
-  else launch_dw<1>(p, d, zp, xp, out, st);
+  RdArgs g{zh, zp, wh, xp, ze, we, dx, out, d.T, p.part_rows, d.H, d.E, p.Ep, 0, d.H / DBN, 0, 0};
+  // 128 tokens a tile of dx once that gives every CU one
+  if ((d.T + 127) / 128 * g.nt >= 256) launch_products<128>(g, p, f32, st);
+  else launch_products<64>(g, p, f32, st);
   if ((e = hipGetLastError()) != hipSuccess || p.parts == 1) return e;
   const int64_t n = (int64_t)d.E * d.H;
   hipLaunchKernelGGL(k_rd_join, dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0, st, out,
