@@ -10,13 +10,15 @@
 // The backward joins the gradient of the chosen gates to it (the formula of the router's
 // backward), so a training step reads the logits once for both.
 //
-// Forward, two launches and no atomics on floats (the sums' order is fixed):
+// Forward, two launches (one for a small batch) and no atomics on floats (the sums' order is
+// fixed):
 //   k_balance_part: one workgroup per chunk of C tokens.  A chunk may hold pieces of several
 //     sequences; chunk c's piece of sequence q is slot c + q of the workspace (pieces in
 //     order raise c or q by at least one, so slots do not collide).  Lanes own 4 adjacent
 //     experts each and LP lanes a token, so a wave takes 64/LP tokens at a time; the
 //     shares add up in registers, the choices in an LDS histogram.
 //   k_balance_seq: one workgroup per sequence sums its slots and forms P and the loss.
+// k_balance_short is both for a small batch.
 // Both passes are bound by the logits' bytes.
 #include "common.h"
 
@@ -246,6 +248,82 @@ __global__ __launch_bounds__(1024) void k_balance_seq(
   }
 }
 
+// A small batch (T <= kShort): one workgroup per sequence does all of it, in one launch.
+constexpr int kShort = 512;
+template <int LP, int SL, bool kVec, bool kFull>
+__global__ __launch_bounds__(1024) void k_balance_short(
+    const float* __restrict__ z, const int32_t* __restrict__ idx, const int32_t* __restrict__ off,
+    int64_t T, int E, int K, int32_t* __restrict__ counts, float* __restrict__ prob,
+    float* __restrict__ loss) {
+  constexpr int TPW = 64 / LP, kWaves = 16;
+  __shared__ int hist[4 * LP * SL];
+  __shared__ float s_p[kWaves][4 * LP * SL];
+  __shared__ float s_l[kWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  const int seg = lane / LP, l = lane % LP, q = blockIdx.x;
+  const int64_t lo = max(0, off[q]), hi = min((int64_t)off[q + 1], T), L = hi - lo;
+  for (int e = tid; e < 4 * LP * SL; e += 1024) hist[e] = 0;
+  __syncthreads();
+  for (int64_t i = lo * K + tid; i < hi * K; i += 1024) {
+    const int e = idx[i];
+    if (e >= 0 && e < E) atomicAdd(&hist[e], 1);
+  }
+  float acc[SL][4] = {};
+  for (int64_t t0 = lo + wv * TPW; t0 < hi; t0 += kWaves * TPW) {
+    const int64_t t = t0 + seg;
+    float s[SL][4], sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < SL; ++j) {
+      const float4 v = load_row4<kVec>(z + t * E, 4 * (LP * j + l), t < hi ? E : 0, -INFINITY);
+      const float w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[j][i] = __builtin_amdgcn_rcpf(1.0f + exp_neg(clamp80(w[i])));
+        if (!kFull && w[i] == -INFINITY) s[j][i] = 0.0f;
+        sum += s[j][i];
+      }
+    }
+    sum = seg_sum<LP>(sum);
+    const float inv = t < hi ? __builtin_amdgcn_rcpf(sum) : 0.0f;
+#pragma unroll
+    for (int j = 0; j < SL; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[j][i] = __builtin_fmaf(s[j][i], inv, acc[j][i]);
+  }
+#pragma unroll
+  for (int o = LP; o < 64; o <<= 1)
+#pragma unroll
+    for (int j = 0; j < SL; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[j][i] += __shfl_xor(acc[j][i], o);
+  if (seg == 0)
+#pragma unroll
+    for (int j = 0; j < SL; ++j)
+      *reinterpret_cast<float4*>(&s_p[wv][4 * (LP * j + l)]) =
+          make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+  __syncthreads();
+  const float len = L > 0 ? (float)L : 1.0f;
+  const float per = (float)E / ((float)K * len);
+  float mine = 0.0f;
+  for (int e = tid; e < E; e += 1024) {
+    float p = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) p += s_p[w][e];
+    p /= len;
+    counts[(int64_t)q * E + e] = hist[e];
+    prob[(int64_t)q * E + e] = p;
+    mine = __builtin_fmaf((float)hist[e] * per, p, mine);
+  }
+  mine = seg_sum<64>(mine);
+  if (lane == 0) s_l[wv] = mine;
+  __syncthreads();
+  if (tid == 0) {
+    float v = 0.0f;
+    for (int w = 0; w < kWaves; ++w) v += s_l[w];
+    loss[q] = v;
+  }
+}
+
 // LP lanes a token as in the forward; a group takes TW consecutive tokens and looks its
 // sequence up once.  gates: dgate != nullptr.
 template <int LP, int SL, bool kVec, bool kFull>
@@ -304,12 +382,15 @@ __global__ __launch_bounds__(256) void k_balance_bwd(
         q_hi = off[q + 1];
         const float len = (float)(q_hi - q_lo);
         const float k = dloss[q] * ((float)E / ((float)K * len)) / len;
+        // the counts from the uniform share on, in whole numbers: a constant in c drops out of
+        // c - m, and near balance, where the counts are nearly equal, it would cancel badly
+        const int uniform = (int)((q_hi - q_lo) * K / E);
 #pragma unroll
         for (int j = 0; j < SL; ++j)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int e = 4 * (LP * j + l) + i;
-            cf[j][i] = e < E ? (float)counts[(int64_t)q * E + e] * k : 0.0f;
+            cf[j][i] = e < E ? (float)(counts[(int64_t)q * E + e] - uniform) * k : 0.0f;
           }
       }
     }
@@ -443,6 +524,14 @@ hipError_t launch_balance_loss(const Dims& d, const float* z, const int32_t* idx
   const int64_t nch = (d.T + C - 1) / C;
   float* pp = static_cast<float*>(ws);
   int32_t* pn = reinterpret_cast<int32_t*>(pp + (nch + n_seq) * E4);
+  if (d.T <= kShort) {
+#define BAL_SHORT(LP, SL, V, F)                                                                  \
+  hipLaunchKernelGGL((k_balance_short<LP, SL, V, F>), dim3((unsigned)n_seq), dim3(1024), 0, st, z, \
+                     idx, off, d.T, d.E, d.K, counts, prob, loss)
+    BAL_SHAPES(BAL_SHORT)
+#undef BAL_SHORT
+    return hipGetLastError();
+  }
 #define BAL_PART(LP, SL, V, F)                                                                 \
   hipLaunchKernelGGL((k_balance_part<LP, SL, V, F>), dim3((unsigned)nch), dim3(256), 0, st, z, \
                      idx, off, n_seq, d.T, d.E, E4, d.K, C, pp, pn)

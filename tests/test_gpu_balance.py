@@ -139,12 +139,13 @@ def check(z, idx, off, dgate=None, tag="", seed=5):
                                512])
 def test_expert_counts(E):
     """Every lane layout, expert counts that fill none, and K from 1 to 16."""
-    T, K = 77, min(E, 1 + E % 16)
-    z, idx, dgate = inputs(T, E, K, seed=E)
-    check(z, idx, [0, 40, 40, 77], dgate, f"E={E} K={K}")
+    K = min(E, 1 + E % 16)
+    for T in (77, 600):  # one launch and two
+        z, idx, dgate = inputs(T, E, K, seed=E + T)
+        check(z, idx, [0, 40, 40, T - 9], dgate, f"E={E} K={K} T={T}")
 
 
-@pytest.mark.parametrize("T", [1, 2, 7, 8, 9, 63, 300, 1000, 8193, 17001])
+@pytest.mark.parametrize("T", [1, 2, 7, 8, 9, 63, 300, 512, 513, 1000, 8193, 17001])
 def test_token_counts(T):
     """One token to more than a chunk per compute unit; ragged cuts, empty sequences."""
     E, K = 64, 6
@@ -208,8 +209,9 @@ def test_uniform_loads_give_one():
     T, E, K = 64, 8, 2
     z, _, _ = inputs(T, E, K, seed=9)
     idx = torch.stack([torch.tensor([(2 * t) % E, (2 * t + 1) % E]) for t in range(T)]).int()
-    loss = check(z, idx, [0, T], None, "uniform loads")[2]
+    loss, dz = check(z, idx, [0, T], None, "uniform loads")[2:]
     assert abs(float(loss[0]) - 1) <= (160 + T / 8) * U
+    assert not dz.any()  # every c[e] is the same: nothing to gain
     loss = check(torch.zeros_like(z), torch.zeros_like(idx), [0, T], None, "uniform shares")[2]
     assert abs(float(loss[0]) - 1) <= (160 + T / 8) * U
 
