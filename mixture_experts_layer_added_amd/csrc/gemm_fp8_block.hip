@@ -207,29 +207,30 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_fp8_tile(GemmArgs g) {
     load4_to_lds(sar, lds_sc + ((c & 1) * kScBuf + 64 * q) * 4,
                  (uint32_t)((16 * q + (lane >> 2)) * nk + k) * 4);
   };
-  auto stage = [&](int kt, int st) {
+  // load instruction i (of kPer) of a wave for step kt's stage
+  auto load = [&](int kt, int st, int i) {
     const uint32_t dst = lds0 + st * kStage + 8 * wv * GBK, ko = (uint32_t)kt * GBK;
-#pragma unroll
-    for (int i = 0; i < NA; ++i) load16_to_lds(ar, dst + i * 8 * W * GBK, ao[i] + ko);
-#pragma unroll
-    for (int i = 0; i < NB; ++i)
-      load16_to_lds(br, dst + (BM + i * 8 * W) * GBK, bo[i] + ko);
-    if (kRowB) {  // 64 rows a wave; waves past the last repeat a group
+    if (i < NA) {
+      load16_to_lds(ar, dst + i * 8 * W * GBK, ao[i] + ko);
+    } else if (i < NA + NB) {
+      load16_to_lds(br, dst + (BM + (i - NA) * 8 * W) * GBK, bo[i < NA + NB ? i - NA : 0] + ko);
+    } else if (kRowB) {  // 64 rows' scales a wave; waves past the last repeat a group
       const int q = wv % ((BM + BN) / 64);
       const int row = 64 * (q < BM / 64 ? q : q - BM / 64) + lane;
       load4_to_lds(q < BM / 64 ? sar : sbr, lds_sc + (st * kScBuf + 64 * q) * 4,
                    (uint32_t)(row * nk + kt) * 4);
     } else {
-      const int c = (kt - k0) / kSc, i = (kt - k0) % kSc - (NST - 1);
-#pragma unroll
-      for (int l = 0; l < kL; ++l) {
-        const int q = (i * W + wv) * kL + l;
-        // nothing of the next chunk to load: one of its own again (every wave's count of
-        // loads in flight stays the same)
-        const bool ahead = i >= 0 && q < kG;
-        chunk(ahead ? c + 1 : c, ahead ? q : wv % kG);
-      }
+      const int c = (kt - k0) / kSc, at = (kt - k0) % kSc - (NST - 1);
+      const int q = (at * W + wv) * kL + i - NA - NB;
+      // nothing of the next chunk to load: one of its own again (every wave's count of loads in
+      // flight stays the same)
+      const bool ahead = at >= 0 && q < kG;
+      chunk(ahead ? c + 1 : c, ahead ? q : wv % kG);
     }
+  };
+  auto stage = [&](int kt, int st) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) load(kt, st, i);
   };
   // !kRowB: the scales of the wave's 128-row block (the last one where the wave is past N)
   // read through the constant address space: as scalar loads they stay out of the count of
@@ -258,16 +259,18 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_fp8_tile(GemmArgs g) {
   if (!kRowB)
     for (int q = wv; q < kG; q += W) chunk(0, q);
 #pragma unroll
-  for (int j = 0; j < NST - 1; ++j)
-    if (k0 + j < k1) stage(k0 + j, j);
+  for (int j = 0; j < NST - 1; ++j) stage(k0 + j, j);
+  constexpr int kIssue = SM * SN / 2 > 0 ? SM * SN / 2 : 1;
   int st = 0;
   float sw_next = kRowB ? 1.0f : sbp[k0];
   for (int kt = k0; kt < k1; ++kt) {
     const float sw = sw_next;
-    if (k1 - kt >= NST - 1) wait_vm<(NST - 2) * kPer>();
-    else wait_vm<0>();
+    wait_vm<(NST - 2) * kPer>();
     __syncthreads();
-    if (kt + NST - 1 < k1) stage(kt + NST - 1, st == 0 ? NST - 1 : st - 1);
+    // the loads of step kt + NST - 1 go out between the products below, over the first
+    // kIssue sub-tiles: all at once they hold the waves up for 800 cycles of 4600, the time
+    // that a CU takes to fetch 64 KiB (past the last step they fetch what nothing reads)
+    const int kt_ld = kt + NST - 1, st_ld = st == 0 ? NST - 1 : st - 1;
     if (kt == nk - 1 && (g.K & (GBK - 1))) {  // the last block's codes past K
       const int left = (int)(g.K & (GBK - 1));
       for (int q = tid; q < (BM + BN) * 8; q += 64 * W) {
@@ -334,6 +337,9 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_fp8_tile(GemmArgs g) {
         if (n + 1 < SN) codes(b_at + kT * (n + 1) * GBK, next);
       }
       t[j % O::kD] = O::mul(fb, fa[m]);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (i * kIssue / kPer == j) load(kt_ld, st_ld, i);
       if (j >= O::kD - 1) promote(j - (O::kD - 1));
       __builtin_amdgcn_sched_barrier(0);
     }
