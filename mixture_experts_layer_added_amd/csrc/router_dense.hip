@@ -14,8 +14,8 @@
 //   k_rd_split: the parts of dz (both kinds) and of W_r, transposed, with their exponents.
 //   k_rd_split_x: the parts of an fp32 x.
 //   k_rd_products, 4 waves a workgroup:
-//     dx: 128 (or 64) tokens x 128 columns; both operands have k innermost, so a step is 64 of
-//       k (128-byte rows, as in the FP8 product), 3 Ep / 64 steps.
+//     dx: 128 (or 64) tokens x 128 columns; both operands have k innermost, so a step is 32 of
+//       k, both parts (128-byte rows, as in the FP8 product).
 //     dW: 128 (or 64) experts x 128 columns, 32 tokens a step (16 for fp32 x); both operands have
 //       k outermost and are read with ds_read_b64_tr_b16 (gemm_bwd.hip).  Split over the
 //       tokens; k_rd_join adds the parts in order.
@@ -46,6 +46,9 @@ __device__ __forceinline__ uint16_t f16_bits(_Float16 v) {
 __device__ __forceinline__ int lift(float amax) {
   return amax > 0.0f ? 15 - __builtin_amdgcn_frexp_expf(amax) : 0;
 }
+// Where the fp16 parts of a row's element e stand: 32 hi values, then their 32 lo values, so that
+// 128 bytes of a row hold both parts of 32 of k.
+__device__ __forceinline__ int pair_at(int e) { return (e >> 5) * 64 + (e & 31); }
 // the three bf16 parts of v: each the rounding of what is left
 __device__ __forceinline__ void parts3(float v, uint16_t* p) {
 #pragma unroll
@@ -107,8 +110,9 @@ __global__ __launch_bounds__(256) void k_rd_split(
         for (int n = 0; n < 3; ++n) b[n][k] = i & 1 ? b[n][k] | (uint32_t)p[n] << sh : p[n];
       }
       const int64_t at = t * Ep + e;
-      *reinterpret_cast<uint2*>(zh + at) = make_uint2(hi[0], hi[1]);
-      *reinterpret_cast<uint2*>(zh + plane + at) = make_uint2(lo[0], lo[1]);
+      uint16_t* q = zh + t * 2 * Ep + pair_at(e);
+      *reinterpret_cast<uint2*>(q) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(q + 32) = make_uint2(lo[0], lo[1]);
 #pragma unroll
       for (int n = 0; n < 3; ++n)
         *reinterpret_cast<uint2*>(zp + n * plane + at) = make_uint2(b[n][0], b[n][1]);
@@ -150,9 +154,9 @@ __global__ __launch_bounds__(256) void k_rd_split(
       hi[i] = (a & 0xFFFFu) | b << 16;
       lo[i] = a >> 16 | (b & 0xFFFF0000u);
     }
-    uint16_t* q = wh + (int64_t)(h0 + c2) * Ep + e0 + 8 * l;
+    uint16_t* q = wh + (int64_t)(h0 + c2) * 2 * Ep + pair_at(e0 + 8 * l);
     *reinterpret_cast<uint4*>(q) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4*>(q + (int64_t)H * Ep) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    *reinterpret_cast<uint4*>(q + 32) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
 }
 
@@ -185,8 +189,8 @@ __device__ __forceinline__ void band_tile(int tile, int mt, int nt, int* m, int*
 // 16-byte chunk c of a 128-byte row r
 __device__ __forceinline__ int at128(int r, int c) { return r * 128 + ((c ^ (r >> 1)) & 7) * 16; }
 
-// dx: k runs over 3 Ep: (hi, hi), (lo, hi), (hi, lo) of (dz, W_r).  The W_r part is the first
-// operand, so a lane's results lie in one row.
+// dx: 32 of k a step, hi hi + lo hi + hi lo of (dz, W_r).  The W_r part is the first operand, so
+// a lane's results lie in one row.
 template <int BM>
 __device__ __forceinline__ void rd_dx(char* smem, int block, const uint16_t* __restrict__ zh,
                                       const int32_t* __restrict__ ze,
@@ -208,18 +212,15 @@ __device__ __forceinline__ void rd_dx(char* smem, int block, const uint16_t* __r
   const int wm = wv / WN, wn = wv % WN, fr = lane & 31, kq = lane >> 5;
   const int m_rows = (int)min((int64_t)BM, T - m0);
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(smem));
-  const uint32_t row_b = 2 * Ep;  // bytes of a row of either operand
+  const uint32_t row_b = 4 * Ep;  // bytes of a row of either operand
   const int lrow = 8 * wv + (lane >> 3);
   const uint32_t lchunk = 16 * ((lane & 7) ^ ((4 * (wv & 1) + (lane >> 4)) & 7));
-  const int per_part = Ep / 64, nk = 3 * per_part;
+  const int nk = Ep / 32;
+  // rows past T arrive as zeros
+  const i32x4 ar = buffer_rsrc(zh + m0 * 2 * Ep, m_rows * row_b);
+  const i32x4 br = buffer_rsrc(wh + (int64_t)n0 * 2 * Ep, DBN * row_b);
   auto stage = [&](int kt, int st) {
-    const int part = kt / per_part;
-    const uint32_t ko = (uint32_t)(kt - part * per_part) * 128;
-    // rows past T arrive as zeros
-    const i32x4 ar = buffer_rsrc(zh + (part == 1 ? T * Ep : 0) + m0 * Ep, m_rows * row_b);
-    const i32x4 br = buffer_rsrc(wh + (part == 2 ? (int64_t)H * Ep : 0) + (int64_t)n0 * Ep,
-                                 DBN * row_b);
-    const uint32_t dst = lds0 + st * kStage + 8 * wv * 128;
+    const uint32_t dst = lds0 + st * kStage + 8 * wv * 128, ko = (uint32_t)kt * 128;
 #pragma unroll
     for (int i = 0; i < NA; ++i)
       load16_to_lds(ar, dst + i * 8 * W * 128, (8 * W * i + lrow) * row_b + lchunk + ko);
@@ -242,19 +243,28 @@ __device__ __forceinline__ void rd_dx(char* smem, int block, const uint16_t* __r
     const char* as = smem + (kt & 1) * kStage;
     const char* bs = as + BM * 128;
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      f16x8 a[SM], b[SN];
+    for (int s = 0; s < 2; ++s) {
+      f16x8 a[2][SM], b[2][SN];  // hi, lo
 #pragma unroll
-      for (int m = 0; m < SM; ++m)
-        a[m] = *reinterpret_cast<const f16x8*>(as + at128(wm * (BM / WM) + 32 * m + fr, 2 * s + kq));
+      for (int p = 0; p < 2; ++p) {
 #pragma unroll
-      for (int n = 0; n < SN; ++n)
-        b[n] = *reinterpret_cast<const f16x8*>(bs + at128(wn * (DBN / WN) + 32 * n + fr, 2 * s + kq));
-#pragma unroll
-      for (int m = 0; m < SM; ++m)
+        for (int m = 0; m < SM; ++m)
+          a[p][m] = *reinterpret_cast<const f16x8*>(
+              as + at128(wm * (BM / WM) + 32 * m + fr, 4 * p + 2 * s + kq));
 #pragma unroll
         for (int n = 0; n < SN; ++n)
-          acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(b[n], a[m], acc[m][n], 0, 0, 0);
+          b[p][n] = *reinterpret_cast<const f16x8*>(
+              bs + at128(wn * (DBN / WN) + 32 * n + fr, 4 * p + 2 * s + kq));
+      }
+      // the small products first
+#pragma unroll
+      for (int p = 2; p >= 0; --p)
+#pragma unroll
+        for (int m = 0; m < SM; ++m)
+#pragma unroll
+          for (int n = 0; n < SN; ++n)
+            acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(b[p >> 1][n], a[p & 1][m],
+                                                               acc[m][n], 0, 0, 0);
     }
   }
   __syncthreads();  // every wave is done with the ring, which now stages the output
