@@ -188,8 +188,10 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_fp8_tile(GemmArgs g) {
   const int m_rows = (int)min((int64_t)BM, g.M - m0), n_rows = (int)min((int64_t)BN, g.N - n0);
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(smem));
   const uint32_t lds_sc = __builtin_amdgcn_readfirstlane(lds_offset(&s_sc[0][0]));
-  const i32x4 ar = buffer_rsrc(g.a + m0 * g.lda, (uint32_t)(m_rows * g.lda));
-  const i32x4 br = buffer_rsrc(g.b + n0 * g.ldb, (uint32_t)(n_rows * g.ldb));
+  // a tile's last row ends with its codes: there may be no memory behind it
+  const int64_t k16 = (g.K + 15) / 16 * 16;
+  const i32x4 ar = buffer_rsrc(g.a + m0 * g.lda, (uint32_t)((m_rows - 1) * g.lda + k16));
+  const i32x4 br = buffer_rsrc(g.b + n0 * g.ldb, (uint32_t)((n_rows - 1) * g.ldb + k16));
   // instruction i of wave wv fills rows 8 (i W + wv) .. +7 of the stage (A's, then B's)
   const int lrow = 8 * wv + (lane >> 3);
   const int lchunk = (lane & 7) ^ ((4 * (wv & 1) + (lane >> 4)) & 7);

@@ -207,6 +207,30 @@ def test_strides_and_accumulation(M, N, K):
     near(run(M, N, K, a, sa, b, sb, 1, "bf16", ldc=N + 5), A, B, "bf16")
 
 
+@pytest.mark.parametrize("M", [1, 50, 140, 3500])
+def test_columns_of_wider_operands(M):
+    """The last columns of wider code matrices: behind a last row lies another buffer, here of
+    NaN codes, which no product may take."""
+    from mixture_experts_layer_added_amd import _lib as L
+    N, K, left = 260 if M < 3500 else 3600, 400, 144
+    g = torch.Generator().manual_seed(M)
+    a, sa = operand(M, K, 1, g)
+    b, sb = operand(N, K, 128, g)
+
+    def inside(q):
+        held = torch.full((q.shape[0] * (left + K) + 4096,), 0x7f, dtype=torch.uint8)
+        held[:q.shape[0] * (left + K)].view(q.shape[0], left + K)[:, left:] = q[:, :K]
+        return held.cuda()
+    ad, bd, sad, sbd = inside(a), inside(b), sa.cuda(), sb.cuda()
+    c = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    n = L.moe_gemm_fp8_workspace_bytes(M, N, K)
+    ws = torch.empty((n + 16,), dtype=torch.uint8, device="cuda")
+    L.moe_gemm_fp8(M, N, K, ad[left:], left + K, sad, bd[left:], left + K, sbd, 128, c, N,
+                   L.MOE_BF16, 0, ws, n)
+    torch.cuda.synchronize()
+    assert torch.equal(c.cpu(), run(M, N, K, a, sa, b, sb, 128, "bf16"))
+
+
 def test_largest_codes():
     """Sums of products of the largest codes, 448 x 448, of one sign: nothing overflows before
     its scale."""
