@@ -107,6 +107,7 @@ class Fp8Linear:
 
     def backward(self, dy):
         assert self.train, "construct the layer with train=True"
+        assert self._x is not None, "call forward first"
         M, xt, xt_scale = self._x
         assert dy.dtype == torch.bfloat16 and dy.shape == (M, self.N)
         q, scale, qt, scale_t = quantize_fp8(dy, True, True)
@@ -155,7 +156,8 @@ class MoELayer:
         assert not checkpoint8 or train, "checkpoint8 is for training"
         assert share is None or (checkpoint8 and share.checkpoint8 and share.shape == shape)
         self.checkpoint8 = checkpoint8
-        self._balance = None
+        self._seq_offsets = None  # of the balance loss of the last forward
+        self._buffers = {}
         self.shape = shape
         self.gather = gather
         self.train = train
@@ -235,7 +237,19 @@ class MoELayer:
         t = self.ws[call]
         return t, t.numel()
 
+    def _grown(self, name, n, dtype, stream):
+        """The first n elements of a buffer that is made on its first use, on the stream that
+        uses it, and made larger when n passes it.  Outgrown ones are kept: work that reads
+        them may still be in flight, on whatever stream."""
+        held = self._buffers.setdefault(name, [])
+        if not held or held[-1].numel() < n:
+            size = max(n, 2 * held[-1].numel()) if held else n
+            with torch.cuda.stream(torch.cuda.ExternalStream(L._stream(stream))):
+                held.append(torch.empty((size,), dtype=dtype, device=self.logits.device))
+        return held[-1][:n]
+
     def route(self, x, stream=None):
+        self._seq_offsets = None
         L.moe_route(self.p, x, self.w_router, self.bias, self.topk_idx, self.topk_gate,
                     self.counts, self.logits, None, 0, stream)
 
@@ -309,34 +323,32 @@ class MoELayer:
         on the device -> [n_seq] fp32 (overwritten by the next call with as many sequences).
         Also kept: counts per (sequence, expert) and mean affinity shares in self.seq_counts,
         self.seq_prob.  Its gradient joins the next backward(dy, dseq_loss=...)."""
-        n, E = seq_offsets.numel() - 1, self.shape.E
-        if self._balance is None or self._balance[0] != n:
-            dev, f32 = self.logits.device, torch.float32
-            self._balance = (n, torch.empty((n,), dtype=f32, device=dev), torch.empty(
-                (L.moe_balance_loss_workspace_bytes(self.p, n),), dtype=torch.uint8, device=dev))
-            self.seq_counts = torch.empty((n, E), dtype=torch.int32, device=dev)
-            self.seq_prob = torch.empty((n, E), dtype=f32, device=dev)
-        self._seq_offsets = seq_offsets
-        _, loss, ws = self._balance
+        assert seq_offsets.dtype == torch.int32 and seq_offsets.dim() == 1
+        n, E, f32 = seq_offsets.numel() - 1, self.shape.E, torch.float32
+        need = L.moe_balance_loss_workspace_bytes(self.p, n)
+        ws = self._grown("balance_ws", need, torch.uint8, stream)
+        loss = self._grown("seq_loss", n, f32, stream)
+        self.seq_counts = self._grown("seq_counts", n * E, torch.int32, stream).view(n, E)
+        self.seq_prob = self._grown("seq_prob", n * E, f32, stream).view(n, E)
         L.moe_balance_loss(self.p, self.logits, self.topk_idx, seq_offsets, n, self.seq_counts,
-                           self.seq_prob, loss, ws, ws.numel(), stream)
+                           self.seq_prob, loss, ws, need, stream)
+        self._seq_offsets = seq_offsets
         return loss
 
     def router_backward_dense(self, dseq_loss, stream=None):
         """The router's backward with the balance loss's gradient (dseq_loss [n_seq] fp32, the
         gradient of the sequences' losses) joined to the gates'."""
-        assert self._balance is not None, "call balance_loss first"
+        assert self._seq_offsets is not None, "call balance_loss after the forward first"
+        n_seq = self._seq_offsets.numel() - 1
+        assert dseq_loss.dtype == torch.float32 and dseq_loss.shape == (n_seq,)
         T, E = self.shape.T, self.shape.E
-        if not hasattr(self, "dlogits"):
-            self.dlogits = torch.empty((T, E), dtype=torch.float32, device=self.logits.device)
-            n = L.moe_workspace_bytes(self.p, L.MOE_CALL_ROUTER_BACKWARD_DENSE)
-            self.ws[L.MOE_CALL_ROUTER_BACKWARD_DENSE] = torch.empty(
-                (n,), dtype=torch.uint8, device=self.logits.device)
-        L.moe_balance_loss_backward(self.p, self.logits, self._seq_offsets, self._balance[0],
+        self.dlogits = self._grown("dlogits", T * E, torch.float32, stream).view(T, E)
+        L.moe_balance_loss_backward(self.p, self.logits, self._seq_offsets, n_seq,
                                     self.seq_counts, dseq_loss, self.topk_idx, self.topk_gate,
                                     self.dgate, self.dlogits, stream)
         x = self._x if self.gather else self._xin
-        ws, n = self._ws(L.MOE_CALL_ROUTER_BACKWARD_DENSE)
+        n = L.moe_workspace_bytes(self.p, L.MOE_CALL_ROUTER_BACKWARD_DENSE)
+        ws = self._grown("dense_ws", n, torch.uint8, stream)
         L.moe_router_backward_dense(self.p, x, self.w_router, self.dlogits, self.dx_router,
                                     self.dw_router, ws, n, stream)
 

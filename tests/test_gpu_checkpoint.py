@@ -233,3 +233,39 @@ def test_training_layer(name, gather, packed):
     log(f"    {name} gather={gather}: " + ", ".join(f"{k} {v:.2e}" for k, v in errs.items()))
     for k, v in errs.items():
         assert v <= TOL[w.expert], (k, v)
+
+
+def test_balance_loss_of_changing_sequences():
+    """Batches cut into other sequences step by step, on a stream of their own, have the losses
+    and gradients of a fresh layer; a forward without its balance loss has none to go back
+    through."""
+    from mixture_experts_layer_added_amd.layer import MoELayer
+    w = case("ragged-bf16")
+    inp = make_cpu_inputs(w)
+    dev = {k: v.contiguous().cuda() for k, v in inp.items()}
+    args = (shape_of(w), dev["w_router"], dev["bias"], dev["w13"], dev["w2"])
+    layer = MoELayer(*args, train=True)
+    x, dy = dev["x"], workloads.make_dy(w).cuda()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = []
+    for n in (2, 7, 1, 40, 3):
+        off = torch.linspace(0, w.T, n + 1).to(torch.int32).cuda()
+        dl = torch.linspace(-1, 1, n).cuda()
+        torch.cuda.synchronize()
+        layer.forward(x, stream=side)
+        loss = layer.balance_loss(off, stream=side)
+        layer.backward(dy, stream=side, dseq_loss=dl)
+        with torch.cuda.stream(side):
+            got.append((off, dl, loss.clone(), layer.dw_router.clone(), layer.dx.clone()))
+    torch.cuda.synchronize()
+    for off, dl, loss, dw, dx in got:
+        fresh = MoELayer(*args, train=True)
+        fresh.forward(x)
+        assert torch.equal(fresh.balance_loss(off), loss)
+        fresh.backward(dy, dseq_loss=dl)
+        torch.cuda.synchronize()
+        assert torch.equal(fresh.dw_router, dw) and torch.equal(fresh.dx, dx)
+    layer.forward(x)
+    with pytest.raises(AssertionError, match="balance_loss"):
+        layer.backward(dy, dseq_loss=dl)
