@@ -425,8 +425,8 @@ moe_status moe_quantize_weights_fp8(const void* w_bf16, void* w_fp8, float* scal
  *   seq_counts  [n_seq,E] int32 out: n;  seq_prob [n_seq,E] fp32 out: P;
  *   seq_loss    [n_seq] fp32 out (an empty sequence gets zeros in all three)
  *   ws          >= moe_balance_loss_workspace_bytes(p, n_seq) bytes, 16-byte aligned
- * fp32 sums in a fixed order (bit-for-bit reproducible).  Limits (checked): 1 <= n_seq <=
- * 2^24, n_seq*E < 2^31.  Offsets that break the ordering, or indices outside [0,E) (not
+ * fp32 sums in a fixed order (bit-for-bit reproducible).  Limit (checked): 1 <= n_seq < 2^22.
+ * Offsets that break the ordering, or indices outside [0,E) (not
  * counted), give unspecified values but every write stays inside the outputs. */
 size_t moe_balance_loss_workspace_bytes(const moe_problem* p, int32_t n_seq);
 moe_status moe_balance_loss(const moe_problem* p, const float* logits, const int32_t* topk_idx,
@@ -452,7 +452,10 @@ moe_status moe_balance_loss_backward(const moe_problem* p, const float* logits,
  *   dx_router[t] = sum_e dlogits[t,e] W_r[e]   [T,H] fp32 out,
  *   dw_router[e] = sum_t dlogits[t,e] x[t]     [E,H] fp32 out   (fp32, a fixed order).
  *   dlogits [T,E] fp32, e.g. from moe_balance_loss_backward with dgate
- *   ws      >= moe_workspace_bytes(p, MOE_CALL_ROUTER_BACKWARD_DENSE) bytes, 16-byte aligned */
+ *   ws      >= moe_workspace_bytes(p, MOE_CALL_ROUTER_BACKWARD_DENSE) bytes, 16-byte aligned
+ * The products run on 16-bit matrix instructions over parts of the fp32 operands: an error of
+ * about 2^-22 of a product's terms (2^-40 of its row's largest term where a term is under 2^-17
+ * of that).  Extra limits (checked): T <= 2^25, T*H <= 2^36. */
 moe_status moe_router_backward_dense(const moe_problem* p, const void* x, const float* w_router,
                                      const float* dlogits, float* dx_router, float* dw_router,
                                      void* ws, size_t ws_bytes, void* stream);
@@ -491,7 +494,8 @@ moe_status moe_expert_ffn_backward_input_checkpoint(const moe_problem* p, const 
  *   qt [cols, ldqt] codes, scale_t [cols, ceil(rows/128)]: the transpose, blocks along a column
  *      of x; or both NULL (one of the two forms is required; both come from one read of x)
  * Limits (checked): rows, cols >= 1; ldx >= cols; ldq >= cols and ldqt >= rows, multiples of 16;
- * q, qt 16-byte aligned, x aligned to its element.  Bytes of a row past its codes are not
+ * q, qt 16-byte aligned, x aligned to its element; fewer than 2^31 blocks of 128 x 128, with qt
+ * fewer than 2^24.  Bytes of a row past its codes are not
  * written. */
 moe_status moe_quantize_fp8(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ldx,
                             void* q, int64_t ldq, float* scale, void* qt, int64_t ldqt,
@@ -507,9 +511,12 @@ moe_status moe_quantize_fp8(const void* x, int32_t dtype, int64_t rows, int64_t 
  *   ws >= moe_gemm_fp8_workspace_bytes(M, N, K) bytes, 16-byte aligned (may be NULL if that is 0)
  * A linear layer y = x W^T: a = x by rows, b = W; its gradients: dx = dy W with a = dy by rows,
  * b = W^T; dW = dy^T x with a = dy, b = x, both by columns (moe_quantize_fp8's transposes).
+ * bf16 C: a block's sum of products is the FP8 matrix instruction's, which keeps 13 bits below the
+ * largest of each 8 products; fp32 C: fp32 sums.
  * Any M, N, K >= 1.  Code bytes past K in a row are ignored.  Limits (checked): lda, ldb
- * multiples of 16, >= K and at most 2^22; ldc >= N; M, N < 2^31; a, b, c 16-byte aligned, c
- * apart from a and b; at most 2^31 - 1 tiles of 64 x 64. */
+ * multiples of 16, >= K and at most 2^22; ldc >= N; M, N <= 2^26, M*N <= 2^37; a, b, c 16-byte
+ * aligned, c apart from a and b.  A matrix's last row is read up to K rounded up to 16, the
+ * others may be read up to their stride. */
 size_t moe_gemm_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K);
 moe_status moe_gemm_fp8(int64_t M, int64_t N, int64_t K, const void* a, int64_t lda,
                         const float* a_scale, const void* b, int64_t ldb, const float* b_scale,

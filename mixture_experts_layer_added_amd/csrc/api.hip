@@ -662,9 +662,10 @@ moe_status moe_quantize_weights_fp8(const void* w_bf16, void* w_fp8, float* scal
   return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_quantize_weights_fp8 launch");
 }
 
-static moe_status check_sequences(const Dims& d, int32_t n_seq) {
-  if (n_seq < 1 || n_seq > (1 << 24) || (int64_t)n_seq * d.E >= ((int64_t)1 << 31))
-    return fail(MOE_ERR_INVALID_ARG, "n_seq=%d must be in [1, 2^24] with n_seq*E < 2^31", n_seq);
+static moe_status check_sequences(int32_t n_seq) {
+  // one workgroup of 1024 threads a sequence; a launch holds fewer than 2^32 threads
+  if (n_seq < 1 || n_seq >= (1 << 22))
+    return fail(MOE_ERR_INVALID_ARG, "n_seq=%d must be in [1, 2^22)", n_seq);
   return MOE_OK;
 }
 
@@ -677,7 +678,7 @@ static moe_status check_ws(const char* call, const void* ws, size_t got, size_t 
 
 size_t moe_balance_loss_workspace_bytes(const moe_problem* p, int32_t n_seq) {
   Dims d;
-  if (validate(p, &d) != MOE_OK || check_sequences(d, n_seq) != MOE_OK) return 0;
+  if (validate(p, &d) != MOE_OK || check_sequences(n_seq) != MOE_OK) return 0;
   return balance_ws_bytes(d, n_seq);
 }
 
@@ -688,7 +689,7 @@ moe_status moe_balance_loss(const moe_problem* p, const float* logits, const int
   Dims d;
   moe_status s = validate(p, &d);
   if (s != MOE_OK) return s;
-  if ((s = check_sequences(d, n_seq)) != MOE_OK) return s;
+  if ((s = check_sequences(n_seq)) != MOE_OK) return s;
   REQUIRE_PTR(logits);
   REQUIRE_PTR(topk_idx);
   REQUIRE_PTR(seq_counts);
@@ -712,7 +713,7 @@ moe_status moe_balance_loss_backward(const moe_problem* p, const float* logits,
   Dims d;
   moe_status s = validate(p, &d);
   if (s != MOE_OK) return s;
-  if ((s = check_sequences(d, n_seq)) != MOE_OK) return s;
+  if ((s = check_sequences(n_seq)) != MOE_OK) return s;
   REQUIRE_PTR(logits);
   REQUIRE_PTR(seq_counts);
   REQUIRE_PTR(dlogits);
@@ -740,6 +741,9 @@ moe_status moe_router_backward_dense(const moe_problem* p, const void* x, const 
   REQUIRE_PTR(dlogits);
   REQUIRE_PTR(dx_router);
   REQUIRE_PTR(dw_router);
+  // a launch holds fewer than 2^32 threads
+  if (d.T > (1 << 25) || d.T * d.H > ((int64_t)1 << 36))
+    return fail(MOE_ERR_INVALID_ARG, "T=%lld must be <= 2^25 with T*H <= 2^36", (long long)d.T);
   if ((s = check_ws("moe_router_backward_dense", ws, ws_bytes, router_dense_ws_bytes(d))) != MOE_OK)
     return s;
   if ((s = check_device(nullptr)) != MOE_OK) return s;
@@ -820,7 +824,8 @@ moe_status moe_quantize_fp8(const void* x, int32_t dtype, int64_t rows, int64_t 
   constexpr int64_t kMost = (int64_t)1 << 40;
   if (rows < 1 || cols < 1 || rows > kMost || cols > kMost)
     return fail(MOE_ERR_INVALID_ARG, "rows and cols must be in [1, 2^40]");
-  if (((rows + 127) / 128) * (double)((cols + 127) / 128) >= 2147483648.0)
+  // the transpose takes a workgroup of 256 threads a block, and a launch holds fewer than 2^32
+  if (((rows + 127) / 128) * (double)((cols + 127) / 128) >= (qt ? 16777216.0 : 2147483648.0))
     return fail(MOE_ERR_INVALID_ARG, "too many 128x128 blocks");
   if (ldx < cols) return fail(MOE_ERR_INVALID_ARG, "ldx=%lld < cols", (long long)ldx);
   if (!x || (reinterpret_cast<uintptr_t>(x) & (dtype == MOE_F32 ? 3 : 1)))
@@ -843,11 +848,12 @@ moe_status moe_quantize_fp8(const void* x, int32_t dtype, int64_t rows, int64_t 
 }
 
 static moe_status check_gemm_fp8(int64_t M, int64_t N, int64_t K) {
-  constexpr int64_t kMost = ((int64_t)1 << 31) - 1;
+  // workgroups of 512 threads take 16 columns (few rows) or tiles of 64 x 128 to 256 x 256, and
+  // a launch holds fewer than 2^32 threads
+  constexpr int64_t kMost = (int64_t)1 << 26;
   if (M < 1 || N < 1 || K < 1 || M > kMost || N > kMost || K > ((int64_t)1 << 22))
-    return fail(MOE_ERR_INVALID_ARG, "M, N must be in [1, 2^31) and K in [1, 2^22]");
-  if (((M + 63) / 64) * ((N + 63) / 64) > kMost)
-    return fail(MOE_ERR_INVALID_ARG, "more than 2^31 - 1 tiles of 64 x 64");
+    return fail(MOE_ERR_INVALID_ARG, "M, N must be in [1, 2^26] and K in [1, 2^22]");
+  if (M * N > ((int64_t)1 << 37)) return fail(MOE_ERR_INVALID_ARG, "M*N must be <= 2^37");
   return MOE_OK;
 }
 
