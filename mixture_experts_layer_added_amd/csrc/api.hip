@@ -848,7 +848,7 @@ moe_status moe_quantize_fp8(const void* x, int32_t dtype, int64_t rows, int64_t 
 }
 
 static moe_status check_gemm_fp8(int64_t M, int64_t N, int64_t K) {
-  // workgroups of 512 threads take 16 columns (few rows) or tiles of 64 x 128 to 256 x 256, and
+  // workgroups of 512 threads take 16 columns (few rows) or tiles of 128 x 64 to 256 x 256, and
   // a launch holds fewer than 2^32 threads
   constexpr int64_t kMost = (int64_t)1 << 26;
   if (M < 1 || N < 1 || K < 1 || M > kMost || N > kMost || K > ((int64_t)1 << 22))

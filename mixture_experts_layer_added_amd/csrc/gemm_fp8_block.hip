@@ -22,6 +22,7 @@
 // N arrive as zeros by the descriptor's range check.  B is the matrix instruction's first
 // operand, so a lane's results lie in one row of C and take one activation scale.  Split over
 // k (few tiles): fp32 partial sums to the workspace, k_fp8_join adds them in order.
+#include <algorithm>
 #include <type_traits>
 
 #include "common.h"
@@ -574,8 +575,17 @@ struct Plan {
 
 int64_t up4(int64_t n) { return (n + 3) / 4 * 4; }
 
-// The tile and the split over k, from the sizes alone (the workspace's size depends on it).
-Plan plan(int64_t M, int64_t N, int64_t K) {
+// The form, the tile and the split over k, from the sizes and the form of the products.
+//   k_fp8_rows (us against the tile's): 16 x 4096 x 7168 11.8 (13.9), 32 x 1024 x 1024 7.1 (9.7),
+//     32 x 4096 x 7168 16.2 (14.3)
+//   256 x 256 (fp32 C: 256 x 128) once that leaves 192 CUs a tile: 2048 x 6400 x 4096 58 us
+//     against 81 in tiles of 128 x 128
+//   else the cheaper of 128 x 64 and 128 x 128, whole or split, by what was measured of each: a
+//     step of a round of 256 workgroups, and for a split 3 us of k_fp8_join and its partial sums'
+//     way out and in at 4 TB/s.  bf16 C: 1000 x 2048 x 2048 11.4 us as 128 x 64 (128 x 128: 14.2,
+//     and 22.7 split in two); 640 x 2048 x 7168 24.8 as 128 x 128 in three parts (128 x 64
+//     whole: 30.3); 128 x 4096 x 7168 16.6 as 128 x 64 in four (128 x 128 in eight: 18.3)
+Plan plan(int64_t M, int64_t N, int64_t K, bool wide) {
   const int64_t nk = (K + GBK - 1) / GBK;
   Plan p;
   if (M <= 16 || (M <= 32 && K <= 2048)) {  // k_fp8_rows
@@ -585,15 +595,28 @@ Plan plan(int64_t M, int64_t N, int64_t K) {
     p.steps = (int)nk;
     return p;
   }
-  if (M <= 64) { p.bm = 64; p.bn = 128; }
-  else if (((M + 255) / 256) * ((N + 255) / 256) >= 192) { p.bm = 256; p.bn = 256; }
-  else { p.bm = 128; p.bn = 128; }
-  const int64_t tiles = ((M + p.bm - 1) / p.bm) * ((N + p.bn - 1) / p.bn);
-  int64_t s = tiles >= 192 ? 1 : 256 / tiles;
-  s = s < nk / 4 ? s : nk / 4;  // at least 4 blocks a part
-  if (s < 1) s = 1;
-  p.steps = (int)((nk + s - 1) / s);
-  p.splits = (int)((nk + p.steps - 1) / p.steps);
+  p.splits = 1;
+  p.steps = (int)nk;
+  if (M > 128 && N > 128 && ((M + 255) / 256) * ((N + 255) / 256) >= 192) {
+    p.bm = p.bn = 256;
+    return p;
+  }
+  p.bm = 128;
+  double best = 1e30;
+  for (int bn = 64; bn <= 128; bn += 64) {
+    const double step_us = bn == 64 ? (wide ? 0.73 : 0.55) : (wide ? 1.2 : 0.69);
+    const int64_t tiles = ((M + 127) / 128) * ((N + bn - 1) / bn);
+    for (int64_t s = 1; s == 1 || (s * tiles <= 256 && s <= nk / 8); ++s) {
+      const int64_t steps = (nk + s - 1) / s, parts = (nk + steps - 1) / steps;
+      double us = (double)((tiles * parts + 255) / 256 * steps) * step_us;
+      if (parts > 1) us += 3.0 + 2e-6 * (double)(parts * M * N);
+      if (us >= best) continue;
+      best = us;
+      p.bn = bn;
+      p.splits = (int)parts;
+      p.steps = (int)steps;
+    }
+  }
   return p;
 }
 
@@ -625,15 +648,16 @@ void launch_rows(const Plan& p, const GemmArgs& g, bool row_b, hipStream_t st) {
 }  // namespace
 
 size_t gemm_fp8_ws_bytes(int64_t M, int64_t N, int64_t K) {
-  const Plan p = plan(M, N, K);
-  return p.splits > 1 ? (size_t)p.splits * (size_t)M * (size_t)up4(N) * 4 : 0;
+  int splits = 1;  // the larger of the two forms
+  for (int wide = 0; wide < 2; ++wide) splits = std::max(splits, plan(M, N, K, wide).splits);
+  return splits > 1 ? (size_t)splits * (size_t)M * (size_t)up4(N) * 4 : 0;
 }
 
 hipError_t launch_gemm_fp8(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda,
                            const float* sa, const uint8_t* b, int64_t ldb, const float* sb,
                            int b_rows, void* c, int64_t ldc, int c_f32, int accumulate, void* ws,
                            hipStream_t st) {
-  const Plan p = plan(M, N, K);
+  const Plan p = plan(M, N, K, c_f32);
   GemmArgs g{a, b, sa, sb, c, lda, ldb, ldc, M, N, K, 0, 0, p.splits, p.steps, c_f32, accumulate};
   if (p.splits > 1) {
     g.c = ws;
@@ -643,10 +667,15 @@ hipError_t launch_gemm_fp8(int64_t M, int64_t N, int64_t K, const uint8_t* a, in
   if (p.bn == 16) {
     if (c_f32) launch_rows<true>(p, g, row_b, st);
     else launch_rows<false>(p, g, row_b, st);
-  } else if (p.bm == 64) {
-    if (c_f32) launch_tile<64, 128, 2, 4, 3, true>(g, row_b, st);
-    else launch_tile<64, 128, 2, 4, 3, false>(g, row_b, st);
-  } else if (p.bm == 128) {
+  } else if (p.bn == 64) {
+    if (c_f32) launch_tile<128, 64, 4, 2, 3, true>(g, row_b, st);
+    else launch_tile<128, 64, 4, 2, 3, false>(g, row_b, st);
+  } else if (p.bn == 128 && (M + 127) / 128 * ((N + 127) / 128) * p.splits <= 256) {
+    // one workgroup a CU: three stages (1408 x 2048 x 7168: 39 us, with two 52); more of them:
+    // two stages, with which a CU holds two workgroups (2048 x 4096 x 4096: 45 us, with three 56)
+    if (c_f32) launch_tile<128, 128, 4, 2, 3, true>(g, row_b, st);
+    else launch_tile<128, 128, 4, 2, 3, false>(g, row_b, st);
+  } else if (p.bn == 128) {
     if (c_f32) launch_tile<128, 128, 4, 2, 2, true>(g, row_b, st);
     else launch_tile<128, 128, 4, 2, 2, false>(g, row_b, st);
   } else {

@@ -177,7 +177,9 @@ def near(c, A, B, out, c0=None):
 SIZES = [(1, 1, 1), (1, 128, 128), (3, 5, 7), (1, 200, 500), (16, 64, 16), (17, 33, 130),
          (31, 129, 257), (32, 512, 1024), (33, 256, 384), (64, 64, 4099), (65, 300, 640),
          (100, 1000, 129), (128, 128, 128), (129, 260, 1025), (200, 513, 300), (256, 256, 2048),
-         (257, 511, 777), (300, 1024, 256), (1000, 77, 130), (520, 770, 515)]
+         (257, 511, 777), (300, 1024, 256), (1000, 77, 130), (520, 770, 515),
+         # 128 x 128 tiles in one round, in three parts, in several rounds; 256 x 256
+         (1100, 2050, 300), (650, 2040, 5000), (2100, 2500, 260), (2100, 5400, 140)]
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)
