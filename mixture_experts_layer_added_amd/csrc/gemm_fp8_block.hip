@@ -62,7 +62,7 @@ struct Op<false> {
   };
   static __device__ __forceinline__ int row(int lane) { return lane & 15; }
   static __device__ __forceinline__ int col(int lane, int i) { return 4 * (lane >> 4) + i; }
-  static __device__ __forceinline__ int chunk(int lane, int i) { return 2 * (lane >> 4) + i; }
+  static __device__ __forceinline__ int chunk(int lane, int i) { return (lane >> 4) + 4 * i; }
   static __device__ __forceinline__ Frag from(const u32x4 (&c)[kC]) {
     Frag f;
 #pragma unroll

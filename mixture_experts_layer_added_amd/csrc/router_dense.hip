@@ -19,6 +19,8 @@
 //     dW: 128 (or 64) experts x 128 columns, 32 tokens a step (16 for fp32 x); both operands have
 //       k outermost and are read with ds_read_b64_tr_b16 (gemm_bwd.hip).  Split over the
 //       tokens; k_rd_join adds the parts in order.
+#include <algorithm>
+
 #include "common.h"
 
 namespace moe {
@@ -459,11 +461,15 @@ RdPlan rd_plan(const Dims& d) {
   RdPlan p;
   p.bm = d.E <= 64 ? 64 : 128;
   p.Ep = (d.E + p.bm - 1) / p.bm * p.bm;
-  // about two workgroups a CU, parts of at least 256 tokens
+  // bf16 x: about one workgroup a CU (T=4096 H=7168 E=256 110 us; two workgroups a CU 115, half a
+  // one 127); fp32 x, twice the products: two (T=8192 H=4096 E=64 143 us, one 163).  Parts of at
+  // least 256 tokens (T=1024 H=2048 E=64 14.7 us, of 512 17.9), where the tiles are many of 512
+  // (T=512 H=7168 E=256 24 us, of 256 30).
+  const bool f32 = d.act == MOE_F32;
   const int64_t tiles = (int64_t)(p.Ep / p.bm) * (d.H / DBN);
   const int64_t steps = (d.T + 31) / 32;
-  int64_t s = 512 / tiles;
-  if (s > steps / 8) s = steps / 8;
+  int64_t s = (f32 ? 512 : 256) / tiles;
+  s = std::min(s, steps / (tiles >= 64 ? 16 : 8));
   if (s < 1) s = 1;
   p.part_rows = (steps + s - 1) / s * 32;
   p.parts = (int)((d.T + p.part_rows - 1) / p.part_rows);
@@ -536,7 +542,8 @@ hipError_t launch_router_dense_bwd(const Dims& d, const void* x, const float* w,
   }
   float* out = p.parts > 1 ? reinterpret_cast<float*>(b + p.part) : dw;
   RdArgs g{zh, zp, wh, xp, ze, we, dx, out, d.T, p.part_rows, d.H, d.E, p.Ep, 0, d.H / DBN, 0, 0};
-  // 128 tokens a tile of dx once that gives every CU one
+  // 128 tokens a tile of dx once that gives every CU one (T=4096 H=7168 E=256: 110 us, with 64
+  // tokens 120; T=128: 14.8 us with 64, 16.8 with 128)
   if ((d.T + 127) / 128 * g.nt >= 256) launch_products<128>(g, p, f32, st);
   else launch_products<64>(g, p, f32, st);
   if ((e = hipGetLastError()) != hipSuccess || p.parts == 1) return e;
