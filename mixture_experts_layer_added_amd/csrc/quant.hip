@@ -79,7 +79,10 @@ struct Scale {
   }
   __device__ __forceinline__ uint32_t codes(float a, float b, float c, float d) const {
     if (plain) return pack4_e4m3(a / s, b / s, c / s, d / s);
-    return pack4_e4m3(of(a), of(b), of(c), of(d));
+    // no saturation needed: |v| <= amax and s >= amax/448 (1 - 2^-24), so |v/s| < 448.0001, whose
+    // code is 448's (the conversion overflows from 464 on)
+    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(of(a), of(b), 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(of(c), of(d), w, true);
   }
 };
 
@@ -199,12 +202,13 @@ __global__ __launch_bounds__(256) void k_quant_tile(const T* __restrict__ x, int
   }
   *reinterpret_cast<float2*>(&s_m[wv][2 * lane]) = make_float2(m0, m1);
   __syncthreads();
-  const int nr = (int)max((int64_t)0, min((int64_t)32, rows - r0 - 32 * wv));
+  // every wave has its part of the tile in registers: the tile's memory now takes the codes, 128
+  // bytes a column (16-byte chunks swizzled by the column's pair), so that 8 lanes write a line
+  char* codes = reinterpret_cast<char*>(tile);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int cc = 2 * lane + h;
     const int64_t c = c0 + cc;
-    if (c >= cols) continue;
     const Scale s(__builtin_fmaxf(__builtin_fmaxf(s_m[0][cc], s_m[1][cc]),
                                   __builtin_fmaxf(s_m[2][cc], s_m[3][cc])));
     uint32_t w[8];
@@ -212,16 +216,30 @@ __global__ __launch_bounds__(256) void k_quant_tile(const T* __restrict__ x, int
     for (int k = 0; k < 8; ++k)
       w[k] = h ? s.codes(P::hi(v[4 * k]), P::hi(v[4 * k + 1]), P::hi(v[4 * k + 2]), P::hi(v[4 * k + 3]))
                : s.codes(P::lo(v[4 * k]), P::lo(v[4 * k + 1]), P::lo(v[4 * k + 2]), P::lo(v[4 * k + 3]));
-    uint8_t* p = qt + c * ldqt + r0 + 32 * wv;
-    if (nr == 32) {
-      reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    } else {
 #pragma unroll
-      for (int k = 0; k < 32; ++k)
+    for (int i = 0; i < 2; ++i)
+      *reinterpret_cast<uint4*>(codes + cc * kQB + (((2 * wv + i) ^ (lane & 7)) << 4)) =
+          make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    if (wv == 0 && c < cols) scale_t[c * kbt + rb] = s.s;
+  }
+  __syncthreads();
+  const int ch = tid & 7;
+  const int nr = (int)max((int64_t)0, min((int64_t)16, rows - r0 - 16 * ch));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int cc = 32 * i + (tid >> 3);
+    if (c0 + cc >= cols) continue;
+    const uint4 u =
+        *reinterpret_cast<const uint4*>(codes + cc * kQB + ((ch ^ ((cc >> 1) & 7)) << 4));
+    uint8_t* p = qt + (c0 + cc) * ldqt + r0 + 16 * ch;
+    if (nr == 16) {
+      *reinterpret_cast<uint4*>(p) = u;
+    } else {
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
         if (k < nr) p[k] = (uint8_t)(w[k >> 2] >> (8 * (k & 3)));
     }
-    if (wv == 0) scale_t[c * kbt + rb] = s.s;
   }
 }
 
