@@ -60,25 +60,43 @@ __device__ __forceinline__ float amax8(const float* v) {
   return m;
 }
 
-// The rounded quotient v/s of |v| <= 448 s from r = 1/s, rounded: q0 = v r is within an ulp or so
-// of it, and the remainder v - q0 s, exact in one fused operation, corrects it to the nearest
-// (P. Markstein's theorem on division by a rounded reciprocal, IBM J. Res. Dev. 34, 1990).
-// 3 operations in place of the 10 of a division; s is kept away from the ends of the
-// exponent range, where r or the remainder would not be a normal number.
+// A rounded quotient v/d from r, the rounded 1/d: q = v r is within an ulp or so of it, and the
+// remainder v - q d, exact in one fused operation, corrects it to the nearest.  r comes in the
+// same way from an estimate within an ulp, except where d's mantissa is all ones.  (P.
+// Markstein's theorems on division and reciprocals with a fused multiply-add, IBM J. Res. Dev.
+// 34, 1990.)  3 operations in place of the 10 of a division, for the codes and for the scale.
+// Blocks near the ends of the exponent range, where r or a remainder would not be a normal
+// number, of zeros, or with the mantissa named, are divided plainly.
 struct Scale {
   float s, r;
   bool plain;
-  __device__ __forceinline__ explicit Scale(float amax) {
-    s = block_scale(amax);
-    r = 1.0f / s;
-    plain = !(s > 0x1p-100f && s < 0x1p100f);
-  }
-  __device__ __forceinline__ float of(float v) const {
+  static __device__ __forceinline__ float quotient(float v, float d, float r) {
     const float q = v * r;
-    return __builtin_fmaf(__builtin_fmaf(-q, s, v), r, q);
+    return __builtin_fmaf(__builtin_fmaf(-q, d, v), r, q);
   }
-  __device__ __forceinline__ uint32_t codes(float a, float b, float c, float d) const {
-    if (plain) return pack4_e4m3(a / s, b / s, c / s, d / s);
+  __device__ __forceinline__ explicit Scale(float amax) {
+    constexpr float k1By448 = 1.0f / 448.0f;
+    s = quotient(amax, 448.0f, k1By448);
+    const float e = __builtin_amdgcn_rcpf(s);
+    r = __builtin_fmaf(__builtin_fmaf(-s, e, 1.0f), e, e);
+    plain = !(amax > 0x1p-90f && amax < 0x1p100f) || (__float_as_uint(s) & 0x7fffffu) == 0x7fffffu;
+    if (plain) s = block_scale(amax);
+  }
+  __device__ __forceinline__ float of(float v) const { return quotient(v, s, r); }
+  // N groups of 4 codes
+  template <int N, typename F>
+  __device__ __forceinline__ void codes(F v, uint32_t* w) const {
+    if (plain) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        w[i] = pack4_e4m3(v(4 * i) / s, v(4 * i + 1) / s, v(4 * i + 2) / s, v(4 * i + 3) / s);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      w[i] = quick(v(4 * i), v(4 * i + 1), v(4 * i + 2), v(4 * i + 3));
+  }
+  __device__ __forceinline__ uint32_t quick(float a, float b, float c, float d) const {
     // no saturation needed: |v| <= amax and s >= amax/448 (1 - 2^-24), so |v/s| < 448.0001, whose
     // code is 448's (the conversion overflows from 464 on)
     const int w = __builtin_amdgcn_cvt_pk_fp8_f32(of(a), of(b), 0, false);
@@ -89,14 +107,14 @@ struct Scale {
 // the codes of v/s to q, whose first n bytes are the row's
 __device__ __forceinline__ void write8(uint8_t* __restrict__ q, int n, const float* v,
                                        const Scale& s) {
-  const uint32_t a = s.codes(v[0], v[1], v[2], v[3]);
-  const uint32_t b = s.codes(v[4], v[5], v[6], v[7]);
+  uint32_t w[2];
+  s.codes<2>([&](int i) { return v[i]; }, w);
   if (n >= 8) {
-    *reinterpret_cast<uint2*>(q) = make_uint2(a, b);
+    *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < n) q[i] = (uint8_t)((i < 4 ? a : b) >> (8 * (i & 3)));
+      if (i < n) q[i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
   }
 }
 
@@ -212,10 +230,7 @@ __global__ __launch_bounds__(256) void k_quant_tile(const T* __restrict__ x, int
     const Scale s(__builtin_fmaxf(__builtin_fmaxf(s_m[0][cc], s_m[1][cc]),
                                   __builtin_fmaxf(s_m[2][cc], s_m[3][cc])));
     uint32_t w[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      w[k] = h ? s.codes(P::hi(v[4 * k]), P::hi(v[4 * k + 1]), P::hi(v[4 * k + 2]), P::hi(v[4 * k + 3]))
-               : s.codes(P::lo(v[4 * k]), P::lo(v[4 * k + 1]), P::lo(v[4 * k + 2]), P::lo(v[4 * k + 3]));
+    s.codes<8>([&](int i) { return h ? P::hi(v[i]) : P::lo(v[i]); }, w);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       *reinterpret_cast<uint4*>(codes + cc * kQB + (((2 * wv + i) ^ (lane & 7)) << 4)) =

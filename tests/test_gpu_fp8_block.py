@@ -89,6 +89,22 @@ def test_quantize_small_values():
     assert bool(((v - x).abs() <= 2 ** -4 * x + 1e-44).all())
 
 
+@pytest.mark.parametrize("exponent", [-126, -95, -90, -60, 0, 55, 99, 100, 119])
+def test_quantize_every_mantissa(exponent):
+    """Blocks of one element with every mantissa of an exponent: the scale is the rounded quotient
+    by 448, the code 448's."""
+    from mixture_experts_layer_added_amd import _lib as L
+    n = 1 << 23
+    x = (torch.arange(n, dtype=torch.int32) + ((exponent + 127) << 23)).view(torch.float32)
+    q = torch.empty((n, 16), dtype=torch.uint8, device="cuda")
+    s = torch.empty((n, 1), device="cuda")
+    L.moe_quantize_fp8(x.cuda(), L.MOE_F32, n, 1, 1, q, 16, s)
+    torch.cuda.synchronize()
+    assert torch.equal(s.cpu()[:, 0], x / 448)
+    want = (x / (x / 448)).clamp(-448, 448).to(F8).view(torch.uint8)
+    assert torch.equal(q[:, 0].cpu(), want)
+
+
 def test_quantize_next_to_ties():
     """Values whose quotient by the scale lies on or within two steps of the middle between two
     codes: the codes are those of the correctly rounded quotient, as everywhere."""
@@ -99,6 +115,10 @@ def test_quantize_next_to_ties():
     n = 20000
     amax = (torch.rand((n, 1), generator=g) + 0.5) * 2.0 ** torch.randint(-60, 60, (n, 1),
                                                                           generator=g)
+    # scales next to a power of two, those with every bit of the mantissa set among them
+    near = torch.randint(40, 190, (n // 4, 1), generator=g, dtype=torch.int32) * (1 << 23)
+    near += torch.randint(-3, 4, near.shape, generator=g, dtype=torch.int32)
+    amax[:n // 4] = near.view(torch.float32) * 448
     pick = ties[torch.randint(0, len(ties), (n, 127), generator=g)]
     x = (pick.double() * (amax / 448).double()).float()
     for _ in range(2):
