@@ -12,13 +12,13 @@
 //   dW:  bf16 x is taken as it is, dz in three bf16 parts (24 bits, any exponent): three
 //     products.  fp32 x in three parts as well, and the six products above 2^-24.
 //   k_rd_split: the parts of dz (both kinds) and of W_r, transposed, with their exponents.
-//   k_rd_split_x: the parts of an fp32 x.
 //   k_rd_products, 4 waves a workgroup:
 //     dx: 128 (or 64) tokens x 128 columns; both operands have k innermost, so a step is 32 of
 //       k, both parts (128-byte rows, as in the FP8 product).
 //     dW: 128 (or 64) experts x 128 columns, 32 tokens a step (16 for fp32 x); both operands have
-//       k outermost and are read with ds_read_b64_tr_b16 (gemm_bwd.hip).  Split over the
-//       tokens; k_rd_join adds the parts in order.
+//       k outermost and are read with ds_read_b64_tr_b16 (gemm_bwd.hip).  fp32 x is split on
+//       its way to LDS (a pass of its own before the products moved 16 bytes an element more:
+//       T=8192 H=4096 E=64 143 us).  Split over the tokens; k_rd_join adds the parts in order.
 #include <algorithm>
 
 #include "common.h"
@@ -26,6 +26,8 @@
 namespace moe {
 namespace {
 
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef short v4i16 __attribute__((ext_vector_type(4)));
 typedef __attribute__((__vector_size__(8 * sizeof(_Float16)))) _Float16 f16x8;
 
@@ -34,7 +36,8 @@ constexpr int kRdWaves = 4;    // of a workgroup, 2 x 2
 constexpr int kRdLds = 65536;  // a ring of two stages
 
 struct RdArgs {
-  const uint16_t *zh, *zp, *wh, *xp;
+  const uint16_t *zh, *zp, *wh;
+  const void* x;
   const int32_t *ze, *we;
   float *dx, *dw;  // dw: dW or its partial sums [parts, E, H]
   int64_t T, part_rows;
@@ -159,23 +162,6 @@ __global__ __launch_bounds__(256) void k_rd_split(
     uint16_t* q = wh + (int64_t)(h0 + c2) * 2 * Ep + pair_at(e0 + 8 * l);
     *reinterpret_cast<uint4*>(q) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     *reinterpret_cast<uint4*>(q + 32) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-  }
-}
-
-__global__ __launch_bounds__(256) void k_rd_split_x(const float* __restrict__ x, int64_t n,
-                                                    uint16_t* __restrict__ xp) {
-  const int64_t stride = (int64_t)gridDim.x * 256 * 4;
-  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n; i += stride) {
-    const float4 v = *reinterpret_cast<const float4*>(x + i);
-    uint16_t a[3], b[3], c[3], d[3];
-    parts3(v.x, a);
-    parts3(v.y, b);
-    parts3(v.z, c);
-    parts3(v.w, d);
-#pragma unroll
-    for (int p = 0; p < 3; ++p)
-      *reinterpret_cast<uint2*>(xp + p * n + i) =
-          make_uint2(a[p] | (uint32_t)b[p] << 16, c[p] | (uint32_t)d[p] << 16);
   }
 }
 
@@ -324,11 +310,12 @@ __device__ __forceinline__ bf16x8 ko_frag(uint32_t addr) {
 }
 
 // dW partial sums over the tokens of a part: BM experts x 128 columns a workgroup.  XP parts of
-// x: 1 (bf16 x itself) or 3.
+// x: 1 (bf16 x itself) or 3 (fp32 x, 8 elements a thread and step, loaded a step before they
+// are split into the stage).
 template <int BM, int XP>
 __device__ __forceinline__ void rd_dw(char* smem, int tile, int part,
                                       const uint16_t* __restrict__ zp,
-                                      const uint16_t* __restrict__ xp, float* __restrict__ out,
+                                      const void* __restrict__ x, float* __restrict__ out,
                                       int64_t T, int H, int E, int Ep, int64_t part_rows, int nt) {
   constexpr int W = kRdWaves, WM = 2, WN = 2, SM = BM / WM / 32, SN = DBN / WN / 32;
   constexpr int kWStep = XP == 1 ? 32 : 16;  // tokens of a step
@@ -356,13 +343,44 @@ __device__ __forceinline__ void rd_dw(char* smem, int tile, int part,
         load16_to_lds(r, dst + p * kZ + i * 4 * W * kORow, 8 * lc < BM ? o : 0x7ffffff0u);
       }
     }
-#pragma unroll
-    for (int p = 0; p < XP; ++p) {
-      const i32x4 r = buffer_rsrc(xp + (p * T + t) * H, (uint32_t)(rows * H * 2));
+    if constexpr (XP == 1) {
+      const i32x4 r =
+          buffer_rsrc(static_cast<const uint16_t*>(x) + t * H, (uint32_t)(rows * H * 2));
 #pragma unroll
       for (int i = 0; i < kI; ++i)
-        load16_to_lds(r, dst + (3 + p) * kZ + i * 4 * W * kORow,
+        load16_to_lds(r, dst + 3 * kZ + i * 4 * W * kORow,
                       (uint32_t)((4 * (i * W + wv) + lr) * H + n0 + 8 * lc) * 2);
+    }
+  };
+  // XP == 3: elements 8 (tid % 16) .. +7 of the step's token tid / 16
+  const int xr = threadIdx.x >> 4, xc = threadIdx.x & 15;
+  float4 xv[2];
+  auto load_x = [&](int64_t t) {
+    xv[0] = xv[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (t + xr < t1) {
+      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(x) +
+                                                        (t + xr) * H + n0 + 8 * xc);
+      xv[0] = p[0];
+      xv[1] = p[1];
+    }
+  };
+  auto split_x = [&](int st) {
+    static_assert(XP == 1 || kWStep * 16 == 64 * kRdWaves, "a row's chunk a thread");
+    float v[8] = {xv[0].x, xv[0].y, xv[0].z, xv[0].w, xv[1].x, xv[1].y, xv[1].z, xv[1].w};
+    char* to = smem + st * kStage + 3 * kZ + xr * kORow + ((xc ^ (4 * (xr & 3))) << 4);
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+      uint32_t w[4];  // the hardware's conversion: round to nearest even, as f32_to_bf16_bits
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = __builtin_bit_cast(
+            uint32_t, __builtin_convertvector((f32x2){v[2 * i], v[2 * i + 1]}, bf16x2));
+      *reinterpret_cast<uint4*>(to + p * kZ) = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] -= __uint_as_float(w[i] << 16);
+        v[2 * i + 1] -= __uint_as_float(w[i] & 0xFFFF0000u);
+      }
     }
   };
   f32x16 acc[SM][SN];
@@ -378,11 +396,22 @@ __device__ __forceinline__ void rd_dw(char* smem, int tile, int part,
 #pragma unroll
   for (int n = 0; n < SN; ++n) ob[n] = ko_off(lane, wn * SN + n);
   stage(t0, 0);
+  if constexpr (XP == 3) {
+    load_x(t0);
+    split_x(0);
+    load_x(t0 + kWStep);
+  }
   int st = 0;
   for (int64_t t = t0; t < t1; t += kWStep, st ^= 1) {
     wait_vm<0>();
     __syncthreads();
-    if (t + kWStep < t1) stage(t + kWStep, st ^ 1);
+    if (t + kWStep < t1) {
+      stage(t + kWStep, st ^ 1);
+      if constexpr (XP == 3) {
+        split_x(st ^ 1);
+        load_x(t + 2 * kWStep);
+      }
+    }
     const uint32_t zs = lds0 + st * kStage, xs = zs + 3 * kZ;
 #pragma unroll
     for (int s = 0; s < kWStep / 16; ++s) {
@@ -431,7 +460,7 @@ template <int BMX, int BMW, int XP>
 __global__ __launch_bounds__(64 * kRdWaves, 1) void k_rd_products(RdArgs g) {
   __shared__ __attribute__((aligned(1024))) char smem[kRdLds];
   if ((int)blockIdx.x < g.dw_blocks)
-    rd_dw<BMW, XP>(smem, blockIdx.x % g.dw_tiles, blockIdx.x / g.dw_tiles, g.zp, g.xp, g.dw, g.T,
+    rd_dw<BMW, XP>(smem, blockIdx.x % g.dw_tiles, blockIdx.x / g.dw_tiles, g.zp, g.x, g.dw, g.T,
                    g.H, g.E, g.Ep, g.part_rows, g.nt);
   else
     rd_dx<BMX>(smem, blockIdx.x - g.dw_blocks, g.zh, g.ze, g.wh, g.we, g.dx, g.T, g.H, g.Ep, g.mt,
@@ -454,7 +483,7 @@ struct RdPlan {
   int Ep, bm;         // experts padded to whole tiles, experts of a k_rd_dw tile
   int parts;          // of the tokens
   int64_t part_rows;
-  size_t zh, zp, ze, wh, we, xp, part, bytes;  // byte offsets in the workspace
+  size_t zh, zp, ze, wh, we, part, bytes;  // byte offsets in the workspace
 };
 
 RdPlan rd_plan(const Dims& d) {
@@ -462,14 +491,15 @@ RdPlan rd_plan(const Dims& d) {
   p.bm = d.E <= 64 ? 64 : 128;
   p.Ep = (d.E + p.bm - 1) / p.bm * p.bm;
   // bf16 x: about one workgroup a CU (T=4096 H=7168 E=256 110 us; two workgroups a CU 115, half a
-  // one 127); fp32 x, twice the products: two (T=8192 H=4096 E=64 143 us, one 163).  Parts of at
-  // least 256 tokens (T=1024 H=2048 E=64 14.7 us, of 512 17.9), where the tiles are many of 512
-  // (T=512 H=7168 E=256 24 us, of 256 30).
+  // one 127); fp32 x, twice the products: two (T=8192 H=4096 E=64 82 us, one 91).  Parts of at
+  // least 128 tokens (T=1000 H=1024 E=64, fp32 16 us, of 256 19), where the tiles are many of 512
+  // (T=512 H=7168 E=256 24 us, of 256 30), and at most 32 parts (T=16384 H=512 E=100, fp32: 60 us,
+  // 64 parts 61, 128 parts 82).
   const bool f32 = d.act == MOE_F32;
   const int64_t tiles = (int64_t)(p.Ep / p.bm) * (d.H / DBN);
   const int64_t steps = (d.T + 31) / 32;
   int64_t s = (f32 ? 512 : 256) / tiles;
-  s = std::min(s, steps / (tiles >= 64 ? 16 : 8));
+  s = std::min(s, std::min<int64_t>(steps / (tiles >= 64 ? 16 : 4), 32));
   if (s < 1) s = 1;
   p.part_rows = (steps + s - 1) / s * 32;
   p.parts = (int)((d.T + p.part_rows - 1) / p.part_rows);
@@ -485,7 +515,6 @@ RdPlan rd_plan(const Dims& d) {
   p.ze = take((size_t)d.T * 4);
   p.wh = take(HE * 4);
   p.we = take((size_t)d.H * 4);
-  p.xp = take(d.act == MOE_F32 ? (size_t)d.T * d.H * 6 : 0);
   p.part = take(p.parts > 1 ? (size_t)p.parts * d.E * d.H * 4 : 0);
   p.bytes = at;
   return p;
@@ -530,18 +559,9 @@ hipError_t launch_router_dense_bwd(const Dims& d, const void* x, const float* w,
                      d.H, d.E, p.Ep, zb, zh, zp, ze, wh, we);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const uint16_t* xp = static_cast<const uint16_t*>(x);
   const bool f32 = d.act == MOE_F32;
-  if (f32) {
-    uint16_t* parts = reinterpret_cast<uint16_t*>(b + p.xp);
-    const int64_t n = d.T * d.H, blocks = (n / 4 + 255) / 256;
-    hipLaunchKernelGGL(k_rd_split_x, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256),
-                       0, st, static_cast<const float*>(x), n, parts);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    xp = parts;
-  }
   float* out = p.parts > 1 ? reinterpret_cast<float*>(b + p.part) : dw;
-  RdArgs g{zh, zp, wh, xp, ze, we, dx, out, d.T, p.part_rows, d.H, d.E, p.Ep, 0, d.H / DBN, 0, 0};
+  RdArgs g{zh, zp, wh, x, ze, we, dx, out, d.T, p.part_rows, d.H, d.E, p.Ep, 0, d.H / DBN, 0, 0};
   // 128 tokens a tile of dx once that gives every CU one (T=4096 H=7168 E=256: 110 us, with 64
   // tokens 120; T=128: 14.8 us with 64, 16.8 with 128)
   if ((d.T + 127) / 128 * g.nt >= 256) launch_products<128>(g, p, f32, st);
