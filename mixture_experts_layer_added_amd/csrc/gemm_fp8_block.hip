@@ -22,6 +22,12 @@
 // N arrive as zeros by the descriptor's range check.  B is the matrix instruction's first
 // operand, so a lane's results lie in one row of C and take one activation scale.  Split over
 // k (few tiles): fp32 partial sums to the workspace, k_fp8_join adds them in order.
+//   bf16 C, 4096 x 4096 x 7168: 107-111 us, 2200 TFLOP/s, the matrix cores busy 49% of the cycles;
+//   products with their promotions alone reach 3200 on random codes, by the card's power.
+//   fp32 C, 2048 x 7168 x 4099, both operands scaled by the row: 152 us, 790 TFLOP/s, bound by the
+//   vector unit (widening, two scales) and by 448 tiles on 256 CUs.
+//   128 x 4096 x 7168: 14.5 + 4 us, 14 dependent steps and the join of four parts.
+//   1 x 7168 x 2048 (k_fp8_rows): 5.5 us, launch and one round of loads.
 #include <algorithm>
 #include <type_traits>
 

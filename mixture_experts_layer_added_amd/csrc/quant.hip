@@ -5,10 +5,12 @@
 //   x/scale (IEEE division)
 // A code's relative rounding error is at most 2^-4 for values above 2^-6 scale; smaller ones
 // round to multiples of 2^-9 scale.
-// All kernels here are bound by memory: each element is read once and each code written once.
+// Each element is read once and each code written once.
 //   k_quant_rows: 16 lanes take a block of 128 columns, 8 elements a lane (36,864 x 4096 bf16:
 //     95 us, 4.8 TB/s; four blocks a turn with their loads ahead of their codes took as long).
-//   k_quant_tile: a workgroup takes 128 x 128 elements through LDS and writes both orders.
+//   k_quant_tile: a workgroup takes 128 x 128 elements through LDS and writes both orders
+//     (4099 x 7168 bf16, both: 36 us, 3.3 TB/s; two quantisations an element weigh as much as the
+//     bytes).
 //   k_ckpt_restore: 8 columns of h a lane from the gate and the up codes.
 #include <algorithm>
 

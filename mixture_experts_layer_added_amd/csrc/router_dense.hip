@@ -19,6 +19,9 @@
 //       k outermost and are read with ds_read_b64_tr_b16 (gemm_bwd.hip).  fp32 x is split on
 //       its way to LDS (a pass of its own before the products moved 16 bytes an element more:
 //       T=8192 H=4096 E=64 143 us).  Split over the tokens; k_rd_join adds the parts in order.
+// T=4096 H=7168 E=256, bf16 x: products 91 us (90 GFLOP of parts, 1000 TFLOP/s, the matrix cores
+// busy 46% of the time, beside 117 MB of fp32 dx), split 7 us, join 5 us.  T=3137 H=384 E=48, fp32
+// x: 18 us, of three launches.
 #include <algorithm>
 
 #include "common.h"
