@@ -155,16 +155,17 @@ def test_token_counts(T):
     check(z, idx, [0, 0] + cuts + [T, T], dgate, f"T={T} ragged")
 
 
-def test_long_batch():
-    """65,536 tokens: 64-token chunks and eight tokens a lane group in the backward; sequences
-    that begin and end inside chunks."""
-    T, E, K = 65536, 32, 4
-    z, idx, dgate = inputs(1, E, K, seed=1)
+@pytest.mark.parametrize("T,E", [(65536, 32), (65536, 48), (40003, 64), (70001, 50),
+                                 (65537, 300)])
+def test_long_batch(T, E):
+    """64-token chunks, two or eight tokens a lane group in the backward; sequences that begin
+    and end inside chunks, and inside a lane group's tokens."""
+    K = 4
     g = torch.Generator().manual_seed(2)
     z = torch.randn((T, E), generator=g)
     idx = torch.rand((T, E), generator=g).topk(K, dim=1).indices.int()
     dgate = torch.randn((T, K), generator=g)
-    check(z, idx, [0, 1, 63, 64, 200, 40000, 40001, 65000], dgate, "65,536 tokens")
+    check(z, idx, [0, 1, 63, 64, 200, 39000, 39001, T - 500], dgate, f"{T} tokens E={E}")
 
 
 def test_one_token_sequences():
