@@ -466,6 +466,7 @@ moe_status moe_router_backward_dense(const moe_problem* p, const void* x, const 
  * 2 or 4, and h [R,I] is not kept at all (the backward forms it again).  One au (and h) buffer
  * can then serve every layer of a model.  A kept value is off by at most 2^-4 of itself, or
  * 2^-10 scale where it is below 2^-6 scale.
+ * au may hold NaN and infinities, as in moe_quantize_fp8.
  *   au_q [R,2I] codes, au_scale [R,2I/128] fp32. */
 moe_status moe_checkpoint_save(const moe_problem* p, const void* au, void* au_q, float* au_scale,
                                void* stream);
@@ -489,7 +490,9 @@ moe_status moe_expert_ffn_backward_input_checkpoint(const moe_problem* p, const 
 /* ---------------- block-scaled FP8 matrix product ----------------
  * E4M3 quantisation of x [rows, cols] (dtype MOE_BF16 or MOE_F32, row stride ldx elements), one
  * fp32 scale per 128 elements: scale = amax/448 (1 if that is 0), code = RNE-saturating E4M3 of
- * x/scale.
+ * x/scale.  x need not be finite: a NaN has a NaN code and is left out of amax, so its neighbours
+ * keep theirs; an infinity makes its block's scale infinite, its own code NaN and the others 0,
+ * so that the block's values, code * scale, are all NaN.
  *   q  [rows, ldq]  codes, scale   [rows, ceil(cols/128)]: blocks along a row; or both NULL
  *   qt [cols, ldqt] codes, scale_t [cols, ceil(rows/128)]: the transpose, blocks along a column
  *      of x; or both NULL (one of the two forms is required; both come from one read of x)

@@ -3,6 +3,8 @@
 // 8-bit activation checkpoints of the expert backward, which are the row form.
 //   scale = amax/448 over the block (1 where that is 0), code = RNE-saturating E4M3 of
 //   x/scale (IEEE division)
+// A NaN has a NaN code and no part in amax; an infinity makes the scale infinite, its own code
+// NaN and the others 0, so that the whole block comes back as NaN.
 // A code's relative rounding error is at most 2^-4 for values above 2^-6 scale; smaller ones
 // round to multiples of 2^-9 scale.
 // Each element is read once and each code written once.
@@ -55,7 +57,7 @@ __device__ __forceinline__ void read8(const float* __restrict__ p, int n, float*
   }
 }
 
-__device__ __forceinline__ float amax8(const float* v) {
+__device__ __forceinline__ float amax8(const float* v) {  // fmax passes a NaN by
   float m = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = __builtin_fmaxf(m, __builtin_fabsf(v[i]));
@@ -68,7 +70,8 @@ __device__ __forceinline__ float amax8(const float* v) {
 // Markstein's theorems on division and reciprocals with a fused multiply-add, IBM J. Res. Dev.
 // 34, 1990.)  3 operations in place of the 10 of a division, for the codes and for the scale.
 // Blocks near the ends of the exponent range, where r or a remainder would not be a normal
-// number, of zeros, or with the mantissa named, are divided plainly.
+// number, of zeros, of NaN alone, with an infinity, or with the mantissa named, are divided
+// plainly; there the quotient may pass 448, and is clamped by comparisons, which leave a NaN.
 struct Scale {
   float s, r;
   bool plain;
@@ -85,13 +88,21 @@ struct Scale {
     if (plain) s = block_scale(amax);
   }
   __device__ __forceinline__ float of(float v) const { return quotient(v, s, r); }
+  __device__ __forceinline__ float plain_of(float v) const {
+    const float q = v / s;
+    return q > 448.0f ? 448.0f : q < -448.0f ? -448.0f : q;
+  }
   // N groups of 4 codes
   template <int N, typename F>
   __device__ __forceinline__ void codes(F v, uint32_t* w) const {
     if (plain) {
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        w[i] = pack4_e4m3(v(4 * i) / s, v(4 * i + 1) / s, v(4 * i + 2) / s, v(4 * i + 3) / s);
+      for (int i = 0; i < N; ++i) {
+        const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(plain_of(v(4 * i)), plain_of(v(4 * i + 1)),
+                                                       0, false);
+        w[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(plain_of(v(4 * i + 2)),
+                                                         plain_of(v(4 * i + 3)), lo, true);
+      }
       return;
     }
 #pragma unroll
