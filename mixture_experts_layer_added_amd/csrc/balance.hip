@@ -72,6 +72,13 @@ __device__ __forceinline__ float4 load_row4(const float* __restrict__ row, int e
   return v;
 }
 
+// element i of the four at expert e lies past the row.  By its place, not by the fill: a caller's
+// own -inf is a logit as any other, clamped to -80.
+template <bool kVec>
+__device__ __forceinline__ bool past(int e, int i, int E) {
+  return kVec ? e >= E : e + i >= E;
+}
+
 template <int LP>
 __device__ __forceinline__ float seg_sum(float v) {
 #pragma unroll
@@ -132,7 +139,7 @@ __global__ __launch_bounds__(256) void k_balance_part(
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             s[j][i] = __builtin_amdgcn_rcpf(1.0f + exp_neg(clamp80(w[i])));
-            if (!kFull && w[i] == -INFINITY) s[j][i] = 0.0f;
+            if (!kFull && past<kVec>(4 * (LP * j + l), i, E)) s[j][i] = 0.0f;
             sum += s[j][i];
           }
         }
@@ -283,7 +290,7 @@ __global__ __launch_bounds__(1024) void k_balance_short(
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         s[j][i] = __builtin_amdgcn_rcpf(1.0f + exp_neg(clamp80(w[i])));
-        if (!kFull && w[i] == -INFINITY) s[j][i] = 0.0f;
+        if (!kFull && past<kVec>(4 * (LP * j + l), i, E)) s[j][i] = 0.0f;
         sum += s[j][i];
       }
     }
@@ -407,7 +414,7 @@ __global__ __launch_bounds__(256) void k_balance_bwd(
       for (int i = 0; i < 4; ++i) {
         const float c = clamp80(x[i]), em = exp_neg(c);
         const float a = __builtin_amdgcn_rcpf(1.0f + em);
-        s[j][i] = !kFull && x[i] == -INFINITY ? 0.0f : a;
+        s[j][i] = !kFull && past<kVec>(4 * (LP * j + l), i, E) ? 0.0f : a;
         o[j][i] = c == x[i] ? em * a : 0.0f;  // 0 where the clamp is flat
         sum += s[j][i];
         dot = __builtin_fmaf(cf[j][i], s[j][i], dot);

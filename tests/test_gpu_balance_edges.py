@@ -1,0 +1,90 @@
+"""The balance loss and its gradient at the edges of their inputs: infinite and NaN logits, rows
+of saturated logits with large and small weights, and no token lost or taken twice where chunks
+and sequences meet.
+
+Tolerances as in test_gpu_balance.py (u = 2^-24): a share is within 32 u, the gradient within 128 u
+of the magnitude that its bracket can cancel from.  A sum of shares adds u for each addition in
+its longest chain, here counted from the sum's own structure (see `additions`)."""
+import pytest
+
+from test_gpu_balance import Balance, U, inputs, reference
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from mixture_experts_layer_added_amd import _lib
+    _lib.lib()
+
+
+def up(a, b):
+    return -(-a // b)
+
+
+def additions(T, E, n_seq, length):
+    """The longest chain of additions behind a mean share.  A token has 4 to 32 lanes (a count
+    that holds for the fewest tokens a wave takes at once, 2, is an upper bound for all).  Up to
+    512 tokens: 16 waves side by side, the wave's groups (at most 4 steps), the 16 waves.  More:
+    chunks of 16 to 64 tokens up to 65,536 tokens, then as many as make 1024 chunks, 4 waves
+    each; then a sequence's chunks over the rows of a workgroup of at least 256 threads (E/4 up to a
+    power of two of them a row), and those rows in a tree."""
+    if T <= 512:
+        return up(length, 16 * 2) + 4 + 16
+    chunk = 16
+    while chunk * (256 if chunk < 64 else 1024) < T:
+        chunk *= 2
+    row = 1
+    while 4 * row < E:
+        row *= 2
+    rows = max(256 // row, 1)
+    return up(chunk, 4 * 2) + 4 + 2 + up(up(length, chunk) + 1, rows) + 10
+
+
+def check(z, idx, off, dloss, dgate=None, skip=()):
+    """Counts, shares and losses of every sequence but those in `skip`, and their gradients."""
+    b = Balance(z, idx, off, dloss, dgate)
+    b()
+    counts, prob, loss, dz = b.outputs()
+    rc, rp, rl, rg, mag = reference(z, idx, off, dloss, dgate)
+    assert torch.equal(counts, rc)
+    T, E, n = *z.shape, len(off) - 1
+    for q in range(n):
+        if q in skip:
+            continue
+        tol = (32 + 3 + additions(T, E, n, off[q + 1] - off[q])) * U
+        err = (prob[q].double() - rp[q]).abs()
+        assert bool((err <= tol * rp[q]).all()), (q, float((err / rp[q]).max() / U), tol / U)
+        assert abs(float(loss[q]) - float(rl[q])) <= (tol + 32 * U) * float(rl[q]), q
+    return prob, loss, dz, rg, mag
+
+
+def near(dz, rg, mag):
+    """2^-126 more: a result below the smallest normal number may be flushed."""
+    err = (dz.double() - rg).abs()
+    assert bool((err <= 128 * U * mag + 2.0 ** -126).all()), float(
+        (err / (128 * U * mag + 2.0 ** -126)).max())
+
+
+@pytest.mark.parametrize("E", [5, 16, 32, 48, 50, 64, 100, 128, 256, 257, 384, 512])
+@pytest.mark.parametrize("T", [40, 600])
+@pytest.mark.parametrize("with_gates", [False, True])
+def test_infinite_logits(E, T, with_gates):
+    """The clamp makes them 80 and -80: a row of -inf has equal shares, as a row of +inf has."""
+    K = min(E, 4)
+    z, idx, dgate = inputs(T, E, K, seed=E + T)
+    z[0] = -INF
+    z[3] = INF
+    z[4, ::2] = -INF
+    z[5, 1::3] = INF
+    z[T - 2, 0], z[T - 2, E - 1] = -INF, INF
+    z[T - 1] = -INF
+    off = [0, 3, 20, T - 1, T]
+    dloss = torch.tensor([1.0, -0.5, 2.0, 0.25])
+    _, _, dz, rg, mag = check(z, idx, off, dloss, dgate if with_gates else None)
+    near(dz, rg, mag)
+    assert not dz[0].any() and not dz[3].any() and not dz[T - 1].any()
