@@ -418,7 +418,8 @@ moe_status moe_quantize_weights_fp8(const void* w_bf16, void* w_fp8, float* scal
  *   seq_loss[q] = sum_e f[q,e] P[q,e]      (1 when the loads or the shares are uniform).
  * Weights (a small factor, the mean over sequences) are the caller's: they go into
  * dseq_loss of the backward.
- *   logits      [T,E] fp32 from moe_route (infinities are clamped as the formula says);
+ *   logits      [T,E] fp32 from moe_route (infinities are clamped as the formula says,
+ *               a NaN makes its sequence's P and loss and its token's dlogits NaN);
  *   topk_idx    [T,K] int32 from moe_route
  *   seq_offsets [n_seq+1] int32, 0 <= seq_offsets[0] <= ... <= seq_offsets[n_seq] <= T: empty
  *               sequences are allowed, tokens before the first and behind the last one

@@ -72,6 +72,14 @@ __device__ __forceinline__ float4 load_row4(const float* __restrict__ row, int e
   return v;
 }
 
+// A NaN among four logits.  The clamp (a median of three) makes a NaN -80, which would hide a
+// diverged router behind a finite loss: such a token's sum of affinities is made NaN instead.
+// (A clamp that keeps a NaN, by the two instructions of IEEE 754-2019's maximum and minimum, cost
+// 180 us at 262,144 x 256 with its gradient, against 170.)
+__device__ __forceinline__ bool any_nan(const float4& v) {
+  return __builtin_isunordered(v.x, v.y) | __builtin_isunordered(v.z, v.w);
+}
+
 // element i of the four at expert e lies past the row.  By its place, not by the fill: a caller's
 // own -inf is a logit as any other, clamped to -80.
 template <bool kVec>
@@ -133,8 +141,10 @@ __global__ __launch_bounds__(256) void k_balance_part(
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         float s[SL][4], sum = 0.0f;
+        bool lost = false;
 #pragma unroll
         for (int j = 0; j < SL; ++j) {
+          lost |= any_nan(v[u][j]);
           const float w[4] = {v[u][j].x, v[u][j].y, v[u][j].z, v[u][j].w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -143,7 +153,7 @@ __global__ __launch_bounds__(256) void k_balance_part(
             sum += s[j][i];
           }
         }
-        sum = seg_sum<LP>(sum);
+        sum = seg_sum<LP>(lost ? NAN : sum);
         const float inv = t + u * kStep < hi ? __builtin_amdgcn_rcpf(sum) : 0.0f;
 #pragma unroll
         for (int j = 0; j < SL; ++j)
@@ -283,9 +293,11 @@ __global__ __launch_bounds__(1024) void k_balance_short(
   for (int64_t t0 = lo + wv * TPW; t0 < hi; t0 += kWaves * TPW) {
     const int64_t t = t0 + seg;
     float s[SL][4], sum = 0.0f;
+    bool lost = false;
 #pragma unroll
     for (int j = 0; j < SL; ++j) {
       const float4 v = load_row4<kVec>(z + t * E, 4 * (LP * j + l), t < hi ? E : 0, -INFINITY);
+      lost |= any_nan(v);
       const float w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -294,7 +306,7 @@ __global__ __launch_bounds__(1024) void k_balance_short(
         sum += s[j][i];
       }
     }
-    sum = seg_sum<LP>(sum);
+    sum = seg_sum<LP>(lost ? NAN : sum);
     const float inv = t < hi ? __builtin_amdgcn_rcpf(sum) : 0.0f;
 #pragma unroll
     for (int j = 0; j < SL; ++j)
@@ -407,8 +419,10 @@ __global__ __launch_bounds__(256) void k_balance_bwd(
     }
     const bool in = live && q < n_seq && t >= q_lo;
     float s[SL][4], o[SL][4], sum = 0.0f, dot = 0.0f;  // o = 1 - s, without cancellation
+    bool lost = false;
 #pragma unroll
     for (int j = 0; j < SL; ++j) {
+      lost |= any_nan(row[j]);
       const float x[4] = {row[j].x, row[j].y, row[j].z, row[j].w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -420,7 +434,7 @@ __global__ __launch_bounds__(256) void k_balance_bwd(
         dot = __builtin_fmaf(cf[j][i], s[j][i], dot);
       }
     }
-    sum = seg_sum<LP>(sum);
+    sum = seg_sum<LP>(lost ? NAN : sum);
     dot = seg_sum<LP>(dot);
     const float inv = in ? __builtin_amdgcn_rcpf(sum) : 0.0f;
     const float mean = dot * inv;
@@ -445,7 +459,7 @@ __global__ __launch_bounds__(256) void k_balance_bwd(
         sl[n] = 0.0f;
         if (ek[n] >= 0 && ek[n] < E) {
           const float x = sd[ek[n]], c = clamp80(x), em = exp_neg(c);
-          const float a = __builtin_amdgcn_rcpf(1.0f + em);
+          const float a = x != x ? x : __builtin_amdgcn_rcpf(1.0f + em);
           sl[n] = c == x ? a * (em * a) : 0.0f;
           gd = __builtin_fmaf(gk[n], dk[n], gd);
           tot += a;

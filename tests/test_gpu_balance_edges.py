@@ -88,3 +88,21 @@ def test_infinite_logits(E, T, with_gates):
     _, _, dz, rg, mag = check(z, idx, off, dloss, dgate if with_gates else None)
     near(dz, rg, mag)
     assert not dz[0].any() and not dz[3].any() and not dz[T - 1].any()
+
+
+@pytest.mark.parametrize("E", [5, 16, 32, 50, 64, 128, 256, 257, 384, 512])
+@pytest.mark.parametrize("T", [40, 600])
+def test_nan_logits(E, T):
+    """A NaN logit has a NaN affinity: its sequence's shares and loss and its token's gradient
+    are NaN, every other sequence and token as without it."""
+    K = min(E, 4)
+    z, idx, dgate = inputs(T, E, K, seed=2 * E + T)
+    z[25, E // 2] = NAN
+    off = [0, 20, 31, T - 3]
+    dloss = torch.tensor([1.0, -0.5, 2.0])
+    for gates in (None, dgate):
+        prob, loss, dz, rg, mag = check(z, idx, off, dloss, gates, skip=(1,))
+        assert bool(prob[1].isnan().all()) and bool(loss[1].isnan())
+        assert bool(dz[25].isnan().all())
+        keep = torch.arange(T) != 25
+        near(dz[keep], rg[keep], mag[keep])
