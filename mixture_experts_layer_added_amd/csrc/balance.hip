@@ -7,6 +7,9 @@
 // The counts are piecewise constant, so the gradient runs through P alone: with
 // c[q,e] = dloss[q] f[q,e]/L and m_t = sum_e c[q,e] s[t,e]/S_t,
 //   dz[t,e] = (c[q,e] - m_t)/S_t s(1-s), 0 where |z| > 80 (the clamp is flat there).
+// It is formed as k (n' - m') (s/S)(1-s), with c = k n, n' the count from the uniform share on and
+// m' the mean of n': near the lower clamp s and S are about 1e-35, where c s would not be a normal
+// number and c/S would be infinite, while n' s is normal and s/S at most 1.
 // The backward joins the gradient of the chosen gates to it (the formula of the router's
 // backward), so a training step reads the logits once for both.
 //
@@ -363,7 +366,7 @@ __global__ __launch_bounds__(256) void k_balance_bwd(
   const int64_t first = (((int64_t)blockIdx.x * 4 + wv) * TPW + seg) * TW;
   int q = first < T ? seq_after(off, n_seq, first) : n_seq;
   int64_t q_lo = 0, q_hi = -1;  // the sequence whose coefficients are held
-  float cf[SL][4];
+  float cf[SL][4], scale = 0.0f;  // the counts, and what they are to be scaled by
 #pragma unroll
   for (int j = 0; j < SL; ++j)
 #pragma unroll
@@ -404,7 +407,7 @@ __global__ __launch_bounds__(256) void k_balance_bwd(
         q_lo = off[q];
         q_hi = off[q + 1];
         const float len = (float)(q_hi - q_lo);
-        const float k = dloss[q] * ((float)E / ((float)K * len)) / len;
+        scale = dloss[q] * ((float)E / ((float)K * len)) / len;
         // the counts from the uniform share on, in whole numbers: a constant in c drops out of
         // c - m, and near balance, where the counts are nearly equal, it would cancel badly
         const int uniform = (int)((q_hi - q_lo) * K / E);
@@ -413,7 +416,7 @@ __global__ __launch_bounds__(256) void k_balance_bwd(
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int e = 4 * (LP * j + l) + i;
-            cf[j][i] = e < E ? (float)(counts[(int64_t)q * E + e] - uniform) * k : 0.0f;
+            cf[j][i] = e < E ? (float)(counts[(int64_t)q * E + e] - uniform) : 0.0f;
           }
       }
     }
@@ -437,13 +440,13 @@ __global__ __launch_bounds__(256) void k_balance_bwd(
     sum = seg_sum<LP>(lost ? NAN : sum);
     dot = seg_sum<LP>(dot);
     const float inv = in ? __builtin_amdgcn_rcpf(sum) : 0.0f;
-    const float mean = dot * inv;
+    const float mean = dot * inv, k = scale;
     float d[SL][4];
 #pragma unroll
     for (int j = 0; j < SL; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        d[j][i] = (cf[j][i] - mean) * inv * (s[j][i] * o[j][i]);
+        d[j][i] = (cf[j][i] - mean) * k * (s[j][i] * inv * o[j][i]);
     if (dgate) {
       // the chosen gates' part: their logits come from, and their gradients are added to, the
       // token's row in the group's LDS (LDS operations of a wave run in order)
@@ -473,7 +476,7 @@ __global__ __launch_bounds__(256) void k_balance_bwd(
       __builtin_amdgcn_wave_barrier();
 #pragma unroll
       for (int n = 0; n < NK; ++n)
-        if (ek[n] >= 0 && ek[n] < E) atomicAdd(sd + ek[n], (dk[n] - gd) / tot * sl[n]);
+        if (ek[n] >= 0 && ek[n] < E) atomicAdd(sd + ek[n], (dk[n] - gd) * (sl[n] / tot));
       __builtin_amdgcn_wave_barrier();
 #pragma unroll
       for (int j = 0; j < SL; ++j) {

@@ -106,3 +106,21 @@ def test_nan_logits(E, T):
         assert bool(dz[25].isnan().all())
         keep = torch.arange(T) != 25
         near(dz[keep], rg[keep], mag[keep])
+
+
+@pytest.mark.parametrize("E,K", [(8, 1), (48, 3), (64, 8), (256, 8), (384, 6)])
+@pytest.mark.parametrize("weight", [2.0 ** 20, 1.0, 2.0 ** -30])
+def test_saturated_rows(E, K, weight):
+    """Rows whose logits are all near the lower clamp have affinities of 1e-35 and a sum whose
+    reciprocal is 1e34: the gradient, a share times a difference of weights, is an ordinary
+    number, whatever the loss's weight."""
+    T = 64
+    z, idx, dgate = inputs(T, E, K, seed=E)
+    z[::2] = z[::2] * 2 - 74
+    z[1] = -80.0
+    off = [0, 1, 2, 40, T]  # sequences of one token among them
+    dloss = torch.tensor([1.0, -1.0, 0.7, -0.3]) * weight
+    for gates in (None, dgate * weight * 100):
+        _, _, dz, rg, mag = check(z, idx, off, dloss, gates)
+        assert bool(dz.isfinite().all())
+        near(dz, rg, mag)
