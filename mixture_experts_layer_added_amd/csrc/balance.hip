@@ -440,7 +440,7 @@ __global__ __launch_bounds__(256) void k_balance_bwd(
     sum = seg_sum<LP>(lost ? NAN : sum);
     dot = seg_sum<LP>(dot);
     const float inv = in ? __builtin_amdgcn_rcpf(sum) : 0.0f;
-    const float mean = dot * inv, k = scale;
+    const float mean = dot * inv, k = in ? scale : 0.0f;
     float d[SL][4];
 #pragma unroll
     for (int j = 0; j < SL; ++j)

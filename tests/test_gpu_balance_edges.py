@@ -124,3 +124,23 @@ def test_saturated_rows(E, K, weight):
         _, _, dz, rg, mag = check(z, idx, off, dloss, gates)
         assert bool(dz.isfinite().all())
         near(dz, rg, mag)
+
+
+def test_padding_behind_a_diverged_sequence():
+    """A sequence whose loss has an infinite or NaN gradient keeps it to its own tokens."""
+    T, E, K = 90, 64, 4
+    z, idx, dgate = inputs(T, E, K, seed=7)
+    off = [0, 30, 50, 60]
+    for bad in (INF, NAN):
+        b = Balance(z, idx, off, torch.tensor([1.0, 1.0, bad]), None)
+        b()
+        dz = b.outputs()[3]
+        assert bool(dz[:50].isfinite().all()) and not dz[60:].any()
+        assert not dz[50:60].isfinite().all()
+    # several tokens a lane group (from 32,768 tokens on)
+    T = 40000
+    z, idx = torch.randn((T, E)), torch.zeros((T, 1), dtype=torch.int32)
+    b = Balance(z, idx, [0, 11, 1001], torch.tensor([1.0, NAN]), None)
+    b()
+    dz = b.outputs()[3]
+    assert bool(dz[:11].isfinite().all()) and not dz[1001:].any()
