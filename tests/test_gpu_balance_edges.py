@@ -157,7 +157,7 @@ def test_padding_behind_a_diverged_sequence():
 ])
 def test_every_token_once(T, E, cuts):
     """Shares and losses within the error of their own additions: a token lost or taken twice
-    in a sequence of L moves them by about 1/L, 2.5e-5 and more here against under 1e-5."""
+    in a sequence of L moves them by about 1/L, 1.5e-5 and more here against under 1e-5."""
     K = 3
     g = torch.Generator().manual_seed(T + E)
     z = torch.randn((T, E), generator=g)
