@@ -145,7 +145,7 @@ class MoELayer:
     kernels take at most 192 rows of an expert per tile (a larger expert streams its
     weights once per tile), the natural-layout kernels 256.
     checkpoint8 (with train): the pre-activations are kept between forward and backward as
-    8-bit checkpoints (au_q, au_scale) and h is not kept; share: another such layer of the same
+    8-bit checkpoints (au_q, au_scale, written by expert_ffn_up) and h is not kept; share: another such layer of the same
     shape whose au, h, dau, dy_sorted and dx_sorted buffers this one uses too (they hold nothing
     between calls; layers that share them must not run at the same time).
     """
@@ -287,6 +287,8 @@ class MoELayer:
         else:
             L.moe_expert_ffn_up(self.p, self.x_sorted, self.x_scale, self.offsets, self.w13,
                                 self.w13_scale, self.h, self.h_scale, stream)
+        if self.checkpoint8:  # here, so that a forward of single calls keeps its own batch's too
+            L.moe_checkpoint_save(self.p, self.au, self.au_q, self.au_scale, stream)
 
     def expert_ffn_down(self, stream=None):
         if self.packed:
@@ -309,8 +311,6 @@ class MoELayer:
         self.route(x, stream)
         self.permute(x, stream)
         self.expert_ffn(stream)
-        if self.checkpoint8:
-            L.moe_checkpoint_save(self.p, self.au, self.au_q, self.au_scale, stream)
         self.combine(stream)
         return self.y
 

@@ -1,0 +1,71 @@
+"""The layer's training options used step by step: a forward of single calls with kept
+checkpoints."""
+import pytest
+
+import workloads
+from gpu_cases import case, make_cpu_inputs, shape_of
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from mixture_experts_layer_added_amd import _lib
+    _lib.lib()
+
+
+def make(name, **kw):
+    from mixture_experts_layer_added_amd.layer import MoELayer
+    w = case(name)
+    inp = make_cpu_inputs(w)
+    dev = {k: v.contiguous().cuda() for k, v in inp.items()}
+    args = (shape_of(w), dev["w_router"], dev["bias"], dev["w13"], dev["w2"])
+    return w, dev["x"], workloads.make_dy(w).cuda(), lambda **k: MoELayer(*args, **{**kw, **k})
+
+
+def gradients(layer):
+    torch.cuda.synchronize()
+    return [t.clone() for t in (layer.dx, layer.dw_router, layer.dw13, layer.dw2)]
+
+
+@pytest.mark.parametrize("name,gather,packed", [
+    ("ragged-bf16", True, None), ("ragged-bf16", True, False), ("noshared-bf16", False, None),
+    ("tiny-fp32", False, False), ("tiny-fp32", True, False)])
+def test_forward_in_single_calls(name, gather, packed):
+    """route, permute, expert_ffn (or its two halves) and combine called one by one keep this
+    batch's checkpoints, as forward does."""
+    w, x, dy, layer = make(name, gather=gather, packed=packed, train=True, checkpoint8=True)
+    ref = layer()
+    y = ref.forward(x).clone()
+    ref.backward(dy)
+    want = gradients(ref)
+    for halves in (False, True):
+        got = layer()
+        got.forward(x.flip(0).contiguous())  # another batch's checkpoints lie in the buffers
+        got.route(x)
+        got.permute(x)
+        if halves:
+            got.expert_ffn_up()
+            got.expert_ffn_down()
+        else:
+            got.expert_ffn()
+        got.combine()
+        assert torch.equal(got.y, y)
+        got.backward(dy)
+        for a, b in zip(gradients(got), want):
+            assert torch.equal(a, b)
+    # layers that share their scratch: the codes are taken before the other layer's forward
+    first = layer()
+    second = layer(share=first)
+    for m, batch in ((first, x), (second, x.flip(0).contiguous())):
+        m.route(batch)
+        m.permute(batch)
+        m.expert_ffn()
+        m.combine()
+    second.backward(dy)
+    first.backward(dy)
+    for a, b in zip(gradients(first), want):
+        assert torch.equal(a, b)
