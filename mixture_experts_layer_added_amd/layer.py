@@ -4,6 +4,7 @@ marshalling); every step runs in libmoe's HIP kernels.
 """
 from __future__ import annotations
 
+import contextlib
 from dataclasses import dataclass
 
 import torch
@@ -244,9 +245,14 @@ class MoELayer:
         held = self._buffers.setdefault(name, [])
         if not held or held[-1].numel() < n:
             size = max(n, 2 * held[-1].numel()) if held else n
-            with torch.cuda.stream(torch.cuda.ExternalStream(L._stream(stream))):
-                held.append(torch.empty((size,), dtype=dtype, device=self.logits.device))
+            held.append(self._fresh(size, dtype, stream))
         return held[-1][:n]
+
+    def _fresh(self, n, dtype, stream):
+        """n elements allocated on the stream that uses them."""
+        with (contextlib.nullcontext() if stream is None else
+              torch.cuda.stream(torch.cuda.ExternalStream(L._stream(stream)))):
+            return torch.empty((n,), dtype=dtype, device=self.logits.device)
 
     def route(self, x, stream=None):
         self._seq_offsets = None
@@ -320,14 +326,14 @@ class MoELayer:
 
     def balance_loss(self, seq_offsets, stream=None):
         """Sequence-wise balance loss of the last forward's routing: seq_offsets [n_seq+1] int32
-        on the device -> [n_seq] fp32 (overwritten by the next call with as many sequences).
-        Also kept: counts per (sequence, expert) and mean affinity shares in self.seq_counts,
+        on the device -> [n_seq] fp32, a tensor of its own.  Also kept, until the next call:
+        counts per (sequence, expert) and mean affinity shares in self.seq_counts,
         self.seq_prob.  Its gradient joins the next backward(dy, dseq_loss=...)."""
         assert seq_offsets.dtype == torch.int32 and seq_offsets.dim() == 1
         n, E, f32 = seq_offsets.numel() - 1, self.shape.E, torch.float32
         need = L.moe_balance_loss_workspace_bytes(self.p, n)
         ws = self._grown("balance_ws", need, torch.uint8, stream)
-        loss = self._grown("seq_loss", n, f32, stream)
+        loss = self._fresh(n, f32, stream)
         self.seq_counts = self._grown("seq_counts", n * E, torch.int32, stream).view(n, E)
         self.seq_prob = self._grown("seq_prob", n * E, f32, stream).view(n, E)
         L.moe_balance_loss(self.p, self.logits, self.topk_idx, seq_offsets, n, self.seq_counts,

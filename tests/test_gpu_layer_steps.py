@@ -1,5 +1,5 @@
-"""The layer's training options used step by step: a forward of single calls with kept
-checkpoints."""
+"""The layer's training options used step by step and next to other work: a forward of single
+calls with kept checkpoints, losses that a caller keeps."""
 import pytest
 
 import workloads
@@ -69,3 +69,19 @@ def test_forward_in_single_calls(name, gather, packed):
     first.backward(dy)
     for a, b in zip(gradients(first), want):
         assert torch.equal(a, b)
+
+
+def test_kept_losses():
+    """A caller may keep the losses of micro-batches cut into other numbers of sequences."""
+    w, x, dy, layer = make("ragged-bf16", train=True)
+    m = layer()
+    kept = []
+    for n in (7, 3, 1, 9, 7):
+        off = torch.linspace(0, w.T, n + 1).to(torch.int32).cuda()
+        batch = torch.roll(x, n, 0).contiguous()
+        m.forward(batch)
+        loss = m.balance_loss(off)
+        torch.cuda.synchronize()
+        kept.append((loss, loss.clone()))
+    for loss, then in kept:
+        assert torch.equal(loss, then)
