@@ -74,8 +74,9 @@ class Fp8Linear:
     is kept as E4M3 codes with a scale per 128 x 128 block, in both orders; x and dy are
     quantised per 128 along the dimension that each product sums over.
 
-    forward(x [M, K] bf16) -> y [M, N] bf16; backward(dy [M, N] bf16) -> dx [M, K] bf16 and adds
-    dy^T x to self.dw [N, K] fp32 (zero_grad clears it).  Both run on the current stream.
+    forward(x [M, K] bf16) -> y [M, N] bf16; backward(dy [M, N] bf16), of the last forward, ->
+    dx [M, K] bf16 and adds dy^T x to self.dw [N, K] fp32 (zero_grad clears it).  Both run on the
+    current stream; the caller orders the backward's behind the forward's where they differ.
     """
 
     def __init__(self, w: torch.Tensor, train=False):
@@ -110,6 +111,8 @@ class Fp8Linear:
         assert self.train, "construct the layer with train=True"
         assert self._x is not None, "call forward first"
         M, xt, xt_scale = self._x
+        for t in (xt, xt_scale):  # the forward's, perhaps of another stream
+            t.record_stream(torch.cuda.current_stream())
         assert dy.dtype == torch.bfloat16 and dy.shape == (M, self.N)
         q, scale, qt, scale_t = quantize_fp8(dy, True, True)
         dx = torch.empty((M, self.K), dtype=torch.bfloat16, device=dy.device)

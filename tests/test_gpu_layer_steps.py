@@ -1,5 +1,6 @@
 """The layer's training options used step by step and next to other work: a forward of single
-calls with kept checkpoints, losses that a caller keeps."""
+calls with kept checkpoints, losses that a caller keeps, a linear layer whose backward runs on
+another stream."""
 import pytest
 
 import workloads
@@ -85,3 +86,35 @@ def test_kept_losses():
         kept.append((loss, loss.clone()))
     for loss, then in kept:
         assert torch.equal(loss, then)
+
+
+def test_linear_layer_backward_on_another_stream():
+    """The backward on a stream of its own, still running when the next forward begins: the
+    codes that it reads are not handed out again before it has read them."""
+    from mixture_experts_layer_added_amd.layer import Fp8Linear
+    M, N, K = 512, 256, 1024
+    g = torch.Generator(device="cuda").manual_seed(1)
+
+    def rnd(*s):
+        return torch.randn(s, generator=g, device="cuda").bfloat16()
+    w, x, dy = rnd(N, K), rnd(M, K), rnd(M, N)
+    ref = Fp8Linear(w, train=True)
+    ref.forward(x)
+    ref.backward(dy)
+    lin = Fp8Linear(w, train=True)
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    busy = torch.randn((4096, 4096), device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(a):
+        lin.forward(x)
+    b.wait_stream(a)
+    with torch.cuda.stream(b):
+        for _ in range(20):  # holds the stream up for some milliseconds
+            busy = busy @ busy * 1e-2
+        lin.backward(dy)
+    with torch.cuda.stream(a):
+        for _ in range(4):
+            other = x * -3
+            lin.forward(other)
+    torch.cuda.synchronize()
+    assert torch.equal(lin.dw, ref.dw)
