@@ -455,9 +455,11 @@ moe_status moe_balance_loss_backward(const moe_problem* p, const float* logits,
  *   dw_router[e] = sum_t dlogits[t,e] x[t]     [E,H] fp32 out   (fp32, a fixed order).
  *   dlogits [T,E] fp32, e.g. from moe_balance_loss_backward with dgate
  *   ws      >= moe_workspace_bytes(p, MOE_CALL_ROUTER_BACKWARD_DENSE) bytes, 16-byte aligned
- * The products run on 16-bit matrix instructions over parts of the fp32 operands: an error of
- * about 2^-22 of a product's terms (2^-40 of its row's largest term where a term is under 2^-17
- * of that).  Extra limits (checked): T <= 2^25, T*H <= 2^36. */
+ * The products run on bf16 matrix instructions over parts of the fp32 operands, three of 8 bits
+ * each: what is dropped is under 2^-25 of each term (operands' parts below 2^-133, bf16's smallest
+ * step, aside).  A NaN or infinite dlogits[t,e] makes dx_router[t] and dw_router[e] not finite.
+ * fp32 x: |x| at most bf16's largest number, 3.39e38.
+ * Extra limits (checked): T <= 2^25, T*H <= 2^36. */
 moe_status moe_router_backward_dense(const moe_problem* p, const void* x, const float* w_router,
                                      const float* dlogits, float* dx_router, float* dw_router,
                                      void* ws, size_t ws_bytes, void* stream);
