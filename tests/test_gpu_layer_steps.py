@@ -118,3 +118,64 @@ def test_linear_layer_backward_on_another_stream():
             lin.forward(other)
     torch.cuda.synchronize()
     assert torch.equal(lin.dw, ref.dw)
+
+
+@pytest.mark.parametrize("packed", [None, False])
+def test_captured_training_step(packed):
+    """A step with kept checkpoints and the balance loss, captured before its buffers exist and
+    replayed with new batches between eager steps of another layer."""
+    w, x, dy, layer = make("ragged-bf16", gather=True, packed=packed, train=True,
+                           checkpoint8=True)
+    m, eager = layer(), layer()
+    off = torch.tensor([0, w.T // 3, w.T - 1], dtype=torch.int32, device="cuda")
+    dl = torch.tensor([0.5, -1.0], device="cuda")
+    xin, dyin = x.clone(), dy.clone()
+    m.forward(xin)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        m.forward(xin)
+        loss = m.balance_loss(off)
+        m.backward(dyin, dseq_loss=dl)
+    for i in range(4):
+        xin.copy_(torch.roll(x, i, 0))
+        dyin.copy_(dy * (1 + i))
+        eager.forward(xin)
+        want = eager.balance_loss(off)
+        eager.backward(dyin, dseq_loss=dl)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(loss, want), i
+        for a, b in zip(gradients(m), gradients(eager)):
+            assert torch.equal(a, b), i
+
+
+@pytest.mark.parametrize("M", [1, 150])
+def test_captured_linear_layer(M):
+    from mixture_experts_layer_added_amd.layer import Fp8Linear
+    N, K = 256, 512
+    g = torch.Generator(device="cuda").manual_seed(M)
+
+    def rnd(*s):
+        return torch.randn(s, generator=g, device="cuda").bfloat16()
+    w, x, dy = rnd(N, K), rnd(M, K), rnd(M, N)
+    lin, eager = Fp8Linear(w, train=True), Fp8Linear(w, train=True)
+    lin.forward(x)
+    lin.backward(dy)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        y = lin.forward(x)
+        dx = lin.backward(dy)
+    lin.zero_grad()
+    for i in range(4):
+        x.copy_(rnd(M, K))
+        dy.copy_(rnd(M, N))
+        ey = eager.forward(x)
+        ex = eager.backward(dy)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, ey) and torch.equal(dx, ex), i
+        assert torch.equal(lin.dw, eager.dw), i
