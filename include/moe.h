@@ -519,7 +519,8 @@ moe_status moe_quantize_fp8(const void* x, int32_t dtype, int64_t rows, int64_t 
  * A linear layer y = x W^T: a = x by rows, b = W; its gradients: dx = dy W with a = dy by rows,
  * b = W^T; dW = dy^T x with a = dy, b = x, both by columns (moe_quantize_fp8's transposes).
  * bf16 C: a block's sum of products is the FP8 matrix instruction's, which keeps 13 bits below the
- * largest of each 8 products; fp32 C: fp32 sums.
+ * largest of each 8 products; fp32 C: fp32 sums.  The product of the two scales is formed first: it
+ * loses bits below 2^-126 and must not pass fp32's largest number.
  * Any M, N, K >= 1.  Code bytes past K in a row are ignored.  Limits (checked): lda, ldb
  * multiples of 16, >= K and at most 2^22; ldc >= N; M, N <= 2^26, M*N <= 2^37; a, b, c 16-byte
  * aligned, c apart from a and b.  A matrix's last row is read up to K rounded up to 16, the

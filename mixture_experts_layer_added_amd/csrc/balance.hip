@@ -270,9 +270,11 @@ __global__ __launch_bounds__(1024) void k_balance_seq(
   }
 }
 
-// A small batch (T <= kShort): one workgroup per sequence does all of it, in one launch (loss and
-// gradient of 128 x 256: 13.9 us, in two launches 16.8; of 600 x 256 as one sequence 26.2 against
-// 16.4).
+// A small batch (T <= kShort): one workgroup per sequence does all of it, in one launch.  Loss and
+// gradient of 128 x 256: 13.5 us, in two launches 16.8; of 512 x 256 in four sequences 14.6, of 513
+// in two launches 17.4.  The rule goes by T alone, so it also holds where a batch is one
+// sequence, and there from about 300 tokens on the two launches would be the faster ones: 300
+// tokens 16.8 us, 512 22.7, 513 in two launches 16.5.
 constexpr int kShort = 512;
 template <int LP, int SL, bool kVec, bool kFull>
 __global__ __launch_bounds__(1024) void k_balance_short(
