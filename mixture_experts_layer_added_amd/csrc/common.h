@@ -80,7 +80,8 @@ __device__ __forceinline__ float bf16_bits_to_f32(uint16_t b) {
   return __uint_as_float(static_cast<uint32_t>(b) << 16);
 }
 
-// Round-to-nearest-even float -> bf16 bits (inputs are finite on every path here).
+// Round-to-nearest-even float -> bf16 bits.  A NaN as arithmetic makes it (quiet, of a short
+// payload) stays one, an infinity too.
 __device__ __forceinline__ uint16_t f32_to_bf16_bits(float f) {
   uint32_t u = __float_as_uint(f);
   u += 0x7FFFu + ((u >> 16) & 1u);

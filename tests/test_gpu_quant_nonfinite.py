@@ -161,3 +161,40 @@ def test_expert_backward_from_the_codes():
     assert int(dau[5].isnan().sum()) == 2 and int(h[5].isnan().sum()) == 1
     assert bool(dau[17, :I].isnan().all()) and bool(h[17].isnan().all())
     assert bool(dx[5].isnan().all()) and bool(dx[17].isnan().all())
+
+
+@pytest.mark.parametrize("M", [1, 40, 300])
+@pytest.mark.parametrize("bad", [NAN, INF, -INF])
+def test_linear_layer(M, bad):
+    """A NaN or infinite activation reaches its token's outputs and its column of dw, one in the
+    gradient its token's dx and its row of dw; everything else is as without it."""
+    from mixture_experts_layer_added_amd.layer import Fp8Linear
+    N, K, r = 256, 384, M - 1
+    g = torch.Generator(device="cuda").manual_seed(M)
+
+    def rnd(*s):
+        return torch.randn(s, generator=g, device="cuda").bfloat16()
+    w, x, dy = rnd(N, K), rnd(M, K), rnd(M, N)
+
+    def step(x, dy):
+        lin = Fp8Linear(w, train=True)
+        y = lin.forward(x)
+        dx = lin.backward(dy)
+        torch.cuda.synchronize()
+        return y.cpu(), dx.cpu(), lin.dw.cpu()
+    y0, dx0, dw0 = step(x, dy)
+    rows = torch.arange(M) != r
+    xb = x.clone()
+    xb[r, 200] = bad
+    y, dx, dw = step(xb, dy)
+    cols = torch.arange(K) != 200
+    assert bool(y[r].isnan().all()) and torch.equal(y[rows], y0[rows])
+    assert torch.equal(dx, dx0)
+    assert bool(dw[:, 200].isnan().all()) and torch.equal(dw[:, cols], dw0[:, cols])
+    db = dy.clone()
+    db[r, 70] = bad
+    y, dx, dw = step(x, db)
+    outs = torch.arange(N) != 70
+    assert torch.equal(y, y0)
+    assert bool(dx[r].isnan().all()) and torch.equal(dx[rows], dx0[rows])
+    assert bool(dw[70].isnan().all()) and torch.equal(dw[outs], dw0[outs])
