@@ -41,7 +41,7 @@
  * 32-bit byte offsets); 1 <= E <= 512, E % G == 0, 1 <= G <= 64,
  * 1 <= M <= G, 1 <= J <= min(E/G, 8), 1 <= K <= min(M*E/G, 16); S in {0, 1}.
  * Dtypes: act_dtype F32 with expert_dtype F32, or act_dtype BF16 with expert_dtype
- * BF16 or FP8_E4M3.  Inputs must be finite.
+ * BF16 or FP8_E4M3.  Inputs must be finite, but where a call says what becomes of others.
  */
 #ifndef MOE_H
 #define MOE_H
