@@ -61,7 +61,7 @@ typedef enum {
   MOE_ERR_HIP = -4          /* a HIP runtime call or kernel launch failed */
 } moe_status;
 
-typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3 = 2 } moe_dtype;
+typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3 = 2, MOE_MXFP4 = 3 } moe_dtype;
 
 typedef struct moe_problem {
   int64_t T;            /* tokens in the batch (one step)                              */
@@ -74,7 +74,7 @@ typedef struct moe_problem {
   int32_t I;            /* FFN (SwiGLU) width of every expert                          */
   int32_t S;            /* shared experts: 0 or 1                                      */
   int32_t act_dtype;    /* moe_dtype of x, y_sorted and y: MOE_F32 | MOE_BF16           */
-  int32_t expert_dtype; /* moe_dtype of the GEMM operands: MOE_F32 | MOE_BF16 | FP8     */
+  int32_t expert_dtype; /* of the GEMM operands: MOE_F32 | MOE_BF16 | FP8 | MXFP4       */
 } moe_problem;
 
 /* Rows of the permuted buffers: R = T*K + S*T (routed rows, then T shared rows). */
@@ -530,6 +530,133 @@ moe_status moe_gemm_fp8(int64_t M, int64_t N, int64_t K, const void* a, int64_t 
                         const float* a_scale, const void* b, int64_t ldb, const float* b_scale,
                         int32_t b_rows, void* c, int64_t ldc, int32_t c_dtype, int32_t accumulate,
                         void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------- microscaled 4-bit floating point (MXFP4) ----------------
+ * Blocks of 32 elements along a row: E2M1 codes (+-0, 0.5, 1, 1.5, 2, 3, 4, 6), two a byte with
+ * the even element in the low four bits, and one E8M0 scale code E a block, 2^(E - 127); E = 255
+ * is NaN and makes the block NaN.  In memory
+ *   codes  [rows, ldq]  bytes: 16 a block, ldq a multiple of 16 and at least 16*ceil(cols/32)
+ *   scales [rows, lds]  bytes: 1 a block, lds a multiple of 16 and at least ceil(cols/32)
+ * both 16-byte aligned.  What lies in a row behind its last block is neither written nor used
+ * (it may be read).
+ *
+ * Quantisation of x [rows, cols] (MOE_BF16 or MOE_F32, row stride ldx elements).  With m 2^x, 1 <=
+ * m < 2, the block's largest |element|: E = x - 2 + 127, one more from m = 1.75 on, where that
+ * element would round past 6; at least 0; 127 for a block of zeros.  code = x / 2^(E-127) to the
+ * nearest, ties to the even code.  A NaN or an infinity makes its block NaN (E = 255, codes 0).
+ *   q, scale     blocks along the rows of x, or both NULL
+ *   qt, scale_t  the transpose [cols, .], blocks along the columns of x, or both NULL (one of the
+ *                two forms is required; both come from one read of x)
+ *   random       NULL, or [rows, cols] bytes, contiguous: stochastic rounding, for gradients.  An
+ *                element between two codes goes to the upper one (in magnitude) where the part
+ *                of the step above the lower one exceeds (byte + 1/2)/256; E is one more from m >
+ *                1.5 on already, so that no element lies past 6.  The mean over all bytes is off
+ *                by at most 1/512 of a step.  Both forms use an element's one byte.
+ * Codes of a last block past cols are 0.  Limits (checked): rows, cols >= 1, ldx >= cols, x aligned
+ * to its element, fewer than 2^31 blocks of 128 x 128, with qt fewer than 2^24. */
+moe_status moe_quantize_mxfp4(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ldx,
+                              void* q, int64_t ldq, void* scale, int64_t lds, void* qt,
+                              int64_t ldqt, void* scale_t, int64_t ldst, const void* random,
+                              void* stream);
+
+/* The values again: out [rows, ldo] (MOE_BF16 or MOE_F32) = code 2^(E-127), exact in both types
+ * (E = 254: infinite from code 4, 2^128, on), NaN where E = 255. */
+moe_status moe_dequantize_mxfp4(int64_t rows, int64_t cols, const void* q, int64_t ldq,
+                                const void* scale, int64_t lds, void* out, int64_t ldo,
+                                int32_t dtype, void* stream);
+
+/* C = A B^T over MXFP4 operands, fp32 sums, rounded once at the end.
+ *   a [M, lda], a_scale [M, ldsa]; b [N, ldb], b_scale [N, ldsb]: K columns each
+ *   c [M, ldc] out, c_dtype MOE_BF16 or MOE_F32; accumulate = 1 (MOE_F32 only): C += A B^T
+ *   ws >= moe_gemm_mxfp4_workspace_bytes(M, N, K) bytes, 16-byte aligned (may be NULL if 0)
+ * A linear layer y = x W^T: a = x by rows, b = W; its gradients: dx = dy W with a = dy by rows, b =
+ * W's transposed form; dW = dy^T x with both transposed forms (moe_quantize_mxfp4).
+ * Any M, N, K >= 1; codes of a last block past K are ignored.  A NaN block makes its row's (a) or
+ * column's (b) results NaN.  Limits (checked): M, N <= 2^26, M*N <= 2^37, K <= 2^22, strides at
+ * most 2^22, ldc >= N; c 16-byte aligned and apart from the operands.  Codes of a matrix's last row
+ * are read up to its last block, the other rows' and all scales up to their stride. */
+size_t moe_gemm_mxfp4_workspace_bytes(int64_t M, int64_t N, int64_t K);
+moe_status moe_gemm_mxfp4(int64_t M, int64_t N, int64_t K, const void* a, int64_t lda,
+                          const void* a_scale, int64_t ldsa, const void* b, int64_t ldb,
+                          const void* b_scale, int64_t ldsb, void* c, int64_t ldc, int32_t c_dtype,
+                          int32_t accumulate, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------- experts in MXFP4 (act_dtype MOE_BF16, expert_dtype MOE_MXFP4) ----------------
+ * h = mx(silu(x W1^T) (x W3^T)), y = h W2^T per group, mx the quantisation above along a row: 0.53
+ * bytes a weight in place of 1 or 2.  moe_route, moe_permute (x_sorted NULL), moe_combine and
+ * moe_bias_update go with it; the other expert calls and the backward refuse this type.
+ *
+ * Offline: w13 [E+S, 2I, H/2] and w13_scale [E+S, 2I, H/32], w2 [E+S, H, I/2] and w2_scale
+ * [E+S, H, I/32] (contiguous, as moe_quantize_mxfp4 writes them with the smallest strides where
+ * those are multiples of 16) -> packed copies, moe_mxfp4_packed_bytes(E+S, 2I, H) and (E+S, H, I)
+ * bytes, codes and scales in the order in which the products read them.  One of w13_packed and
+ * w2_packed may be NULL, with its inputs.  16-byte alignment throughout. */
+size_t moe_mxfp4_packed_bytes(int64_t batch, int64_t rows, int64_t cols);
+moe_status moe_pack_expert_weights_mxfp4(const moe_problem* p, const void* w13,
+                                         const void* w13_scale, const void* w2,
+                                         const void* w2_scale, void* w13_packed, void* w2_packed,
+                                         void* stream);
+
+/* x_q [T, H/2], x_scale [T, ldxs] (moe_quantize_mxfp4 of x) -> h_q [R, I/2], h_scale [R, ldhs].
+ * Row r of group g, offsets[g] <= r < offsets[g+1], is token sorted_token[r]; rows of no group are
+ * left as they were, groups may be empty.  offsets [E+S+1] ascending, within [0, R]; sorted_token
+ * within [0, T).  Limits (checked): T*H/2 and T*ldxs < 2^31 - 16. */
+moe_status moe_expert_ffn_up_mxfp4(const moe_problem* p, const void* x_q, const void* x_scale,
+                                   int64_t ldxs, const int32_t* sorted_token,
+                                   const int32_t* offsets, const void* w13_packed, void* h_q,
+                                   void* h_scale, int64_t ldhs, void* stream);
+/* h_q, h_scale -> y_sorted [R, H] bf16. */
+moe_status moe_expert_ffn_down_mxfp4(const moe_problem* p, const void* h_q, const void* h_scale,
+                                     int64_t ldhs, const int32_t* offsets, const void* w2_packed,
+                                     void* y_sorted, void* stream);
+
+/* ---------------- a share of the experts ----------------
+ * For a GPU that holds experts first .. first+count-1 of a layer spread over several: the tokens
+ * that chose them, sorted by expert, and back, with the gates on either way, and the gradients.
+ * moe_permute in contrast takes a whole layer's experts and gives every choice a row.
+ *
+ * Sorting.  Pair (t, k) has index t*K + k.  Rows are grouped by expert in index order, pairs
+ * ascending within an expert.
+ *   topk_idx     [T,K] int32: any value; those outside [first, first+count) are not here
+ *   offsets      [count+1] int32 out: first row of each expert; offsets[count] = pairs that are here
+ *   sorted_token [T*K] int32 out: token of each row; entries behind offsets[count] are left as
+ *                they were
+ *   pair_row     [T,K] int32 out: row of each pair, -1 where its expert is not here
+ *   ws >= moe_sort_by_expert_workspace_bytes(T, K, count) bytes, 16-byte aligned
+ * A token may choose an expert more than once.  T = 0 is allowed, here and below (the other
+ * pointers are then not used).  Bit-for-bit reproducible.  Limits (checked): K in [1,16], count in
+ * [1,512], T*K < 2^31 - 1024 K. */
+size_t moe_sort_by_expert_workspace_bytes(int64_t T, int32_t K, int32_t count);
+moe_status moe_sort_by_expert(int64_t T, int32_t K, const int32_t* topk_idx, int32_t first,
+                              int32_t count, int32_t* offsets, int32_t* sorted_token,
+                              int32_t* pair_row, void* ws, size_t ws_bytes, void* stream);
+
+/* To the experts and back.  w = weights [T,K] fp32, or NULL: 1.  r(t,k) = pair_row[t,k]; a pair
+ * with a negative row takes no part.  dtype: MOE_BF16 or MOE_F32, of every matrix; strides in
+ * elements; fp32 arithmetic in the order of k, rounded once.
+ *   moe_dispatch           x_sorted[r(t,k)] = w[t,k] x[t]             (other rows left as they were)
+ *   moe_dispatch_backward  dx[t] = sum_k w[t,k] dx_sorted[r(t,k)],
+ *                          dweights[t,k] = <x[t], dx_sorted[r(t,k)]>  (0 without a row)
+ *   moe_collect            y[t] = sum_k w[t,k] y_sorted[r(t,k)]       (zeros without a row)
+ *   moe_collect_backward   dy_sorted[r(t,k)] = w[t,k] dy[t]           (other rows left as they were),
+ *                          dweights[t,k] = <dy[t], y_sorted[r(t,k)]>  (0 without a row)
+ * dweights [T,K] fp32 or NULL (then x, y_sorted of the backward calls are not read); it needs
+ * weights.  The rows of different pairs must differ.  Any H in [1, 2^20], any stride >= H up to
+ * 2^31; rows at multiples of 16 bytes move in 16-byte pieces, others element by element. */
+moe_status moe_dispatch(int32_t dtype, int64_t T, int32_t K, int64_t H, const void* x, int64_t ldx,
+                        const int32_t* pair_row, const float* weights, void* x_sorted, int64_t ldxs,
+                        void* stream);
+moe_status moe_dispatch_backward(int32_t dtype, int64_t T, int32_t K, int64_t H,
+                                 const void* dx_sorted, int64_t lddxs, const int32_t* pair_row,
+                                 const float* weights, const void* x, int64_t ldx, void* dx,
+                                 int64_t lddx, float* dweights, void* stream);
+moe_status moe_collect(int32_t dtype, int64_t T, int32_t K, int64_t H, const void* y_sorted,
+                       int64_t ldys, const int32_t* pair_row, const float* weights, void* y,
+                       int64_t ldy, void* stream);
+moe_status moe_collect_backward(int32_t dtype, int64_t T, int32_t K, int64_t H, const void* dy,
+                                int64_t lddy, const int32_t* pair_row, const float* weights,
+                                const void* y_sorted, int64_t ldys, void* dy_sorted, int64_t lddys,
+                                float* dweights, void* stream);
 
 /* Text of a status code, and the last error message of the calling thread. */
 const char* moe_status_str(moe_status s);

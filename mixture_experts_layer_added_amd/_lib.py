@@ -14,7 +14,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmoe.so")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = 0, -1, -2, -3, -4
-MOE_F32, MOE_BF16, MOE_FP8_E4M3 = 0, 1, 2
+MOE_F32, MOE_BF16, MOE_FP8_E4M3, MOE_MXFP4 = 0, 1, 2, 3
 MOE_CALL_ROUTE, MOE_CALL_PERMUTE, MOE_CALL_EXPERT_FFN = 0, 1, 2
 MOE_CALL_ROUTER_BACKWARD_DENSE = 3
 
@@ -31,7 +31,12 @@ EXPORTS = ("moe_route", "moe_permute", "moe_expert_ffn", "moe_expert_ffn_up",
            "moe_balance_loss", "moe_balance_loss_backward", "moe_router_backward_dense",
            "moe_checkpoint_save", "moe_checkpoint_restore",
            "moe_expert_ffn_backward_input_checkpoint", "moe_quantize_fp8",
-           "moe_gemm_fp8_workspace_bytes", "moe_gemm_fp8")
+           "moe_gemm_fp8_workspace_bytes", "moe_gemm_fp8",
+           "moe_quantize_mxfp4", "moe_dequantize_mxfp4", "moe_gemm_mxfp4_workspace_bytes",
+           "moe_gemm_mxfp4", "moe_mxfp4_packed_bytes", "moe_pack_expert_weights_mxfp4",
+           "moe_expert_ffn_up_mxfp4", "moe_expert_ffn_down_mxfp4",
+           "moe_sort_by_expert_workspace_bytes", "moe_sort_by_expert", "moe_dispatch",
+           "moe_dispatch_backward", "moe_collect", "moe_collect_backward")
 
 
 class MoeError(RuntimeError):
@@ -99,6 +104,26 @@ def lib():
         L.moe_quantize_fp8.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, vp, i64, vp, vp]
         L.moe_gemm_fp8.argtypes = [i64, i64, i64, vp, i64, vp, vp, i64, vp, i32, vp, i64, i32, i32,
                                    vp, sz, vp]
+        L.moe_quantize_mxfp4.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64,
+                                         vp, vp]
+        L.moe_dequantize_mxfp4.argtypes = [i64, i64, vp, i64, vp, i64, vp, i64, i32, vp]
+        L.moe_gemm_mxfp4.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i32,
+                                     i32, vp, sz, vp]
+        L.moe_pack_expert_weights_mxfp4.argtypes = [pp, vp, vp, vp, vp, vp, vp, vp]
+        L.moe_expert_ffn_up_mxfp4.argtypes = [pp, vp, vp, i64, vp, vp, vp, vp, vp, i64, vp]
+        L.moe_expert_ffn_down_mxfp4.argtypes = [pp, vp, vp, i64, vp, vp, vp, vp]
+        L.moe_sort_by_expert.argtypes = [i64, i32, vp, i32, i32, vp, vp, vp, vp, sz, vp]
+        L.moe_dispatch.argtypes = [i32, i64, i32, i64, vp, i64, vp, vp, vp, i64, vp]
+        L.moe_dispatch_backward.argtypes = [i32, i64, i32, i64, vp, i64, vp, vp, vp, i64, vp, i64,
+                                            vp, vp]
+        L.moe_collect.argtypes = L.moe_dispatch.argtypes
+        L.moe_collect_backward.argtypes = L.moe_dispatch_backward.argtypes
+        L.moe_gemm_mxfp4_workspace_bytes.argtypes = [i64, i64, i64]
+        L.moe_gemm_mxfp4_workspace_bytes.restype = sz
+        L.moe_mxfp4_packed_bytes.argtypes = [i64, i64, i64]
+        L.moe_mxfp4_packed_bytes.restype = sz
+        L.moe_sort_by_expert_workspace_bytes.argtypes = [i64, i32, i32]
+        L.moe_sort_by_expert_workspace_bytes.restype = sz
         L.moe_balance_loss_workspace_bytes.argtypes = [pp, i32]
         L.moe_balance_loss_workspace_bytes.restype = sz
         L.moe_gemm_fp8_workspace_bytes.argtypes = [i64, i64, i64]
@@ -122,7 +147,11 @@ def lib():
                   "moe_balance_loss_backward", "moe_router_backward_dense",
                   "moe_checkpoint_save", "moe_checkpoint_restore",
                   "moe_expert_ffn_backward_input_checkpoint", "moe_quantize_fp8",
-                  "moe_gemm_fp8"):
+                  "moe_gemm_fp8",
+                  "moe_quantize_mxfp4", "moe_dequantize_mxfp4", "moe_gemm_mxfp4",
+                  "moe_pack_expert_weights_mxfp4", "moe_expert_ffn_up_mxfp4",
+                  "moe_expert_ffn_down_mxfp4", "moe_sort_by_expert", "moe_dispatch",
+                  "moe_dispatch_backward", "moe_collect", "moe_collect_backward"):
             getattr(L, n).restype = i32
         _lib = L
     return _lib
@@ -420,3 +449,99 @@ def moe_gemm_fp8(M, N, K, a, lda, a_scale, b, ldb, b_scale, b_rows, c, ldc, c_dt
     a, sa, b, sb, c, w = _ptrs("moe_gemm_fp8", a, a_scale, b, b_scale, c, ws)
     _check(lib().moe_gemm_fp8(M, N, K, a, lda, sa, b, ldb, sb, b_rows, c, ldc, c_dtype,
                               accumulate, w, ws_bytes, _stream(stream)), "moe_gemm_fp8")
+
+
+def _sized(call, n):
+    """A size in bytes; a refused call's is 0, of which last_error() says why."""
+    if n == 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, call, last_error())
+    return n
+
+
+def moe_quantize_mxfp4(x, dtype, rows, cols, ldx, q, ldq, scale, lds, qt=None, ldqt=0, scale_t=None,
+                       ldst=0, random=None, stream=None):
+    x, q, s, qt, st, r = _ptrs("moe_quantize_mxfp4", x, q, scale, qt, scale_t, random)
+    _check(lib().moe_quantize_mxfp4(x, dtype, rows, cols, ldx, q, ldq, s, lds, qt, ldqt, st, ldst, r,
+                                    _stream(stream)), "moe_quantize_mxfp4")
+
+
+def moe_dequantize_mxfp4(rows, cols, q, ldq, scale, lds, out, ldo, dtype, stream=None):
+    q, s, out = _ptrs("moe_dequantize_mxfp4", q, scale, out)
+    _check(lib().moe_dequantize_mxfp4(rows, cols, q, ldq, s, lds, out, ldo, dtype, _stream(stream)),
+           "moe_dequantize_mxfp4")
+
+
+def moe_gemm_mxfp4_workspace_bytes(M, N, K) -> int:
+    return lib().moe_gemm_mxfp4_workspace_bytes(M, N, K)
+
+
+def moe_gemm_mxfp4(M, N, K, a, lda, a_scale, ldsa, b, ldb, b_scale, ldsb, c, ldc, c_dtype=MOE_BF16,
+                   accumulate=0, ws=None, ws_bytes=0, stream=None):
+    a, sa, b, sb, c, w = _ptrs("moe_gemm_mxfp4", a, a_scale, b, b_scale, c, ws)
+    _check(lib().moe_gemm_mxfp4(M, N, K, a, lda, sa, ldsa, b, ldb, sb, ldsb, c, ldc, c_dtype,
+                                accumulate, w, ws_bytes, _stream(stream)), "moe_gemm_mxfp4")
+
+
+def moe_mxfp4_packed_bytes(batch, rows, cols) -> int:
+    return _sized("moe_mxfp4_packed_bytes", lib().moe_mxfp4_packed_bytes(batch, rows, cols))
+
+
+def moe_pack_expert_weights_mxfp4(p, w13, w13_scale, w2, w2_scale, w13_packed, w2_packed,
+                                  stream=None):
+    a = _ptrs("moe_pack_expert_weights_mxfp4", w13, w13_scale, w2, w2_scale, w13_packed, w2_packed)
+    _check(lib().moe_pack_expert_weights_mxfp4(ctypes.byref(p), *a, _stream(stream)),
+           "moe_pack_expert_weights_mxfp4")
+
+
+def moe_expert_ffn_up_mxfp4(p, x_q, x_scale, ldxs, sorted_token, offsets, w13_packed, h_q, h_scale,
+                            ldhs, stream=None):
+    x, s, t, o, w, h, hs = _ptrs("moe_expert_ffn_up_mxfp4", x_q, x_scale, sorted_token, offsets,
+                                 w13_packed, h_q, h_scale)
+    _check(lib().moe_expert_ffn_up_mxfp4(ctypes.byref(p), x, s, ldxs, t, o, w, h, hs, ldhs,
+                                         _stream(stream)), "moe_expert_ffn_up_mxfp4")
+
+
+def moe_expert_ffn_down_mxfp4(p, h_q, h_scale, ldhs, offsets, w2_packed, y_sorted, stream=None):
+    h, hs, o, w, y = _ptrs("moe_expert_ffn_down_mxfp4", h_q, h_scale, offsets, w2_packed, y_sorted)
+    _check(lib().moe_expert_ffn_down_mxfp4(ctypes.byref(p), h, hs, ldhs, o, w, y, _stream(stream)),
+           "moe_expert_ffn_down_mxfp4")
+
+
+def moe_sort_by_expert_workspace_bytes(T, K, count) -> int:
+    return _sized("moe_sort_by_expert_workspace_bytes",
+                  lib().moe_sort_by_expert_workspace_bytes(T, K, count))
+
+
+def moe_sort_by_expert(T, K, topk_idx, first, count, offsets, sorted_token, pair_row, ws, ws_bytes,
+                       stream=None):
+    i, o, t, r, w = _ptrs("moe_sort_by_expert", topk_idx, offsets, sorted_token, pair_row, ws)
+    _check(lib().moe_sort_by_expert(T, K, i, first, count, o, t, r, w, ws_bytes, _stream(stream)),
+           "moe_sort_by_expert")
+
+
+def moe_dispatch(dtype, T, K, H, x, ldx, pair_row, weights, x_sorted, ldxs, stream=None):
+    x, r, w, xs = _ptrs("moe_dispatch", x, pair_row, weights, x_sorted)
+    _check(lib().moe_dispatch(dtype, T, K, H, x, ldx, r, w, xs, ldxs, _stream(stream)),
+           "moe_dispatch")
+
+
+def moe_dispatch_backward(dtype, T, K, H, dx_sorted, lddxs, pair_row, weights, x, ldx, dx, lddx,
+                          dweights=None, stream=None):
+    d, r, w, x, dx, dw = _ptrs("moe_dispatch_backward", dx_sorted, pair_row, weights, x, dx,
+                               dweights)
+    _check(lib().moe_dispatch_backward(dtype, T, K, H, d, lddxs, r, w, x, ldx, dx, lddx, dw,
+                                       _stream(stream)), "moe_dispatch_backward")
+
+
+def moe_collect(dtype, T, K, H, y_sorted, ldys, pair_row, weights, y, ldy, stream=None):
+    ys, r, w, y = _ptrs("moe_collect", y_sorted, pair_row, weights, y)
+    _check(lib().moe_collect(dtype, T, K, H, ys, ldys, r, w, y, ldy, _stream(stream)),
+           "moe_collect")
+
+
+def moe_collect_backward(dtype, T, K, H, dy, lddy, pair_row, weights, y_sorted, ldys, dy_sorted,
+                         lddys, dweights=None, stream=None):
+    d, r, w, ys, o, dw = _ptrs("moe_collect_backward", dy, pair_row, weights, y_sorted, dy_sorted,
+                               dweights)
+    _check(lib().moe_collect_backward(dtype, T, K, H, d, lddy, r, w, ys, ldys, o, lddys, dw,
+                                      _stream(stream)), "moe_collect_backward")

@@ -75,7 +75,8 @@ moe_status validate(const moe_problem* p, Dims* d) {
   if (p->S != 0 && p->S != 1) return fail(MOE_ERR_INVALID_ARG, "S=%d must be 0 or 1", p->S);
   const bool ok_dtypes = (p->act_dtype == MOE_F32 && p->expert_dtype == MOE_F32) ||
                          (p->act_dtype == MOE_BF16 &&
-                          (p->expert_dtype == MOE_BF16 || p->expert_dtype == MOE_FP8_E4M3));
+                          (p->expert_dtype == MOE_BF16 || p->expert_dtype == MOE_FP8_E4M3 ||
+                           p->expert_dtype == MOE_MXFP4));
   if (!ok_dtypes)
     return fail(MOE_ERR_INVALID_ARG, "dtypes act=%d expert=%d not supported", p->act_dtype,
                 p->expert_dtype);
@@ -125,7 +126,12 @@ size_t moe_workspace_bytes(const moe_problem* p, int32_t which_call) {
   switch (which_call) {
     case MOE_CALL_ROUTE: return route_ws_bytes(d);
     case MOE_CALL_PERMUTE: return permute_ws_bytes(d);
-    case MOE_CALL_EXPERT_FFN: return ffn_ws_bytes(d);
+    case MOE_CALL_EXPERT_FFN:
+      if (d.expert == MOE_MXFP4) {
+        fail(MOE_ERR_UNSUPPORTED, "moe_expert_ffn is not built for MXFP4 experts");
+        return 0;
+      }
+      return ffn_ws_bytes(d);
     case MOE_CALL_ROUTER_BACKWARD_DENSE: return router_dense_ws_bytes(d);
   }
   fail(MOE_ERR_INVALID_ARG, "unknown call id %d", which_call);
@@ -166,6 +172,8 @@ moe_status moe_permute(const moe_problem* p, const void* x, const int32_t* topk_
   if (!topk_idx || !offsets || !sorted_token || !inv_perm)
     return fail(MOE_ERR_INVALID_ARG, "topk_idx, offsets, sorted_token and inv_perm are required");
   if (x_sorted) {  // NULL: index maps only
+    if (d.expert == MOE_MXFP4)
+      return fail(MOE_ERR_UNSUPPORTED, "MXFP4 experts gather their rows: x_sorted must be NULL");
     REQUIRE_PTR(x);
     REQUIRE_PTR(x_sorted);
     if (d.expert == MOE_FP8_E4M3 && !x_sorted_scale)
@@ -201,6 +209,8 @@ moe_status moe_permute_noalloc(const moe_problem* p, const void* x, const int32_
   if (!topk_idx || !offsets || !sorted_token || !inv_perm)
     return fail(MOE_ERR_INVALID_ARG, "topk_idx, offsets, sorted_token and inv_perm are required");
   if (x_sorted) {  // NULL: index maps only
+    if (d.expert == MOE_MXFP4)
+      return fail(MOE_ERR_UNSUPPORTED, "MXFP4 experts gather their rows: x_sorted must be NULL");
     REQUIRE_PTR(x);
     REQUIRE_PTR(x_sorted);
     if (d.expert == MOE_FP8_E4M3 && !x_sorted_scale)
@@ -311,6 +321,8 @@ moe_status moe_expert_ffn(const moe_problem* p, const void* x_sorted,
   Dims d;
   moe_status s = validate(p, &d);
   if (s != MOE_OK) return s;
+  if (d.expert == MOE_MXFP4)
+    return fail(MOE_ERR_UNSUPPORTED, "moe_expert_ffn is not built for MXFP4 experts");
   REQUIRE_PTR(x_sorted);
   REQUIRE_PTR(w13);
   REQUIRE_PTR(w2);
@@ -375,7 +387,7 @@ moe_status moe_seq_load_stats(const moe_problem* p, const int32_t* topk_idx,
 }
 
 static moe_status require_no_fp8(const Dims& d, const char* call) {
-  if (d.expert == MOE_FP8_E4M3)
+  if (d.expert == MOE_FP8_E4M3 || d.expert == MOE_MXFP4)
     return fail(MOE_ERR_UNSUPPORTED, "%s: the backward is built for the bf16 and fp32 paths", call);
   return MOE_OK;
 }
@@ -892,6 +904,350 @@ moe_status moe_gemm_fp8(int64_t M, int64_t N, int64_t K, const void* a, int64_t 
       b_scale, b_rows, c, ldc, c_dtype == MOE_F32, accumulate, ws,
       static_cast<hipStream_t>(stream));
   return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_gemm_fp8 launch");
+}
+
+// ---- MXFP4 ----
+static moe_status require_mxfp4(const Dims& d, const char* call) {
+  if (d.expert != MOE_MXFP4)
+    return fail(MOE_ERR_INVALID_ARG, "%s needs act BF16 and expert MXFP4", call);
+  return MOE_OK;
+}
+
+// codes and scales of a quantised matrix [rows, cols]: `name` in messages
+static moe_status check_mx(const char* name, const void* q, int64_t ldq, const void* scale,
+                           int64_t lds, int64_t cols) {
+  const int64_t kb = (cols + 31) / 32;
+  if (!aligned16(q) || ldq % 16 || ldq < 16 * kb)
+    return fail(MOE_ERR_INVALID_ARG,
+                "%s needs 16-byte alignment and a row stride of at least 16*ceil(%lld/32) bytes, a "
+                "multiple of 16", name, (long long)cols);
+  if (!scale || !aligned16(scale) || lds % 16 || lds < kb)
+    return fail(MOE_ERR_INVALID_ARG,
+                "%s's scales need 16-byte alignment and a row stride of at least ceil(%lld/32) "
+                "bytes, a multiple of 16", name, (long long)cols);
+  return MOE_OK;
+}
+
+moe_status moe_quantize_mxfp4(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ldx,
+                              void* q, int64_t ldq, void* scale, int64_t lds, void* qt,
+                              int64_t ldqt, void* scale_t, int64_t ldst, const void* random,
+                              void* stream) {
+  if (dtype != MOE_BF16 && dtype != MOE_F32)
+    return fail(MOE_ERR_INVALID_ARG, "dtype=%d must be MOE_BF16 or MOE_F32", dtype);
+  constexpr int64_t kMost = (int64_t)1 << 40;
+  if (rows < 1 || cols < 1 || rows > kMost || cols > kMost)
+    return fail(MOE_ERR_INVALID_ARG, "rows and cols must be in [1, 2^40]");
+  // the transpose takes a workgroup of 256 threads a block, and a launch holds fewer than 2^32
+  if (((rows + 127) / 128) * (double)((cols + 127) / 128) >= (qt ? 16777216.0 : 2147483648.0))
+    return fail(MOE_ERR_INVALID_ARG, "too many 128x128 blocks");
+  if (ldx < cols) return fail(MOE_ERR_INVALID_ARG, "ldx=%lld < cols", (long long)ldx);
+  if (!x || (reinterpret_cast<uintptr_t>(x) & (dtype == MOE_F32 ? 3 : 1)))
+    return fail(MOE_ERR_INVALID_ARG, "x is NULL or not aligned to its element");
+  if (!q && !qt) return fail(MOE_ERR_INVALID_ARG, "q and qt are both NULL");
+  moe_status s;
+  if (q && (s = check_mx("q", q, ldq, scale, lds, cols)) != MOE_OK) return s;
+  if (qt && (s = check_mx("qt", qt, ldqt, scale_t, ldst, rows)) != MOE_OK) return s;
+  const void* outs[4] = {q, q ? scale : nullptr, qt, qt ? scale_t : nullptr};
+  for (int i = 0; i < 4; ++i) {
+    if (!outs[i]) continue;
+    bool twice = outs[i] == x || outs[i] == random;
+    for (int j = 0; j < i; ++j) twice = twice || outs[i] == outs[j];
+    if (twice)
+      return fail(MOE_ERR_INVALID_ARG, "codes and scales need buffers of their own");
+  }
+  if ((s = check_device(nullptr)) != MOE_OK) return s;
+  const hipError_t e = launch_quantize_mxfp4(
+      x, dtype, rows, cols, ldx, static_cast<const uint8_t*>(random), static_cast<uint8_t*>(q), ldq,
+      static_cast<uint8_t*>(scale), lds, static_cast<uint8_t*>(qt), ldqt,
+      static_cast<uint8_t*>(scale_t), ldst, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_quantize_mxfp4 launch");
+}
+
+moe_status moe_dequantize_mxfp4(int64_t rows, int64_t cols, const void* q, int64_t ldq,
+                                const void* scale, int64_t lds, void* out, int64_t ldo,
+                                int32_t dtype, void* stream) {
+  if (dtype != MOE_BF16 && dtype != MOE_F32)
+    return fail(MOE_ERR_INVALID_ARG, "dtype=%d must be MOE_BF16 or MOE_F32", dtype);
+  constexpr int64_t kMost = (int64_t)1 << 40;
+  if (rows < 1 || cols < 1 || rows > kMost || cols > kMost ||
+      rows * (double)cols >= 1.15e18)
+    return fail(MOE_ERR_INVALID_ARG, "rows and cols must be in [1, 2^40], rows*cols < 2^60");
+  if (!q) return fail(MOE_ERR_INVALID_ARG, "q is NULL");
+  moe_status s = check_mx("q", q, ldq, scale, lds, cols);
+  if (s != MOE_OK) return s;
+  if (ldo < cols) return fail(MOE_ERR_INVALID_ARG, "ldo=%lld < cols", (long long)ldo);
+  if (!out || (reinterpret_cast<uintptr_t>(out) & (dtype == MOE_F32 ? 3 : 1)))
+    return fail(MOE_ERR_INVALID_ARG, "out is NULL or not aligned to its element");
+  if (out == q || out == scale)
+    return fail(MOE_ERR_INVALID_ARG, "out needs a buffer of its own");
+  if ((s = check_device(nullptr)) != MOE_OK) return s;
+  const hipError_t e = launch_dequantize_mxfp4(
+      rows, cols, static_cast<const uint8_t*>(q), ldq, static_cast<const uint8_t*>(scale), lds, out,
+      ldo, dtype, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_dequantize_mxfp4 launch");
+}
+
+size_t moe_gemm_mxfp4_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (check_gemm_fp8(M, N, K) != MOE_OK) return 0;
+  return gemm_mxfp4_ws_bytes(M, N, K);
+}
+
+moe_status moe_gemm_mxfp4(int64_t M, int64_t N, int64_t K, const void* a, int64_t lda,
+                          const void* a_scale, int64_t ldsa, const void* b, int64_t ldb,
+                          const void* b_scale, int64_t ldsb, void* c, int64_t ldc, int32_t c_dtype,
+                          int32_t accumulate, void* ws, size_t ws_bytes, void* stream) {
+  moe_status s = check_gemm_fp8(M, N, K);  // the same limits
+  if (s != MOE_OK) return s;
+  REQUIRE_PTR(a);
+  REQUIRE_PTR(b);
+  REQUIRE_PTR(c);
+  if ((s = check_mx("a", a, lda, a_scale, ldsa, K)) != MOE_OK) return s;
+  if ((s = check_mx("b", b, ldb, b_scale, ldsb, K)) != MOE_OK) return s;
+  constexpr int64_t kMostLd = (int64_t)1 << 22;
+  if (lda > kMostLd || ldb > kMostLd || ldsa > kMostLd || ldsb > kMostLd)
+    return fail(MOE_ERR_INVALID_ARG, "row strides must be at most 2^22 bytes");
+  if (ldc < N) return fail(MOE_ERR_INVALID_ARG, "ldc=%lld < N", (long long)ldc);
+  if (c_dtype != MOE_BF16 && c_dtype != MOE_F32)
+    return fail(MOE_ERR_INVALID_ARG, "c_dtype=%d must be MOE_BF16 or MOE_F32", c_dtype);
+  if (accumulate != 0 && (accumulate != 1 || c_dtype != MOE_F32))
+    return fail(MOE_ERR_INVALID_ARG, "accumulate must be 0, or 1 with c_dtype MOE_F32");
+  if (c == a || c == b || c == a_scale || c == b_scale)
+    return fail(MOE_ERR_INVALID_ARG, "c cannot be written over an operand");
+  if ((s = check_ws("moe_gemm_mxfp4", ws, ws_bytes, gemm_mxfp4_ws_bytes(M, N, K))) != MOE_OK)
+    return s;
+  if ((s = check_device(nullptr)) != MOE_OK) return s;
+  const hipError_t e = launch_gemm_mxfp4(
+      M, N, K, static_cast<const uint8_t*>(a), lda, static_cast<const uint8_t*>(a_scale), ldsa,
+      static_cast<const uint8_t*>(b), ldb, static_cast<const uint8_t*>(b_scale), ldsb, c, ldc,
+      c_dtype == MOE_F32, accumulate, ws, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_gemm_mxfp4 launch");
+}
+
+size_t moe_mxfp4_packed_bytes(int64_t batch, int64_t rows, int64_t cols) {
+  if (batch < 1 || batch > 65536 || rows < 64 || rows % 64 || rows > 65536 || cols < 128 ||
+      cols % 128 || cols > 65536) {
+    fail(MOE_ERR_INVALID_ARG,
+         "batch must be in [1, 65536], rows a multiple of 64 and cols of 128, at most 65536");
+    return 0;
+  }
+  return (size_t)batch * rows * cols / 32 * 17;
+}
+
+moe_status moe_pack_expert_weights_mxfp4(const moe_problem* p, const void* w13,
+                                         const void* w13_scale, const void* w2,
+                                         const void* w2_scale, void* w13_packed, void* w2_packed,
+                                         void* stream) {
+  Dims d;
+  moe_status s = validate(p, &d);
+  if (s != MOE_OK) return s;
+  if ((s = require_mxfp4(d, "moe_pack_expert_weights_mxfp4")) != MOE_OK) return s;
+  if (!w13_packed && !w2_packed)
+    return fail(MOE_ERR_INVALID_ARG, "w13_packed and w2_packed are both NULL");
+  const void* in[4] = {w13, w13_scale, w2, w2_scale};
+  const char* name[4] = {"w13", "w13_scale", "w2", "w2_scale"};
+  for (int i = 0; i < 4; ++i) {
+    if (!(i < 2 ? w13_packed : w2_packed)) continue;
+    if (!in[i]) return fail(MOE_ERR_INVALID_ARG, "%s is NULL", name[i]);
+    if (!aligned16(in[i])) return fail(MOE_ERR_INVALID_ARG, "%s is not 16-byte aligned", name[i]);
+    if (in[i] == w13_packed || in[i] == w2_packed)
+      return fail(MOE_ERR_INVALID_ARG, "packed weights need buffers of their own");
+  }
+  if (!aligned16(w13_packed) || !aligned16(w2_packed))
+    return fail(MOE_ERR_INVALID_ARG, "w13_packed or w2_packed is not 16-byte aligned");
+  if (w13_packed == w2_packed)
+    return fail(MOE_ERR_INVALID_ARG, "packed weights need buffers of their own");
+  if ((s = check_device(nullptr)) != MOE_OK) return s;
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  hipError_t e = hipSuccess;
+  if (w13_packed)
+    e = launch_pack_mxfp4(static_cast<const uint8_t*>(w13), static_cast<const uint8_t*>(w13_scale),
+                          static_cast<uint8_t*>(w13_packed), d.E + d.S, 2 * d.I, d.H, true, st);
+  if (e == hipSuccess && w2_packed)
+    e = launch_pack_mxfp4(static_cast<const uint8_t*>(w2), static_cast<const uint8_t*>(w2_scale),
+                          static_cast<uint8_t*>(w2_packed), d.E + d.S, d.H, d.I, false, st);
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_pack_expert_weights_mxfp4 launch");
+}
+
+moe_status moe_expert_ffn_up_mxfp4(const moe_problem* p, const void* x_q, const void* x_scale,
+                                   int64_t ldxs, const int32_t* sorted_token,
+                                   const int32_t* offsets, const void* w13_packed, void* h_q,
+                                   void* h_scale, int64_t ldhs, void* stream) {
+  Dims d;
+  moe_status s = validate(p, &d);
+  if (s != MOE_OK) return s;
+  if ((s = require_mxfp4(d, "moe_expert_ffn_up_mxfp4")) != MOE_OK) return s;
+  REQUIRE_PTR(x_q);
+  REQUIRE_PTR(w13_packed);
+  REQUIRE_PTR(h_q);
+  if ((s = check_mx("x_q", x_q, d.H / 2, x_scale, ldxs, d.H)) != MOE_OK) return s;
+  if ((s = check_mx("h_q", h_q, d.I / 2, h_scale, ldhs, d.I)) != MOE_OK) return s;
+  if (!sorted_token || !offsets)
+    return fail(MOE_ERR_INVALID_ARG, "sorted_token and offsets are required");
+  if (d.T * (d.H / 2) >= ((int64_t)1 << 31) - 16 || d.T * ldxs >= ((int64_t)1 << 31) - 16 ||
+      ldhs > ((int64_t)1 << 22))
+    return fail(MOE_ERR_INVALID_ARG,
+                "T*H/2 and T*ldxs must be < 2^31 - 16 (32-bit row offsets), ldhs at most 2^22");
+  if (h_q == x_q || h_q == h_scale || h_scale == x_scale || h_q == x_scale || h_scale == x_q)
+    return fail(MOE_ERR_INVALID_ARG, "h_q and h_scale need buffers of their own");
+  if ((s = check_device(nullptr)) != MOE_OK) return s;
+  const hipError_t e = launch_ffn_up_mxfp4(
+      d, static_cast<const uint8_t*>(x_q), static_cast<const uint8_t*>(x_scale), ldxs, sorted_token,
+      offsets, static_cast<const uint8_t*>(w13_packed), static_cast<uint8_t*>(h_q),
+      static_cast<uint8_t*>(h_scale), ldhs, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_expert_ffn_up_mxfp4 launch");
+}
+
+moe_status moe_expert_ffn_down_mxfp4(const moe_problem* p, const void* h_q, const void* h_scale,
+                                     int64_t ldhs, const int32_t* offsets, const void* w2_packed,
+                                     void* y_sorted, void* stream) {
+  Dims d;
+  moe_status s = validate(p, &d);
+  if (s != MOE_OK) return s;
+  if ((s = require_mxfp4(d, "moe_expert_ffn_down_mxfp4")) != MOE_OK) return s;
+  REQUIRE_PTR(h_q);
+  REQUIRE_PTR(w2_packed);
+  REQUIRE_PTR(y_sorted);
+  if ((s = check_mx("h_q", h_q, d.I / 2, h_scale, ldhs, d.I)) != MOE_OK) return s;
+  if (!offsets) return fail(MOE_ERR_INVALID_ARG, "offsets is NULL");
+  if (ldhs > ((int64_t)1 << 22)) return fail(MOE_ERR_INVALID_ARG, "ldhs must be at most 2^22");
+  if (y_sorted == h_q || y_sorted == h_scale)
+    return fail(MOE_ERR_INVALID_ARG, "y_sorted needs a buffer of its own");
+  if ((s = check_device(nullptr)) != MOE_OK) return s;
+  const hipError_t e = launch_ffn_down_mxfp4(
+      d, static_cast<const uint8_t*>(h_q), static_cast<const uint8_t*>(h_scale), ldhs, offsets,
+      static_cast<const uint8_t*>(w2_packed), y_sorted, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_expert_ffn_down_mxfp4 launch");
+}
+
+// ---- a share of the experts ----
+static moe_status check_pairs(int64_t T, int32_t K) {
+  if (K < 1 || K > 16) return fail(MOE_ERR_INVALID_ARG, "K=%d must be in [1,16]", K);
+  if (T < 0 || T > ((int64_t)1 << 31) / K - 1024)
+    return fail(MOE_ERR_INVALID_ARG, "T=%lld must be >= 0 with T*K < 2^31 - 1024*K", (long long)T);
+  return MOE_OK;
+}
+
+size_t moe_sort_by_expert_workspace_bytes(int64_t T, int32_t K, int32_t count) {
+  if (check_pairs(T, K) != MOE_OK) return 0;
+  if (count < 1 || count > 512) {
+    fail(MOE_ERR_INVALID_ARG, "count=%d must be in [1,512]", count);
+    return 0;
+  }
+  return sort_ws_bytes(T * K, count) + 16;
+}
+
+moe_status moe_sort_by_expert(int64_t T, int32_t K, const int32_t* topk_idx, int32_t first,
+                              int32_t count, int32_t* offsets, int32_t* sorted_token,
+                              int32_t* pair_row, void* ws, size_t ws_bytes, void* stream) {
+  const size_t need = moe_sort_by_expert_workspace_bytes(T, K, count);
+  if (!need) return MOE_ERR_INVALID_ARG;
+  if (first < 0) return fail(MOE_ERR_INVALID_ARG, "first=%d must be >= 0", first);
+  if (!offsets) return fail(MOE_ERR_INVALID_ARG, "offsets is NULL");
+  if (T && (!topk_idx || !sorted_token || !pair_row))
+    return fail(MOE_ERR_INVALID_ARG, "topk_idx, sorted_token and pair_row are required");
+  if (T && (topk_idx == pair_row || topk_idx == sorted_token || sorted_token == pair_row))
+    return fail(MOE_ERR_INVALID_ARG, "topk_idx, sorted_token and pair_row need buffers of their own");
+  moe_status s = check_ws("moe_sort_by_expert", ws, ws_bytes, need);
+  if (s != MOE_OK) return s;
+  if ((s = check_device(nullptr)) != MOE_OK) return s;
+  const hipError_t e = launch_sort_by_expert(T * K, K, topk_idx, first, count, offsets,
+                                             sorted_token, pair_row, ws,
+                                             static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_sort_by_expert launch");
+}
+
+// a matrix of `dtype` rows; `there` false: not used
+static moe_status check_rows(const char* name, bool there, const void* x, int64_t ld, int64_t H,
+                             int32_t dtype) {
+  if (!there) return MOE_OK;
+  if (!x) return fail(MOE_ERR_INVALID_ARG, "%s is NULL", name);
+  if (reinterpret_cast<uintptr_t>(x) & (dtype == MOE_F32 ? 3 : 1))
+    return fail(MOE_ERR_INVALID_ARG, "%s is not aligned to its element", name);
+  if (ld < H || ld > ((int64_t)1 << 31))
+    return fail(MOE_ERR_INVALID_ARG, "the row stride of %s must be at least H and at most 2^31",
+                name);
+  return MOE_OK;
+}
+
+static moe_status check_move(int32_t dtype, int64_t T, int32_t K, int64_t H, const void* row) {
+  if (dtype != MOE_BF16 && dtype != MOE_F32)
+    return fail(MOE_ERR_INVALID_ARG, "dtype=%d must be MOE_BF16 or MOE_F32", dtype);
+  moe_status s = check_pairs(T, K);
+  if (s != MOE_OK) return s;
+  if (H < 1 || H > ((int64_t)1 << 20))
+    return fail(MOE_ERR_INVALID_ARG, "H=%lld must be in [1, 2^20]", (long long)H);
+  if (T && !row) return fail(MOE_ERR_INVALID_ARG, "pair_row is NULL");
+  return MOE_OK;
+}
+
+moe_status moe_dispatch(int32_t dtype, int64_t T, int32_t K, int64_t H, const void* x, int64_t ldx,
+                        const int32_t* pair_row, const float* weights, void* x_sorted, int64_t ldxs,
+                        void* stream) {
+  moe_status s = check_move(dtype, T, K, H, pair_row);
+  if (s != MOE_OK) return s;
+  if ((s = check_rows("x", T > 0, x, ldx, H, dtype)) != MOE_OK) return s;
+  if ((s = check_rows("x_sorted", T > 0, x_sorted, ldxs, H, dtype)) != MOE_OK) return s;
+  if (T && x == x_sorted)
+    return fail(MOE_ERR_INVALID_ARG, "x_sorted needs a buffer of its own");
+  if ((s = check_device(nullptr)) != MOE_OK || T == 0) return s;
+  const hipError_t e = launch_spread(dtype, T, K, H, x, ldx, pair_row, weights, nullptr, 0,
+                                     x_sorted, ldxs, nullptr, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_dispatch launch");
+}
+
+moe_status moe_dispatch_backward(int32_t dtype, int64_t T, int32_t K, int64_t H,
+                                 const void* dx_sorted, int64_t lddxs, const int32_t* pair_row,
+                                 const float* weights, const void* x, int64_t ldx, void* dx,
+                                 int64_t lddx, float* dweights, void* stream) {
+  moe_status s = check_move(dtype, T, K, H, pair_row);
+  if (s != MOE_OK) return s;
+  if (dweights && !weights)
+    return fail(MOE_ERR_INVALID_ARG, "dweights without weights");
+  if ((s = check_rows("dx_sorted", T > 0, dx_sorted, lddxs, H, dtype)) != MOE_OK) return s;
+  if ((s = check_rows("x", T > 0 && dweights, x, ldx, H, dtype)) != MOE_OK) return s;
+  if ((s = check_rows("dx", T > 0, dx, lddx, H, dtype)) != MOE_OK) return s;
+  if (T && (dx == dx_sorted || (dweights && dx == x)))
+    return fail(MOE_ERR_INVALID_ARG, "dx needs a buffer of its own");
+  if ((s = check_device(nullptr)) != MOE_OK || T == 0) return s;
+  const hipError_t e =
+      launch_gather(dtype, T, K, H, dx_sorted, lddxs, pair_row, weights, dweights ? x : nullptr,
+                    dweights ? ldx : 0, dx, lddx, dweights, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_dispatch_backward launch");
+}
+
+moe_status moe_collect(int32_t dtype, int64_t T, int32_t K, int64_t H, const void* y_sorted,
+                       int64_t ldys, const int32_t* pair_row, const float* weights, void* y,
+                       int64_t ldy, void* stream) {
+  moe_status s = check_move(dtype, T, K, H, pair_row);
+  if (s != MOE_OK) return s;
+  if ((s = check_rows("y_sorted", T > 0, y_sorted, ldys, H, dtype)) != MOE_OK) return s;
+  if ((s = check_rows("y", T > 0, y, ldy, H, dtype)) != MOE_OK) return s;
+  if (T && y == y_sorted) return fail(MOE_ERR_INVALID_ARG, "y needs a buffer of its own");
+  if ((s = check_device(nullptr)) != MOE_OK || T == 0) return s;
+  const hipError_t e = launch_gather(dtype, T, K, H, y_sorted, ldys, pair_row, weights, nullptr, 0,
+                                     y, ldy, nullptr, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_collect launch");
+}
+
+moe_status moe_collect_backward(int32_t dtype, int64_t T, int32_t K, int64_t H, const void* dy,
+                                int64_t lddy, const int32_t* pair_row, const float* weights,
+                                const void* y_sorted, int64_t ldys, void* dy_sorted, int64_t lddys,
+                                float* dweights, void* stream) {
+  moe_status s = check_move(dtype, T, K, H, pair_row);
+  if (s != MOE_OK) return s;
+  if (dweights && !weights)
+    return fail(MOE_ERR_INVALID_ARG, "dweights without weights");
+  if ((s = check_rows("dy", T > 0, dy, lddy, H, dtype)) != MOE_OK) return s;
+  if ((s = check_rows("y_sorted", T > 0 && dweights, y_sorted, ldys, H, dtype)) != MOE_OK)
+    return s;
+  if ((s = check_rows("dy_sorted", T > 0, dy_sorted, lddys, H, dtype)) != MOE_OK) return s;
+  if (T && (dy_sorted == dy || (dweights && dy_sorted == y_sorted)))
+    return fail(MOE_ERR_INVALID_ARG, "dy_sorted needs a buffer of its own");
+  if ((s = check_device(nullptr)) != MOE_OK || T == 0) return s;
+  const hipError_t e = launch_spread(dtype, T, K, H, dy, lddy, pair_row, weights,
+                                     dweights ? y_sorted : nullptr, dweights ? ldys : 0, dy_sorted,
+                                     lddys, dweights, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_collect_backward launch");
 }
 
 }  // extern "C"

@@ -1,0 +1,506 @@
+// MXFP4 matrix product of any size: C[m,n] = sum_k A[m,k] B[n,k] over E2M1 codes with one E8M0
+// scale per (row, 32 of k) on either side.  The matrix instructions take codes and scales as they
+// are and add in fp32 (products of two codes are multiples of 1/4 up to 36, so the sum of a block's
+// is exact; what is rounded is the sum over blocks).
+//
+// k_mx_gemm: BM x BN outputs a workgroup of WM x WN waves, 256 of k a step.  Codes go from memory
+// straight to a ring of LDS stages (buffer loads with the LDS destination bit; rows of 128 bytes,
+// 16-byte chunks xor-swizzled by the row), rows past M or N arrive as zeros by the descriptor's
+// range check, chunks past K by an offset outside it.  Scales come 16 bytes of a row at a time,
+// two steps' worth, into a ring of their own.  Within a step's 256 of k, part s (of 128) and
+// instruction u of it take the blocks 4 s + 2 h + u in lane half h, the same on both sides, so
+// that a lane's two scales of a part are adjacent bytes.  B is the instruction's first operand: a
+// lane's results lie in one row of C.  Split over k (few tiles): fp32 partial sums to the
+// workspace, k_mx_join adds them in order.
+// k_mx_gemm_rows: few rows of A; see there.
+#include <algorithm>
+#include <type_traits>
+
+#include "mxfp4.h"
+
+namespace moe {
+namespace {
+
+constexpr int kStep = 256;        // of k
+constexpr int kRow = kStep / 2;   // bytes of a row in a stage
+constexpr uint32_t kOut = 0x7ffffff0u;  // an offset past every descriptor's range
+
+__device__ __forceinline__ int at128(int r, int c) { return r * kRow + ((c ^ (r >> 1)) & 7) * 16; }
+__device__ __forceinline__ u32x4 lds16(uint32_t addr) {
+  return *reinterpret_cast<const __attribute__((address_space(3))) u32x4*>((uintptr_t)addr);
+}
+__device__ __forceinline__ uint32_t lds2(uint32_t addr) {
+  return *reinterpret_cast<const __attribute__((address_space(3))) uint16_t*>((uintptr_t)addr);
+}
+
+struct GemmArgs {
+  const uint8_t *a, *b, *sa, *sb;
+  void* c;  // C, or the partial sums [splits, M, ldc] fp32
+  int64_t lda, ldb, ldsa, ldsb, ldc, M, N, K;
+  int mt, nt;         // tiles along M and N
+  int splits, steps;  // k is cut into `splits` parts of `steps` steps
+  int c_f32, accumulate;
+};
+
+// 16 bytes of a row of C from v (8 bf16 or 4 fp32 values), n of its columns valid
+__device__ __forceinline__ void store16(char* p, uint4 v, int n, bool f32, bool vec,
+                                        bool accumulate) {
+  if (f32) {
+    float* q = reinterpret_cast<float*>(p);
+    const float w[4] = {__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
+                        __uint_as_float(v.w)};
+    if (vec && n >= 4) {
+      float4 o = make_float4(w[0], w[1], w[2], w[3]);
+      if (accumulate) {
+        const float4 c = *reinterpret_cast<const float4*>(q);
+        o = make_float4(c.x + o.x, c.y + o.y, c.z + o.z, c.w + o.w);
+      }
+      *reinterpret_cast<float4*>(q) = o;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < n) q[i] = accumulate ? q[i] + w[i] : w[i];
+    }
+  } else if (vec && n >= 8) {
+    *reinterpret_cast<uint4*>(p) = v;
+  } else {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint16_t* q = reinterpret_cast<uint16_t*>(p);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) q[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+  }
+}
+
+template <int BM, int BN, int WM, int WN, int NST>
+__global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_gemm(GemmArgs g) {
+  constexpr int W = WM * WN, SM = BM / WM / 32, SN = BN / WN / 32;
+  constexpr int kStage = (BM + BN) * kRow, kScBuf = (BM + BN) * 16;
+  constexpr int NA = BM / 8 / W, NB = BN / 8 / W;  // code loads of a wave and step
+  constexpr int kG = (BM + BN) / 64, NS = (kG + W - 1) / W;  // scale loads: 64 rows each
+  constexpr int kPer = NA + NB + NS;
+  static_assert(BM % (8 * W) == 0 && BN % (8 * W) == 0 && BM % 64 == 0 && BN % 64 == 0,
+                "whole load instructions");
+  static_assert(W * 32 * (BN / WN) * 4 <= NST * kStage, "output staging fits the ring");
+  __shared__ __attribute__((aligned(1024))) char smem[NST * kStage];
+  // the scales of two steps, 16 bytes a row, twice; and what a step that brings none fills
+  __shared__ __attribute__((aligned(16))) char s_sc[2 * kScBuf + 1024];
+  // tiles in bands of 8 row tiles, column-major inside a band, one contiguous range per XCD
+  const int total = g.mt * g.nt * g.splits;
+  const int per = (total + kXcds - 1) / kXcds;
+  const int work = (blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
+  if (blockIdx.x / kXcds >= per || work >= total) return;
+  const int part = work / (g.mt * g.nt), tile = work % (g.mt * g.nt);
+  constexpr int kBand = 8;
+  const int band = tile / (kBand * g.nt), within = tile % (kBand * g.nt);
+  const int rb = min(kBand, g.mt - band * kBand);
+  const int64_t m0 = (int64_t)(band * kBand + within % rb) * BM, n0 = (int64_t)(within / rb) * BN;
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wv / WN, wn = wv % WN, fr = lane & 31, h = lane >> 5;
+  const int nb = (int)((g.K + kMxBlock - 1) / kMxBlock);  // blocks of k
+  const int nk = (nb + 7) / 8;
+  const int k0 = part * g.steps, k1 = min(k0 + g.steps, nk);
+  const int m_rows = (int)min((int64_t)BM, g.M - m0), n_rows = (int)min((int64_t)BN, g.N - n0);
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(smem));
+  const uint32_t lds_sc = __builtin_amdgcn_readfirstlane(lds_offset(s_sc));
+  // a tile's last row of codes ends with its blocks: there may be no memory behind it
+  const i32x4 ar = buffer_rsrc(g.a + m0 * g.lda, (uint32_t)((m_rows - 1) * g.lda + 16 * nb));
+  const i32x4 br = buffer_rsrc(g.b + n0 * g.ldb, (uint32_t)((n_rows - 1) * g.ldb + 16 * nb));
+  const i32x4 sar = buffer_rsrc(g.sa + m0 * g.ldsa, (uint32_t)(m_rows * g.ldsa));
+  const i32x4 sbr = buffer_rsrc(g.sb + n0 * g.ldsb, (uint32_t)(n_rows * g.ldsb));
+  // instruction i of wave wv fills rows 8 (i W + wv) .. +7 of the stage (A's, then B's)
+  const int lrow = 8 * wv + (lane >> 3);
+  const int lchunk = (lane & 7) ^ ((4 * (wv & 1) + (lane >> 4)) & 7);
+  uint32_t ao[NA], bo[NB];
+#pragma unroll
+  for (int i = 0; i < NA; ++i) ao[i] = (uint32_t)((8 * W * i + lrow) * g.lda) + 16 * lchunk;
+#pragma unroll
+  for (int i = 0; i < NB; ++i) bo[i] = (uint32_t)((8 * W * i + lrow) * g.ldb) + 16 * lchunk;
+  // load instruction i (of kPer) of a wave for step kt's stage; past the last step it fetches
+  // what nothing reads
+  auto load = [&](int kt, int st, int i) {
+    const uint32_t dst = lds0 + st * kStage + 8 * wv * kRow, ko = (uint32_t)kt * kRow;
+    const bool in = 8 * kt + lchunk < nb;
+    if (i < NA) {
+      load16_to_lds(ar, dst + i * 8 * W * kRow, in ? ao[i] + ko : kOut);
+    } else if (i < NA + NB) {
+      load16_to_lds(br, dst + (BM + (i - NA) * 8 * W) * kRow,
+                    in ? bo[i < NA + NB ? i - NA : 0] + ko : kOut);
+    } else {  // the scales of steps kt and kt + 1: rows 64 q .. +63 of A, then of B
+      const int q = (i - NA - NB) * W + wv;
+      const bool now = q < kG && ((kt & 1) == 0 || kt == k0);
+      const bool of_a = q < BM / 64;
+      const int row = 64 * (of_a ? q : q - BM / 64) + lane;
+      load16_to_lds(of_a ? sar : sbr,
+                    lds_sc + (now ? ((kt >> 1) & 1) * kScBuf + 1024 * q : 2 * kScBuf),
+                    now ? (uint32_t)(row * (of_a ? g.ldsa : g.ldsb)) + 16 * (uint32_t)(kt >> 1)
+                        : kOut);
+    }
+  };
+  auto stage = [&](int kt, int st) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) load(kt, st, i);
+  };
+
+  f32x16 acc[SM][SN];
+#pragma unroll
+  for (int m = 0; m < SM; ++m)
+#pragma unroll
+    for (int n = 0; n < SN; ++n)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[m][n][i] = 0.0f;
+
+#pragma unroll
+  for (int j = 0; j < NST - 1; ++j) stage(k0 + j, j);
+  int st = 0;
+  for (int kt = k0; kt < k1; ++kt) {
+    wait_vm<(NST - 2) * kPer>();
+    __syncthreads();
+    const int kt_ld = kt + NST - 1, st_ld = st == 0 ? NST - 1 : st - 1;
+    if (kt == nk - 1 && (g.K & (kStep - 1))) {
+      // the last step's blocks past K: their codes are zeros, their scales become 2^-127, not what
+      // the pad holds, which may be the NaN; and the last block's codes past K are cleared in A
+      char* sc = s_sc + ((kt >> 1) & 1) * kScBuf + 8 * (kt & 1);
+      const int left = nb - 8 * kt;  // blocks of this step
+      for (int r = tid; r < BM + BN; r += 64 * W) {
+        for (int b = left; b < 8; ++b) sc[16 * r + b] = 0;
+        const int n = (int)(g.K & (kMxBlock - 1));
+        if (n && r < BM) {
+          uint32_t* p = reinterpret_cast<uint32_t*>(smem + st * kStage + at128(r, left - 1));
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (n < 8 * i + 8) p[i] = n > 8 * i ? p[i] & ((1u << (4 * (n - 8 * i))) - 1u) : 0u;
+        }
+      }
+      __syncthreads();
+    }
+    const uint32_t a_at = lds0 + st * kStage + wm * (BM / WM) * kRow;
+    const uint32_t b_at = lds0 + st * kStage + (BM + wn * (BN / WN)) * kRow;
+    const uint32_t sc_at = lds_sc + ((kt >> 1) & 1) * kScBuf + 8 * (kt & 1) + 16 * fr + 2 * h;
+    u32x4 fa[2][SM], fb[2][SN];
+    uint32_t sa[SM], sb[SN];
+    auto frags = [&](int j, int buf) {  // j = 2 s + u
+      const uint32_t off = (uint32_t)at128(fr, 4 * (j >> 1) + 2 * h + (j & 1));
+#pragma unroll
+      for (int m = 0; m < SM; ++m) fa[buf][m] = lds16(a_at + 32 * m * kRow + off);
+#pragma unroll
+      for (int n = 0; n < SN; ++n) fb[buf][n] = lds16(b_at + 32 * n * kRow + off);
+    };
+    auto scales = [&](int s) {
+#pragma unroll
+      for (int m = 0; m < SM; ++m) sa[m] = lds2(sc_at + 16 * (wm * (BM / WM) + 32 * m) + 4 * s);
+#pragma unroll
+      for (int n = 0; n < SN; ++n)
+        sb[n] = lds2(sc_at + 16 * (BM + wn * (BN / WN) + 32 * n) + 4 * s);
+    };
+    frags(0, 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if ((j & 1) == 0) scales(j >> 1);
+      if (j < 3) frags(j + 1, (j + 1) & 1);
+      // the next stage's loads go out between the products
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (i * 4 / kPer == j) load(kt_ld, st_ld, i);
+#pragma unroll
+      for (int n = 0; n < SN; ++n)
+#pragma unroll
+        for (int m = 0; m < SM; ++m)
+          acc[m][n] = (j & 1) ? mx_mfma32<1, 1>(fb[j & 1][n], fa[j & 1][m], acc[m][n], sb[n], sa[m])
+                              : mx_mfma32<0, 0>(fb[j & 1][n], fa[j & 1][m], acc[m][n], sb[n], sa[m]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (++st == NST) st = 0;
+  }
+  wait_vm<0>();
+  __syncthreads();  // every wave is done with the ring, which now stages the output
+
+  // a wave's 32 x (BN/WN) outputs of sub-tile row m in LDS (16-byte chunks swizzled by the row),
+  // stored back 16 bytes a lane along the rows
+  auto store = [&](auto is_f32) {
+    constexpr bool f32 = decltype(is_f32)::value;
+    constexpr int es = f32 ? 4 : 2, kCols = BN / WN, row_bytes = kCols * es;
+    constexpr int chunks = row_bytes / 16, mask = (chunks < 16 ? chunks : 16) - 1;
+    char* stg = smem + wv * 32 * kCols * 4;
+    char* out = static_cast<char*>(g.c) + (g.splits > 1 ? (int64_t)part * g.M * g.ldc * 4 : 0);
+    const bool vec = g.ldc * es % 16 == 0;
+    const bool add = g.accumulate && g.splits == 1;
+#pragma unroll
+    for (int m = 0; m < SM; ++m) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+      for (int n = 0; n < SN; ++n)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const auto& a = acc[m][n];
+          const int col = 32 * n + 8 * q + 4 * h;  // 4 adjacent columns
+          char* p = stg + fr * row_bytes + (((col * es / 16) ^ (fr & mask)) << 4);
+          if (f32)
+            *reinterpret_cast<float4*>(p) =
+                make_float4(a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]);
+          else
+            *reinterpret_cast<uint2*>(p + (col & 4) * 2) =
+                pack4_bf16(a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]);
+        }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      const int64_t row0 = m0 + wm * (BM / WM) + 32 * m;
+#pragma unroll
+      for (int e0 = 0; e0 < 32 * chunks; e0 += 64) {
+        const int r = (e0 + lane) / chunks, ch = (e0 + lane) % chunks;
+        const int64_t n = n0 + wn * kCols + ch * (16 / es);
+        const uint4 v =
+            *reinterpret_cast<const uint4*>(stg + r * row_bytes + ((ch ^ (r & mask)) << 4));
+        if (row0 + r < g.M && n < g.N)
+          store16(out + ((row0 + r) * g.ldc + n) * es, v, (int)min((int64_t)8, g.N - n), f32, vec,
+                  add);
+      }
+    }
+  };
+  if (g.c_f32 || g.splits > 1) store(std::true_type());
+  else store(std::false_type());
+}
+
+// Few rows: a workgroup takes 16 columns and every row of A, its 8 waves every 8th step of k each,
+// with the codes of kU steps on their way from memory straight into registers, and they add their
+// sums in LDS, in order.  B is read once in all, A once a workgroup (from the L2).  The 16 x 16 x
+// 128 instruction: B the first operand, lane l holds block l / 16 of its row, l % 16, and the
+// result's rows 4 (l / 16) .. +3 of B for row l % 16 of A.
+struct Half {  // a row's 128 of k: the lane's block and its scale
+  u32x4 q;
+  uint32_t s;
+};
+__device__ __forceinline__ f32x4 mul16(const Half& b, const Half& a, const f32x4& c) {
+  const i32x8 x = {(int)b.q[0], (int)b.q[1], (int)b.q[2], (int)b.q[3], 0, 0, 0, 0};
+  const i32x8 y = {(int)a.q[0], (int)a.q[1], (int)a.q[2], (int)a.q[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, 0, (int)b.s, 0, (int)a.s);
+}
+
+template <int MG, int kU>
+__global__ __launch_bounds__(512) void k_mx_gemm_rows(GemmArgs g) {
+  constexpr int kW = 8, kM = 16 * MG;
+  __shared__ float s_sum[kW][kM][17];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, q = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int nb = (int)((g.K + kMxBlock - 1) / kMxBlock), nk = (nb + 7) / 8;
+  const int whole = (int)(g.K / kStep);
+  // rows past M or N repeat the last one (their results are not stored)
+  const uint8_t *ap[MG], *sap[MG];
+#pragma unroll
+  for (int m = 0; m < MG; ++m) {
+    const int64_t row = min((int64_t)16 * m + r, g.M - 1);
+    ap[m] = g.a + row * g.lda + 16 * q;
+    sap[m] = g.sa + row * g.ldsa;
+  }
+  const int64_t brow = min(n0 + r, g.N - 1);
+  const uint8_t *bp = g.b + brow * g.ldb + 16 * q, *sbp = g.sb + brow * g.ldsb;
+  struct Step {
+    Half a[MG][2], b[2];
+  };
+  auto scale = [&](const uint8_t* p, int st, Half (&v)[2]) {
+    const uint2 s = *reinterpret_cast<const uint2*>(p + 8 * st);
+    v[0].s = s.x >> (8 * q);
+    v[1].s = s.y >> (8 * q);
+  };
+  auto load = [&](Step& v, int st) {  // a whole step
+    const int64_t k = (int64_t)st * kRow;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      v.b[h].q = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(bp + k + 64 * h));
+#pragma unroll
+      for (int m = 0; m < MG; ++m)
+        v.a[m][h].q = *reinterpret_cast<const u32x4*>(ap[m] + k + 64 * h);
+    }
+    scale(sbp, st, v.b);
+#pragma unroll
+    for (int m = 0; m < MG; ++m) scale(sap[m], st, v.a[m]);
+  };
+  f32x4 acc[MG];
+#pragma unroll
+  for (int m = 0; m < MG; ++m) acc[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  auto add = [&](const Step& v) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int m = 0; m < MG; ++m) acc[m] = mul16(v.b[h], v.a[m][h], acc[m]);
+  };
+  Step v[kU];
+#pragma unroll
+  for (int u = 0; u < kU; ++u)
+    if (wv + kW * u < whole) load(v[u], wv + kW * u);
+  for (int b = wv; b < whole; b += kW * kU)
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int st = b + kW * u;
+      if (st >= whole) break;
+      add(v[u]);
+      if (st + kW * kU < whole) load(v[u], st + kW * kU);
+    }
+  if (whole < nk && whole % kW == wv) {  // the last, partial step
+    const int64_t k = (int64_t)whole * kRow;
+    const u32x4 zero = {0, 0, 0, 0};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int b = 8 * whole + 4 * h + q;  // this lane's block: zeros past K
+      const bool in = b < nb;
+      const int n = (int)min((int64_t)kMxBlock, g.K - (int64_t)kMxBlock * b);
+      v[0].b[h].q = in ? *reinterpret_cast<const u32x4*>(bp + k + 64 * h) : zero;
+      v[0].b[h].s = in ? sbp[b] : 0;
+#pragma unroll
+      for (int m = 0; m < MG; ++m) {
+        u32x4 w = in ? *reinterpret_cast<const u32x4*>(ap[m] + k + 64 * h) : zero;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // the codes past K: cleared in A
+          if (n < 8 * i + 8) w[i] = n > 8 * i ? w[i] & ((1u << (4 * (n - 8 * i))) - 1u) : 0u;
+        v[0].a[m][h].q = w;
+        v[0].a[m][h].s = in ? sap[m][b] : 0;
+      }
+    }
+    add(v[0]);
+  }
+#pragma unroll
+  for (int m = 0; m < MG; ++m)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s_sum[wv][16 * m + r][4 * q + i] = acc[m][i];
+  __syncthreads();
+  for (int e = tid; e < kM * 16; e += 512) {
+    const int m = e >> 4, n = e & 15;
+    if (m >= g.M || n0 + n >= g.N) continue;
+    float s = s_sum[0][m][n];
+#pragma unroll
+    for (int w = 1; w < kW; ++w) s += s_sum[w][m][n];
+    const int64_t at = m * g.ldc + n0 + n;
+    if (g.c_f32) {
+      float* p = static_cast<float*>(g.c) + at;
+      *p = g.accumulate ? *p + s : s;
+    } else {
+      static_cast<uint16_t*>(g.c)[at] = f32_to_bf16_bits(s);
+    }
+  }
+}
+
+// C = the parts' sum, in order
+__global__ __launch_bounds__(256) void k_mx_join(const float* __restrict__ part, int splits,
+                                                 int64_t M, int64_t N, int64_t ldp,
+                                                 void* __restrict__ c, int64_t ldc, int c_f32,
+                                                 int accumulate) {
+  const int64_t per = ldp / 4, total = M * per, stride = (int64_t)gridDim.x * 256;
+  const bool vec = ldc * (c_f32 ? 4 : 2) % 16 == 0;
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += stride) {
+    const int64_t r = e / per, n = (e - r * per) * 4;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int p = 0; p < splits; ++p) {
+      const float4 v = *reinterpret_cast<const float4*>(part + (p * M + r) * ldp + n);
+      s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+    }
+    const int left = (int)min((int64_t)4, N - n);
+    if (c_f32) {
+      store16(static_cast<char*>(c) + (r * ldc + n) * 4,
+              make_uint4(__float_as_uint(s.x), __float_as_uint(s.y), __float_as_uint(s.z),
+                         __float_as_uint(s.w)),
+              left, true, vec, accumulate);
+    } else {
+      const uint2 w = pack4_bf16(s.x, s.y, s.z, s.w);
+      uint16_t* p = static_cast<uint16_t*>(c) + r * ldc + n;
+      if (vec && left == 4) {
+        *reinterpret_cast<uint2*>(p) = w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i < left) p[i] = (uint16_t)((i < 2 ? w.x : w.y) >> (16 * (i & 1)));
+      }
+    }
+  }
+}
+
+struct Plan {
+  int bm, bn, splits, steps;
+};
+
+int64_t up4(int64_t n) { return (n + 3) / 4 * 4; }
+
+// The form, the tile and the split over k, from the sizes.
+Plan plan(int64_t M, int64_t N, int64_t K) {
+  const int64_t nk = (K + kStep - 1) / kStep;
+  Plan p;
+  p.splits = 1;
+  p.steps = (int)nk;
+  if (M <= 32) {  // k_mx_gemm_rows
+    p.bm = M <= 16 ? 16 : 32;
+    p.bn = 16;
+    return p;
+  }
+  if (M > 128 && N > 128 && ((M + 255) / 256) * ((N + 255) / 256) >= 192) {
+    p.bm = p.bn = 256;
+    return p;
+  }
+  p.bm = 128;
+  double best = 1e30;
+  for (int bn = 64; bn <= 128; bn += 64) {
+    const double step_us = bn == 64 ? 0.55 : 0.69;
+    const int64_t tiles = ((M + 127) / 128) * ((N + bn - 1) / bn);
+    for (int64_t s = 1; s == 1 || (s * tiles <= 256 && s <= nk / 4); ++s) {
+      const int64_t steps = (nk + s - 1) / s, parts = (nk + steps - 1) / steps;
+      double us = (double)((tiles * parts + 255) / 256 * steps) * step_us;
+      if (parts > 1) us += 3.0 + 2e-6 * (double)(parts * M * N);
+      if (us >= best) continue;
+      best = us;
+      p.bn = bn;
+      p.splits = (int)parts;
+      p.steps = (int)steps;
+    }
+  }
+  return p;
+}
+
+template <int BM, int BN, int WM, int WN, int NST>
+void launch_tile(GemmArgs g, hipStream_t st) {
+  g.mt = (int)((g.M + BM - 1) / BM);
+  g.nt = (int)((g.N + BN - 1) / BN);
+  const int per = (g.mt * g.nt * g.splits + kXcds - 1) / kXcds;
+  hipLaunchKernelGGL((k_mx_gemm<BM, BN, WM, WN, NST>), dim3(per * kXcds), dim3(64 * WM * WN), 0, st,
+                     g);
+}
+
+}  // namespace
+
+size_t gemm_mxfp4_ws_bytes(int64_t M, int64_t N, int64_t K) {
+  const int splits = plan(M, N, K).splits;
+  return splits > 1 ? (size_t)splits * (size_t)M * (size_t)up4(N) * 4 : 0;
+}
+
+hipError_t launch_gemm_mxfp4(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda,
+                             const uint8_t* sa, int64_t ldsa, const uint8_t* b, int64_t ldb,
+                             const uint8_t* sb, int64_t ldsb, void* c, int64_t ldc, int c_f32,
+                             int accumulate, void* ws, hipStream_t st) {
+  const Plan p = plan(M, N, K);
+  GemmArgs g{a, b, sa, sb, c, lda, ldb, ldsa, ldsb, ldc, M, N, K, 0, 0, p.splits, p.steps, c_f32,
+             accumulate};
+  if (p.splits > 1) {
+    g.c = ws;
+    g.ldc = up4(N);
+  }
+  if (p.bn == 16) {
+    const dim3 grid((unsigned)((N + 15) / 16));
+    if (p.bm == 16) hipLaunchKernelGGL((k_mx_gemm_rows<1, 4>), grid, dim3(512), 0, st, g);
+    else hipLaunchKernelGGL((k_mx_gemm_rows<2, 4>), grid, dim3(512), 0, st, g);
+  } else if (p.bn == 64) {
+    launch_tile<128, 64, 4, 2, 3>(g, st);
+  } else if (p.bn == 128) {
+    launch_tile<128, 128, 4, 2, 3>(g, st);
+  } else {
+    launch_tile<256, 256, 4, 2, 2>(g, st);
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.splits == 1) return e;
+  const int64_t blocks = (M * (up4(N) / 4) + 255) / 256;
+  hipLaunchKernelGGL(k_mx_join, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0,
+                     st, static_cast<const float*>(ws), p.splits, M, N, up4(N), c, ldc, c_f32,
+                     accumulate);
+  return hipGetLastError();
+}
+
+}  // namespace moe

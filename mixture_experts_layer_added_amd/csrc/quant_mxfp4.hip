@@ -1,0 +1,352 @@
+// MXFP4 quantisation of matrices of any size, along the rows, along the columns (written
+// transposed), or both from one read of the matrix, and the values of quantised matrices again.
+// A code is off by at most half a step: a quarter of the value where that is at least its scale
+// (1/2, 1, 2 are the steps of 0 .. 2, 2 .. 4, 4 .. 6), a quarter of the scale below.
+// Each element is read once and each code written once.
+//   k_mx_rows: 4 lanes take a block of 32 columns, 8 elements a lane.
+//   k_mx_tile: a workgroup takes 128 x 128 elements through LDS; a wave's lane forms two whole
+//     blocks of 32 rows, of two adjacent columns, without its neighbours.
+//   k_mx_values: 8 values a lane.
+#include <algorithm>
+
+#include "mxfp4.h"
+
+namespace moe {
+namespace {
+
+constexpr int kTile = 128;
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// 8 elements from p, zeros from the n-th on
+template <bool kVec>
+__device__ __forceinline__ void read8(const uint16_t* __restrict__ p, int n, float* v) {
+  if (kVec && n >= 8) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? bf16_bits_to_f32(p[i]) : 0.0f;
+  }
+}
+template <bool kVec>
+__device__ __forceinline__ void read8(const float* __restrict__ p, int n, float* v) {
+  if (kVec && n >= 8) {
+    const float4 a = *reinterpret_cast<const float4*>(p);
+    const float4 b = *reinterpret_cast<const float4*>(p + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : 0.0f;
+  }
+}
+// 8 random bytes, the first n of them there
+__device__ __forceinline__ uint2 read8r(const uint8_t* __restrict__ p, int n) {
+  if (n >= 8 && (reinterpret_cast<uintptr_t>(p) & 7) == 0)
+    return *reinterpret_cast<const uint2*>(p);
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) w[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
+  return make_uint2(w[0], w[1]);
+}
+
+__device__ __forceinline__ uint32_t max8(const float* v) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
+  return m;
+}
+
+// 8 codes of one block, whose scale code is sc
+template <bool kRandom>
+__device__ __forceinline__ uint32_t codes8(const float* v, uint32_t sc, uint2 r) {
+  if (sc == 255) return 0;
+  if (!kRandom) return mx_pack8(v, mx_scale(sc));
+  const float inv = mx_scale(254 - sc);
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    w |= mx_code_random(v[i], inv, ((i < 4 ? r.x : r.y) >> (8 * (i & 3))) & 255u) << (4 * i);
+  return w;
+}
+
+template <typename T, bool kVec, bool kRandom>
+__global__ __launch_bounds__(256) void k_mx_rows(const T* __restrict__ x, int64_t rows,
+                                                 int64_t cols, int64_t ldx,
+                                                 const uint8_t* __restrict__ rnd,
+                                                 uint8_t* __restrict__ q, int64_t ldq,
+                                                 uint8_t* __restrict__ scale, int64_t lds,
+                                                 int64_t kb) {
+  const int l = threadIdx.x & 3;
+  const int64_t total = rows * kb, stride = (int64_t)gridDim.x * 64;
+  for (int64_t g = (int64_t)blockIdx.x * 64 + (threadIdx.x >> 2); g < total; g += stride) {
+    const int64_t r = (uint64_t)total >> 32 ? g / kb : (int64_t)((uint32_t)g / (uint32_t)kb);
+    const int64_t b = g - r * kb, c = b * kMxBlock + 8 * l;
+    const int n = (int)max((int64_t)0, min((int64_t)8, cols - c));
+    float v[8];
+    read8<kVec>(x + r * ldx + c, n, v);
+    uint2 rb = make_uint2(0, 0);
+    if (kRandom) rb = read8r(rnd + r * cols + c, n);
+    uint32_t m = max8(v);
+    m = max(m, (uint32_t)__shfl_xor((int)m, 1));
+    m = max(m, (uint32_t)__shfl_xor((int)m, 2));
+    const uint32_t sc = mx_scale_code<kRandom>(m);
+    *reinterpret_cast<uint32_t*>(q + r * ldq + 16 * b + 4 * l) = codes8<kRandom>(v, sc, rb);
+    if (l == 0) scale[r * lds + b] = (uint8_t)sc;
+  }
+}
+
+template <typename T>
+struct Pair;
+template <>
+struct Pair<uint16_t> {
+  typedef uint32_t type;
+  static __device__ __forceinline__ float lo(uint32_t p) { return __uint_as_float(p << 16); }
+  static __device__ __forceinline__ float hi(uint32_t p) { return __uint_as_float(p & 0xFFFF0000u); }
+};
+template <>
+struct Pair<float> {
+  typedef float2 type;
+  static __device__ __forceinline__ float lo(const float2& p) { return p.x; }
+  static __device__ __forceinline__ float hi(const float2& p) { return p.y; }
+};
+__device__ __forceinline__ void keep8(uint16_t* p, const float* v) {  // exact: v came as bf16
+  uint4 o;
+  uint32_t* w = reinterpret_cast<uint32_t*>(&o);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = __float_as_uint(v[2 * i]) >> 16 | (__float_as_uint(v[2 * i + 1]) & 0xFFFF0000u);
+  *reinterpret_cast<uint4*>(p) = o;
+}
+__device__ __forceinline__ void keep8(float* p, const float* v) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+// 128 x 128 elements a workgroup.  Rows: 16 lanes a row, 8 elements a lane, which also go to LDS
+// as they are.  Columns: lane l of wave w takes columns 2 l and 2 l + 1 of rows 32 w .. +31.
+template <typename T, bool kVec, bool kRandom>
+__global__ __launch_bounds__(256) void k_mx_tile(const T* __restrict__ x, int64_t rows,
+                                                 int64_t cols, int64_t ldx,
+                                                 const uint8_t* __restrict__ rnd,
+                                                 uint8_t* __restrict__ q, int64_t ldq,
+                                                 uint8_t* __restrict__ scale, int64_t lds,
+                                                 uint8_t* __restrict__ qt, int64_t ldqt,
+                                                 uint8_t* __restrict__ scale_t, int64_t ldst,
+                                                 int64_t nb) {
+  typedef Pair<T> P;
+  __shared__ __attribute__((aligned(16))) T tile[kTile * kTile];
+  __shared__ __attribute__((aligned(16))) uint8_t s_r[kRandom ? kTile * kTile : 16];
+  const int tid = threadIdx.x, l = tid & 15;
+  const int64_t rb = blockIdx.x / nb, cb = blockIdx.x - rb * nb;
+  const int64_t r0 = rb * kTile, c0 = cb * kTile;
+  const int n = (int)max((int64_t)0, min((int64_t)8, cols - c0 - 8 * l));
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float v[4][8];
+    uint2 rr[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t r = r0 + 64 * h + 16 * i + (tid >> 4);
+      const int nr = r < rows ? n : 0;
+      read8<kVec>(x + r * ldx + c0 + 8 * l, nr, v[i]);
+      rr[i] = make_uint2(0, 0);
+      if (kRandom) rr[i] = read8r(rnd + r * cols + c0 + 8 * l, nr);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int at = 64 * h + 16 * i + (tid >> 4);
+      const int64_t r = r0 + at;
+      keep8(tile + at * kTile + 8 * l, v[i]);
+      if (kRandom) *reinterpret_cast<uint2*>(s_r + at * kTile + 8 * l) = rr[i];
+      if (!q) continue;
+      uint32_t m = max8(v[i]);
+      m = max(m, (uint32_t)__shfl_xor((int)m, 1));
+      m = max(m, (uint32_t)__shfl_xor((int)m, 2));
+      const int64_t c = c0 + 8 * (l & ~3);  // the block's first column
+      if (r < rows && c < cols) {
+        const uint32_t sc = mx_scale_code<kRandom>(m);
+        *reinterpret_cast<uint32_t*>(q + r * ldq + (c0 + 8 * l) / 2) =
+            codes8<kRandom>(v[i], sc, rr[i]);
+        if ((l & 3) == 0) scale[r * lds + c / kMxBlock] = (uint8_t)sc;
+      }
+    }
+  }
+  __syncthreads();
+  const int lane = tid & 63, wv = tid >> 6;
+  typename P::type v[32];
+  uint32_t m0 = 0, m1 = 0;
+#pragma unroll
+  for (int k = 0; k < 32; ++k) {
+    v[k] = *reinterpret_cast<const typename P::type*>(tile + (32 * wv + k) * kTile + 2 * lane);
+    m0 = max(m0, abs_bits(P::lo(v[k])));
+    m1 = max(m1, abs_bits(P::hi(v[k])));
+  }
+  const uint32_t sc[2] = {mx_scale_code<kRandom>(m0), mx_scale_code<kRandom>(m1)};
+  uint32_t w[2][4];
+  if (kRandom) {
+    const float i0 = mx_scale(254 - min(sc[0], 254u)), i1 = mx_scale(254 - min(sc[1], 254u));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      w[0][j] = w[1][j] = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int k = 8 * j + i;
+        const uint32_t r =
+            *reinterpret_cast<const uint16_t*>(s_r + (32 * wv + k) * kTile + 2 * lane);
+        w[0][j] |= mx_code_random(P::lo(v[k]), i0, r & 255u) << (4 * i);
+        w[1][j] |= mx_code_random(P::hi(v[k]), i1, r >> 8) << (4 * i);
+      }
+    }
+  } else {
+    const float s0 = mx_scale(sc[0]), s1 = mx_scale(sc[1]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float a[8], b[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        a[i] = P::lo(v[8 * j + i]);
+        b[i] = P::hi(v[8 * j + i]);
+      }
+      w[0][j] = mx_pack8(a, s0);
+      w[1][j] = mx_pack8(b, s1);
+    }
+  }
+  __syncthreads();
+  // every wave has its part of the tile in registers: the tile's memory now takes the codes, 64
+  // bytes a column (16-byte chunks swizzled by the column's pair), so that 4 lanes write 64 bytes
+  char* codes = reinterpret_cast<char*>(tile);
+  const int64_t blk = r0 / kMxBlock + wv;  // this wave's block of rows
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int cc = 2 * lane + h;
+    const bool nan = sc[h] == 255;
+    *reinterpret_cast<uint4*>(codes + cc * 64 + ((wv ^ (lane & 3)) << 4)) =
+        make_uint4(nan ? 0 : w[h][0], nan ? 0 : w[h][1], nan ? 0 : w[h][2], nan ? 0 : w[h][3]);
+    if (c0 + cc < cols && blk * kMxBlock < rows) scale_t[(c0 + cc) * ldst + blk] = (uint8_t)sc[h];
+  }
+  __syncthreads();
+  const int ch = tid & 3;
+  if (r0 + kMxBlock * ch >= rows) return;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int cc = 64 * i + (tid >> 2);
+    if (c0 + cc >= cols) continue;
+    *reinterpret_cast<uint4*>(qt + (c0 + cc) * ldqt + r0 / 2 + 16 * ch) =
+        *reinterpret_cast<const uint4*>(codes + cc * 64 + ((ch ^ ((cc >> 1) & 3)) << 4));
+  }
+}
+
+// values of 8 codes: exact in bf16 too (two significant bits, at least 2^-128), NaN for scale 255
+__device__ __forceinline__ void put8(uint16_t* __restrict__ p, const float* v, int n) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = __float_as_uint(v[2 * i]) >> 16 | (__float_as_uint(v[2 * i + 1]) & 0xFFFF0000u);
+  if (n >= 8 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+  }
+}
+__device__ __forceinline__ void put8(float* __restrict__ p, const float* v, int n) {
+  if (n >= 8 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = v[i];
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void k_mx_values(int64_t rows, int64_t cols,
+                                                   const uint8_t* __restrict__ q, int64_t ldq,
+                                                   const uint8_t* __restrict__ scale, int64_t lds,
+                                                   T* __restrict__ out, int64_t ldo) {
+  const int64_t per = (cols + 7) / 8, total = rows * per, stride = (int64_t)gridDim.x * 256;
+  for (int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x; g < total; g += stride) {
+    const int64_t r = (uint64_t)total >> 32 ? g / per : (int64_t)((uint32_t)g / (uint32_t)per);
+    const int64_t c = (g - r * per) * 8;
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(q + r * ldq + c / 2);
+    const uint32_t sc = scale[r * lds + c / kMxBlock];
+    const float s = sc == 255 ? __uint_as_float(0x7fc00000u) : mx_scale(sc);
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      typedef float f32x2 __attribute__((ext_vector_type(2)));
+      const f32x2 p = i == 0   ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0)
+                      : i == 1 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1)
+                      : i == 2 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2)
+                               : __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
+      v[2 * i] = p.x * s;
+      v[2 * i + 1] = p.y * s;
+    }
+    put8(out + r * ldo + c, v, (int)min((int64_t)8, cols - c));
+  }
+}
+
+template <typename T, bool kRandom>
+hipError_t quantize(const T* x, int64_t rows, int64_t cols, int64_t ldx, const uint8_t* rnd,
+                    uint8_t* q, int64_t ldq, uint8_t* scale, int64_t lds, uint8_t* qt,
+                    int64_t ldqt, uint8_t* scale_t, int64_t ldst, hipStream_t st) {
+  // 16-byte loads need every row to start at a multiple of 16 bytes
+  const bool vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && ldx * sizeof(T) % 16 == 0;
+  if (qt) {
+    const int64_t nb = (cols + kTile - 1) / kTile, nr = (rows + kTile - 1) / kTile;
+    auto k = vec ? k_mx_tile<T, true, kRandom> : k_mx_tile<T, false, kRandom>;
+    hipLaunchKernelGGL(k, dim3((unsigned)(nb * nr)), dim3(256), 0, st, x, rows, cols, ldx, rnd, q,
+                       ldq, scale, lds, qt, ldqt, scale_t, ldst, nb);
+  } else {
+    const int64_t kb = (cols + kMxBlock - 1) / kMxBlock;
+    const int64_t blocks = std::min<int64_t>((rows * kb + 63) / 64, 1 << 20);
+    auto k = vec ? k_mx_rows<T, true, kRandom> : k_mx_rows<T, false, kRandom>;
+    hipLaunchKernelGGL(k, dim3((unsigned)blocks), dim3(256), 0, st, x, rows, cols, ldx, rnd, q,
+                       ldq, scale, lds, kb);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_quantize_mxfp4(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ldx,
+                                 const uint8_t* rnd, uint8_t* q, int64_t ldq, uint8_t* scale,
+                                 int64_t lds, uint8_t* qt, int64_t ldqt, uint8_t* scale_t,
+                                 int64_t ldst, hipStream_t st) {
+#define MX_QUANT(T, R)                                                                        \
+  return quantize<T, R>(static_cast<const T*>(x), rows, cols, ldx, rnd, q, ldq, scale, lds, qt, \
+                        ldqt, scale_t, ldst, st)
+  if (dtype == MOE_BF16) {
+    if (rnd) MX_QUANT(uint16_t, true);
+    MX_QUANT(uint16_t, false);
+  }
+  if (rnd) MX_QUANT(float, true);
+  MX_QUANT(float, false);
+#undef MX_QUANT
+}
+
+hipError_t launch_dequantize_mxfp4(int64_t rows, int64_t cols, const uint8_t* q, int64_t ldq,
+                                   const uint8_t* scale, int64_t lds, void* out, int64_t ldo,
+                                   int dtype, hipStream_t st) {
+  const int64_t n = rows * ((cols + 7) / 8);
+  const dim3 g((unsigned)std::min<int64_t>((n + 255) / 256, 1 << 20));
+  if (dtype == MOE_BF16)
+    hipLaunchKernelGGL(k_mx_values<uint16_t>, g, dim3(256), 0, st, rows, cols, q, ldq, scale, lds,
+                       static_cast<uint16_t*>(out), ldo);
+  else
+    hipLaunchKernelGGL(k_mx_values<float>, g, dim3(256), 0, st, rows, cols, q, ldq, scale, lds,
+                       static_cast<float*>(out), ldo);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -1,0 +1,378 @@
+"""MXFP4: the quantiser, its values, the product and the experts against their definitions.
+
+Tolerances: the quantiser's codes and scales, and the values of codes, bit for bit (every step of
+it is exact in fp32).  The product: a product of two codes is a multiple of 1/4 up to 36 and a
+block's sum of 32 of them has 13 bits, so it is exact; the nb blocks' sums are added in fp32, each
+addition rounded or truncated, with those of the split and of the accumulation: (nb + 8) 2^-23 of
+sum |a b|.  A bf16 output has half a step more, 2^-8 of the result."""
+import pytest
+
+from mxfp4_cases import GRID, buffers, operand, quantize, up, values
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from mixture_experts_layer_added_amd import _lib
+    _lib.lib()
+
+
+def code(L, dtype):
+    return L.MOE_F32 if dtype == "f32" else L.MOE_BF16
+
+
+# ---------------------------------------------------------------------------
+# quantiser
+# ---------------------------------------------------------------------------
+def run_quantize(x, cols, dtype, form, random=None, pad=1):
+    """The call on x[:, :cols]; checks that nothing behind the last blocks is written."""
+    from mixture_experts_layer_added_amd import _lib as L
+    rows = x.shape[0]
+    q, s = buffers(rows, cols, pad, 0x55, "cuda")
+    qt, st = buffers(cols, rows, pad, 0x55, "cuda")
+    a, b = form != "cols", form != "rows"
+    r = None if random is None else random.cuda()
+    x = x.cuda()
+    L.moe_quantize_mxfp4(x, code(L, dtype), rows, cols, x.shape[1], q if a else None, q.shape[1],
+                         s if a else None, s.shape[1], qt if b else None, qt.shape[1],
+                         st if b else None, st.shape[1], r)
+    torch.cuda.synchronize()
+    kb, kt = up(cols, 32) // 32, up(rows, 32) // 32
+    assert bool((q[:, 16 * kb if a else 0:] == 0x55).all())
+    assert bool((s[:, kb if a else 0:] == 0x55).all())
+    assert bool((qt[:, 16 * kt if b else 0:] == 0x55).all())
+    assert bool((st[:, kt if b else 0:] == 0x55).all())
+    return (q.cpu()[:, :16 * kb], s.cpu()[:, :kb]), (qt.cpu()[:, :16 * kt], st.cpu()[:, :kt])
+
+
+@pytest.mark.parametrize("random", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols,pad", [(1, 1, 0), (1, 8, 0), (3, 7, 1), (16, 128, 0),
+                                           (33, 129, 0), (128, 128, 8), (129, 255, 1),
+                                           (200, 640, 24), (1, 4099, 0), (4099, 1, 0),
+                                           (300, 264, 0)])
+def test_quantize(rows, cols, pad, dtype, random):
+    g = torch.Generator().manual_seed(rows * 7 + cols)
+    x = torch.randn((rows, cols + pad), generator=g)
+    x *= 10.0 ** torch.randint(-5, 4, (rows, 1), generator=g)
+    x[rows // 2] = 0
+    x = x.to(DT[dtype])
+    x[:, cols:] = float("nan")  # behind the row: not read
+    r = torch.randint(0, 256, (rows, cols), generator=g, dtype=torch.uint8) if random else None
+    want = quantize(x[:, :cols], r), quantize(x[:, :cols].t(), None if r is None else r.t())
+    for form in ("rows", "cols", "both"):
+        got = run_quantize(x, cols, dtype, form, r)
+        for i in (0, 1):
+            if form != ("cols", "rows")[i]:
+                assert torch.equal(got[i][1], want[i][1])
+                assert torch.equal(got[i][0], want[i][0])
+
+
+@pytest.mark.parametrize("random", [False, True])
+def test_quantize_borders(random):
+    """Values on and next to the middles between codes and the ends of the scales, at every scale,
+    zeros of both signs, and blocks whose scale is the smallest."""
+    g = torch.Generator().manual_seed(5)
+    mid = torch.cat([(GRID[1:] + GRID[:-1]) / 2, GRID, torch.tensor([6.5, 7.0, 7.5, 7.999])])
+    n = 254 * 8
+    e = torch.arange(n) % 254
+    pick = mid[torch.randint(0, len(mid), (n, 32), generator=g)]
+    x = (pick * 2.0 ** (e.double()[:, None] - 126)).float()
+    step = torch.randint(-1, 2, x.shape, generator=g)
+    x = torch.where(step < 0, torch.nextafter(x, torch.zeros(())),
+                    torch.where(step > 0, torch.nextafter(x, torch.full((), 3.4e38)), x))
+    x = torch.where(x.isfinite(), x, 1.0)
+    x *= torch.where(torch.rand(x.shape, generator=g) < 0.5, -1.0, 1.0)
+    x[0] = 0
+    x[1] = -0.0
+    x[2], x[3], x[4] = 1e-45, 3e-39, 2.0 ** -126
+    r = torch.randint(0, 256, x.shape, generator=g, dtype=torch.uint8) if random else None
+    (q, s), _ = run_quantize(x, 32, "f32", "rows", r)
+    want = quantize(x, r)
+    assert torch.equal(s, want[1]) and torch.equal(q, want[0])
+    y = x.t().contiguous()
+    _, (q, s) = run_quantize(y, n, "f32", "cols", None if r is None else r.t().contiguous())
+    assert torch.equal(s, want[1]) and torch.equal(q, want[0])
+
+
+@pytest.mark.parametrize("random", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_quantize_not_finite(dtype, random):
+    """A NaN or an infinity makes its block NaN, along the rows and along the columns, and no
+    other."""
+    x = torch.randn((130, 200), generator=torch.Generator().manual_seed(3)).to(DT[dtype])
+    x[0, 0], x[5, 70], x[64, 199], x[129, 33] = float("nan"), float("inf"), -float("inf"), -float(
+        "nan")
+    r = torch.full(x.shape, 77, dtype=torch.uint8) if random else None
+    got = run_quantize(x, 200, dtype, "both", r)
+    want = quantize(x, r), quantize(x.t(), None if r is None else r.t())
+    for i in (0, 1):
+        assert int((want[i][1] == 255).sum()) == 4
+        assert torch.equal(got[i][1], want[i][1]) and torch.equal(got[i][0], want[i][0])
+
+
+def test_random_mean():
+    """Over all 256 bytes a value's mean is within 1/512 of a step of it."""
+    v = torch.linspace(-5.9, 5.9, 31)
+    x = torch.cat([v, torch.tensor([6.0])]).repeat(256, 1)
+    r = torch.arange(256, dtype=torch.uint8)[:, None].expand(256, 32).contiguous()
+    (q, s), _ = run_quantize(x, 32, "f32", "rows", r)
+    mean = values(q, s, 32).mean(0)
+    step = torch.where(x[0].abs() < 2, 0.5, torch.where(x[0].abs() < 4, 1.0, 2.0)).double()
+    assert bool(((mean - x[0].double()).abs() <= step / 512 + 1e-12).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols,pad", [(1, 1, 0), (7, 31, 3), (255, 33, 0), (64, 256, 8)])
+def test_values(rows, cols, pad, dtype):
+    from mixture_experts_layer_added_amd import _lib as L
+    g = torch.Generator().manual_seed(cols)
+    q, s = buffers(rows, cols, 1)
+    q = torch.randint(0, 256, q.shape, generator=g, dtype=torch.uint8)
+    s = torch.randint(0, 256, s.shape, generator=g, dtype=torch.uint8)
+    out = torch.full((rows, cols + pad), 7.0, dtype=DT[dtype], device="cuda")
+    qd, sd = q.cuda(), s.cuda()
+    L.moe_dequantize_mxfp4(rows, cols, qd, q.shape[1], sd, s.shape[1], out, cols + pad,
+                           code(L, dtype))
+    torch.cuda.synchronize()
+    assert bool((out[:, cols:] == 7).all())
+    want = values(q, s, cols).to(DT[dtype])
+    assert torch.equal(out[:, :cols].cpu().nan_to_num(nan=11), want.nan_to_num(nan=11))
+
+
+# ---------------------------------------------------------------------------
+# product
+# ---------------------------------------------------------------------------
+def check_product(c, A, B, c0=None, nb=None):
+    """c against A B^T (+ c0) in 64 bits."""
+    nb = up(A.shape[1], 32) // 32 if nb is None else nb
+    want, size = A @ B.t(), A.abs() @ B.abs().t()
+    if c0 is not None:
+        want, size = want + c0.double(), size + c0.double().abs()
+    tol = (nb + 8) * 2.0 ** -23 * size
+    if c.dtype == torch.bfloat16:
+        tol = tol * (1 + 2.0 ** -8) + 2.0 ** -8 * want.abs()
+    err = (c.double() - want).abs()
+    assert bool((err <= tol).all()), float((err - tol).max())
+
+
+def product(a, b, M, N, K, out, ldc=None, c0=None):
+    from mixture_experts_layer_added_amd import _lib as L
+    (aq, as_), (bq, bs) = a, b
+    ldc = N if ldc is None else ldc
+    c = torch.full((M, ldc), 3.0, dtype=DT[out], device="cuda")
+    if c0 is not None:
+        c[:, :N] = c0.cuda()
+    n = L.moe_gemm_mxfp4_workspace_bytes(M, N, K)
+    ws = torch.full((max(n, 16),), 0xff, dtype=torch.uint8, device="cuda")
+    dev = [t.cuda() for t in (aq, as_, bq, bs)]
+    L.moe_gemm_mxfp4(M, N, K, dev[0], aq.shape[1], dev[1], as_.shape[1], dev[2], bq.shape[1],
+                     dev[3], bs.shape[1], c, ldc, code(L, out), 0 if c0 is None else 1, ws, n)
+    torch.cuda.synchronize()
+    assert bool((c[:, N:] == 3).all())
+    return c[:, :N].cpu()
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K,pad", [
+    (1, 1, 1, 0), (1, 16, 32, 0), (1, 700, 2048, 0), (7, 33, 95, 1), (16, 16, 256, 0),
+    (17, 100, 300, 0), (32, 130, 1000, 2), (33, 65, 64, 0), (100, 200, 31, 0), (128, 128, 256, 0),
+    (129, 127, 257, 1), (130, 300, 4099, 0), (300, 520, 700, 0), (64, 4096, 512, 0),
+    (1000, 70, 2048, 0), (257, 129, 511, 3), (40, 40, 16384, 0)])
+def test_product(M, N, K, pad, out):
+    g = torch.Generator().manual_seed(M * 3 + N * 5 + K)
+    a = torch.randn((M, K), generator=g) * 2.0 ** torch.randint(-9, 9, (M, 1), generator=g)
+    b = torch.randn((N, K), generator=g) * 2.0 ** torch.randint(-9, 9, (N, 1), generator=g)
+    a, b = operand(a, pad), operand(b, pad)  # the pads hold NaN scales
+    if K % 32:  # codes of the last blocks past K that are no zeros
+        for q, _ in (a, b):
+            last = q[:, (K // 32) * 16:up(K, 32) // 2]
+            k = torch.arange(up(K, 32) - 32, up(K, 32)).view(16, 2)
+            last |= torch.where(k[:, 0] >= K, 7, 0).to(torch.uint8)
+            last |= torch.where(k[:, 1] >= K, 0x70, 0).to(torch.uint8)
+    A, B = values(*a, K), values(*b, K)
+    check_product(product(a, b, M, N, K, out), A, B)
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 40, 100), (130, 300, 1024), (70, 64, 8192)])
+def test_product_accumulates(M, N, K):
+    g = torch.Generator().manual_seed(M)
+    a, b = operand(torch.randn((M, K), generator=g)), operand(torch.randn((N, K), generator=g))
+    c0 = torch.randn((M, N), generator=g) * 30
+    c = product(a, b, M, N, K, "f32", ldc=N + 5, c0=c0)
+    check_product(c, values(*a, K), values(*b, K), c0)
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_product_large(out):
+    """Tiles of 256 x 256 (at least 192 of them), with ragged edges and a partial last step, against
+    rows of the definition."""
+    M, N, K = 3000, 4200, 608
+    g = torch.Generator().manual_seed(1)
+    a, b = operand(torch.randn((M, K), generator=g)), operand(torch.randn((N, K), generator=g))
+    c = product(a, b, M, N, K, out)
+    rows = torch.cat([torch.arange(0, M, 37), torch.arange(M - 70, M)])
+    check_product(c[rows], values(*a, K)[rows], values(*b, K))
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 50, 320), (20, 50, 352), (150, 200, 320), (50, 200, 8192)])
+def test_product_nan_and_infinity(M, N, K):
+    """A NaN block reaches its row or column and nothing else; sums past the range are infinite."""
+    g = torch.Generator().manual_seed(2)
+    a, b = operand(torch.randn((M, K), generator=g)), operand(torch.randn((N, K), generator=g))
+    a[1][1, 3], b[1][7, 0] = 255, 255
+    a[1][2, :K // 32] = 253  # one row whose products pass the range
+    b[1][8, :K // 32] = 200
+    c = product(a, b, M, N, K, "f32")
+    A, B = values(*a, K), values(*b, K)
+    assert bool(c[1].isnan().all()) and bool(c[:, 7].isnan().all())
+    rows = [m for m in range(M) if m not in (1, 2)]
+    cols = [n for n in range(N) if n != 7]
+    check_product(c[rows][:, cols], A[rows], B[cols])
+    assert not bool(c[2, 8].isfinite())
+
+
+def test_product_rows_behind():
+    """Operands that end with their last block's codes: nothing behind them is needed."""
+    from mixture_experts_layer_added_amd import _lib as L
+    for M, N, K in ((5, 20, 96), (70, 200, 96), (200, 130, 288)):
+        g = torch.Generator().manual_seed(K)
+        A, B = torch.randn((M, K), generator=g), torch.randn((N, K), generator=g)
+        nb = K // 32
+        dev = []
+        for x in (A, B):
+            q, s = operand(x, 2)
+            flat = torch.cat([q.flatten()[:(len(x) - 1) * q.shape[1] + 16 * nb]])
+            dev.append((flat.cuda(), s.cuda(), q.shape[1], s.shape[1], values(q, s, K)))
+        (a, sa, lda, la, va), (b, sb, ldb, lb, vb) = dev
+        c = torch.empty((M, N), device="cuda")
+        n = L.moe_gemm_mxfp4_workspace_bytes(M, N, K)
+        ws = torch.empty((max(n, 16),), dtype=torch.uint8, device="cuda")
+        L.moe_gemm_mxfp4(M, N, K, a, lda, sa, la, b, ldb, sb, lb, c, N, L.MOE_F32, 0, ws, n)
+        torch.cuda.synchronize()
+        check_product(c.cpu(), va, vb)
+
+
+# ---------------------------------------------------------------------------
+# experts
+# ---------------------------------------------------------------------------
+def groups(counts, T, S, seed):
+    g = torch.Generator().manual_seed(seed)
+    off = [0]
+    for c in counts:
+        off.append(off[-1] + c)
+    token = [torch.randint(0, T, (off[-1],), generator=g)]
+    return off, torch.cat(token)
+
+
+def run_experts(T, H, I, counts, seed, S=0, K=None, ldx=0, ldh=0, x=None, w=None):
+    """moe_pack / up / down over groups of `counts` rows; returns what they read and wrote."""
+    from mixture_experts_layer_added_amd import _lib as L
+    g = torch.Generator().manual_seed(seed)
+    NG, E = len(counts), len(counts) - S
+    off, token = groups(counts, T, S, seed)
+    K = K or -(-off[-1] // T)
+    p = L.problem(T, H, E, 1, 1, min(K, E), 1, I, S, L.MOE_BF16, L.MOE_MXFP4)
+    R = max(off[-1], T * (min(K, E) + S)) + 3
+    x = torch.randn((T, H), generator=g) if x is None else x
+    xq, xs = operand(x, ldx)
+    xq = xq[:, :H // 2].contiguous()
+    w = w or [(torch.randn((2 * I, H), generator=g) * 0.1, torch.randn((H, I), generator=g) * 0.1)
+              for _ in range(NG)]
+    q13 = [quantize(a) for a, _ in w]
+    q2 = [quantize(b) for _, b in w]
+    w13, s13 = torch.stack([a for a, _ in q13]), torch.stack([b for _, b in q13])
+    w2, s2 = torch.stack([a for a, _ in q2]), torch.stack([b for _, b in q2])
+    dev = dict(xq=xq, xs=xs, w13=w13, s13=s13, w2=w2, s2=s2)
+    dev = {k: v.contiguous().cuda() for k, v in dev.items()}
+    p13 = torch.empty((L.moe_mxfp4_packed_bytes(NG, 2 * I, H),), dtype=torch.uint8, device="cuda")
+    p2 = torch.empty((L.moe_mxfp4_packed_bytes(NG, H, I),), dtype=torch.uint8, device="cuda")
+    L.moe_pack_expert_weights_mxfp4(p, dev["w13"], dev["s13"], dev["w2"], dev["s2"], p13, p2)
+    hq = torch.full((R, I // 2), 0x55, dtype=torch.uint8, device="cuda")
+    hs = torch.full((R, up(I // 32, 16) + ldh), 0x55, dtype=torch.uint8, device="cuda")
+    y = torch.full((R, H), 5.0, dtype=torch.bfloat16, device="cuda")
+    offs = torch.tensor(off, dtype=torch.int32, device="cuda")
+    tok = torch.cat([token, torch.full((R - off[-1],), -5)]).to(torch.int32).cuda()
+    L.moe_expert_ffn_up_mxfp4(p, dev["xq"], dev["xs"], xs.shape[1], tok, offs, p13, hq, hs,
+                              hs.shape[1])
+    L.moe_expert_ffn_down_mxfp4(p, hq, hs, hs.shape[1], offs, p2, y)
+    torch.cuda.synchronize()
+    X = values(xq, xs, H)
+    return dict(off=off, token=token, X=X, hq=hq.cpu(), hs=hs.cpu(), y=y.cpu(),
+                W13=[values(a, b, H) for a, b in q13], W2=[values(a, b, I) for a, b in q2])
+
+
+def half_step(v, s):
+    """Half the step of the codes at magnitudes v under scales s."""
+    a = v / s
+    return s * torch.where(a < 2, 0.25, torch.where(a < 4, 0.5, 1.0))
+
+
+def check_experts(r, H, I):
+    """h within half a step of its definition and the error of the sums and of silu; y from the h
+    that was written."""
+    off, nb = r["off"], H // 32
+    n = off[-1]
+    assert bool((r["hq"][n:] == 0x55).all() and (r["hs"][n:] == 0x55).all())
+    assert bool((r["hs"][:, I // 32:] == 0x55).all())
+    assert bool((r["y"][n:] == 5).all())
+    for e, (lo, hi) in enumerate(zip(off[:-1], off[1:])):
+        if lo == hi:
+            continue
+        X, W = r["X"][r["token"][lo:hi]], r["W13"][e]
+        au, size = X @ W.t(), X.abs() @ W.abs().t()
+        err = (nb + 8) * 2.0 ** -23 * size
+        a, u, ea, eu = au[:, :I], au[:, I:], err[:, :I], err[:, I:]
+        sil = a / (1 + torch.exp(-a))
+        # silu's slope is below 1.1; its exponential is off by 2^-24 |a| (the argument's rounding)
+        # and a few units of 2^-23, the quotient and the product by as much
+        es = 1.1 * ea + sil.abs() * (a.abs() + 8) * 2.0 ** -22
+        h = sil * u
+        eh = es * (u.abs() + eu) + sil.abs() * eu + h.abs() * 2.0 ** -23
+        got = values(r["hq"][lo:hi], r["hs"][lo:hi], I)
+        sc = r["hs"][lo:hi, :I // 32]
+        top, et = h.abs().view(hi - lo, -1, 32), eh.view(hi - lo, -1, 32)
+        low = quantize((top - et).clamp(min=0).flatten(1))[1]
+        high = quantize((top + et).flatten(1))[1]
+        assert bool(((sc >= low) & (sc <= high) | (sc == quantize(h)[1])).all())
+        s = (2.0 ** (sc.double() - 127)).repeat_interleave(32, 1)
+        assert bool(((got - h).abs() <= half_step(h.abs() + eh, s) + eh).all())
+        check_product(r["y"][lo:hi], got, r["W2"][e])
+
+
+@pytest.mark.parametrize("T,H,I,counts,S", [
+    (1, 128, 128, [1], 0), (5, 256, 128, [3, 0, 5, 1], 0), (40, 384, 256, [31, 32, 33, 1], 1),
+    (70, 128, 384, [64, 65, 0, 0, 70], 1), (129, 512, 128, [96, 97, 127, 128, 129], 0),
+    (300, 640, 256, [300, 257, 0, 130], 1), (16, 1152, 640, [2] * 24, 0)])
+def test_experts(T, H, I, counts, S):
+    check_experts(run_experts(T, H, I, counts, seed=T + H, S=S, ldx=1, ldh=16), H, I)
+
+
+def test_experts_empty():
+    """No rows at all: nothing is written."""
+    r = run_experts(4, 256, 256, [0, 0, 0], seed=9, K=1)
+    check_experts(r, 256, 256)
+
+
+def test_experts_nan_and_large():
+    """A token with a NaN block: its rows of h and y are NaN, and no others.  Values of h past the
+    range become NaN blocks too (infinity quantises to NaN)."""
+    T, H, I = 40, 256, 128
+    g = torch.Generator().manual_seed(0)
+    x = torch.randn((T, H), generator=g)
+    x[3, 200] = float("inf")
+    x[5] *= 1e30
+    r = run_experts(T, H, I, [40, 40], seed=1, x=x)
+    for lo, hi in ((0, 40), (40, 80)):
+        tok = r["token"][lo:hi]
+        got = r["y"][lo:hi].isnan().any(1)
+        assert torch.equal(got, (tok == 3) | (tok == 5))
+        assert bool(r["y"][lo:hi][tok == 3].isnan().all())
+        ok = (tok != 3) & (tok != 5)
+        want = values(r["hq"][lo:hi][ok], r["hs"][lo:hi][ok], I)
+        check_product(r["y"][lo:hi][ok], want, r["W2"][lo // 40])
