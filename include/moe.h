@@ -600,7 +600,8 @@ moe_status moe_pack_expert_weights_mxfp4(const moe_problem* p, const void* w13,
 /* x_q [T, H/2], x_scale [T, ldxs] (moe_quantize_mxfp4 of x) -> h_q [R, I/2], h_scale [R, ldhs].
  * Row r of group g, offsets[g] <= r < offsets[g+1], is token sorted_token[r]; rows of no group are
  * left as they were, groups may be empty.  offsets [E+S+1] ascending, within [0, R]; sorted_token
- * within [0, T).  Limits (checked): T*H/2 and T*ldxs < 2^31 - 16. */
+ * within [0, T).  Limits (checked): T*H/2 and T*ldxs < 2^31 - 16, (E+S+R/128) max(2I,H)/256 <
+ * 2^23 (both calls). */
 moe_status moe_expert_ffn_up_mxfp4(const moe_problem* p, const void* x_q, const void* x_scale,
                                    int64_t ldxs, const int32_t* sorted_token,
                                    const int32_t* offsets, const void* w13_packed, void* h_q,

@@ -913,6 +913,15 @@ static moe_status require_mxfp4(const Dims& d, const char* call) {
   return MOE_OK;
 }
 
+// a workgroup of 256 threads a tile of 128 rows x 256 columns, somewhat more of them than tiles,
+// and a launch holds fewer than 2^32 threads
+static moe_status check_mx_tiles(const Dims& d) {
+  const int64_t wide = d.H > 2 * d.I ? d.H : 2 * d.I;
+  if ((d.E + d.S + d.R() / 128) * ((wide + 255) / 256) >= ((int64_t)1 << 23))
+    return fail(MOE_ERR_INVALID_ARG, "(E+S+R/128)*max(2I,H)/256 must be < 2^23");
+  return MOE_OK;
+}
+
 // codes and scales of a quantised matrix [rows, cols]: `name` in messages
 static moe_status check_mx(const char* name, const void* q, int64_t ldq, const void* scale,
                            int64_t lds, int64_t cols) {
@@ -1076,6 +1085,7 @@ moe_status moe_expert_ffn_up_mxfp4(const moe_problem* p, const void* x_q, const 
   moe_status s = validate(p, &d);
   if (s != MOE_OK) return s;
   if ((s = require_mxfp4(d, "moe_expert_ffn_up_mxfp4")) != MOE_OK) return s;
+  if ((s = check_mx_tiles(d)) != MOE_OK) return s;
   REQUIRE_PTR(x_q);
   REQUIRE_PTR(w13_packed);
   REQUIRE_PTR(h_q);
@@ -1104,6 +1114,7 @@ moe_status moe_expert_ffn_down_mxfp4(const moe_problem* p, const void* h_q, cons
   moe_status s = validate(p, &d);
   if (s != MOE_OK) return s;
   if ((s = require_mxfp4(d, "moe_expert_ffn_down_mxfp4")) != MOE_OK) return s;
+  if ((s = check_mx_tiles(d)) != MOE_OK) return s;
   REQUIRE_PTR(h_q);
   REQUIRE_PTR(w2_packed);
   REQUIRE_PTR(y_sorted);

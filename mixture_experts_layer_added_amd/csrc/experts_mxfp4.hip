@@ -17,25 +17,18 @@
 // for all rows; activations (gathered through sorted_token, or in order) go by direct-to-LDS
 // loads into a three-slot ring, 256 of k (a 128-byte line a row) a slot, their scales 16 bytes a
 // row, 512 of k, at a time.  Two workgroups share a CU.
+#include <algorithm>
+
 #include "mxfp4.h"
-#include "schedule.h"
 
 namespace moe {
 namespace {
 
-using sched::build_costs;
-using sched::build_schedule;
-using sched::decode_tile;
-using sched::kMaxGroups;
-using sched::Tile;
-using sched::xcd_boundary;
-
 constexpr int kRows = 128;               // rows of a tile
 constexpr int kUnit = 4352;              // bytes of a (block, step) of packed weights
 constexpr int kSlot = kRows * 128;       // activations of 256 of k
-constexpr int kRing = 3 * kSlot;
+constexpr int kRing = 4 * kSlot;
 constexpr int kScSlot = kRows * 16;      // their scales, of 512 of k
-constexpr int kDeep = 3;                 // weight steps on their way
 constexpr uint32_t kOut = 0x7ffffff0u;   // an offset past every descriptor's range
 
 __device__ __forceinline__ float silu(float a) { return a / (1.0f + __expf(-a)); }
@@ -104,8 +97,8 @@ struct GroupArgs {
   int NG, Kd, nblk, n_out;
 };
 
-// one tile of MS sub-tiles of 32 rows
-template <bool kSwiglu, int MS>
+// one tile of MS sub-tiles of 32 rows, D weight steps on their way
+template <bool kSwiglu, int MS, int D>
 __device__ __forceinline__ void mx_group_tile(const GroupArgs& g, int group, int n_idx,
                                               int64_t row0, int m_rows, char* smem, uint32_t lds0,
                                               uint32_t lds_sc) {
@@ -114,8 +107,9 @@ __device__ __forceinline__ void mx_group_tile(const GroupArgs& g, int group, int
   const int nk = g.Kd / 128, ns = (nk + 1) / 2;
   const int b = 4 * n_idx + wv;
   const bool on = b < g.nblk;  // a wave without a block streams the tile's first one
-  const uint8_t* wp =
-      g.w + ((int64_t)group * g.nblk + (on ? b : 4 * n_idx)) * nk * kUnit + lane * 16;
+  const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t*>(g.w) + ((int64_t)group * g.nblk + (on ? b : 4 * n_idx)) * nk * kUnit, 0,
+      nk * kUnit, 0x00020000);
   const int32_t* gather = g.gather;
   const i32x4 ar = gather ? buffer_rsrc(g.a, (uint32_t)(g.a_rows * g.lda))
                           : buffer_rsrc(g.a + row0 * g.lda, (uint32_t)(m_rows * g.lda));
@@ -133,26 +127,24 @@ __device__ __forceinline__ void mx_group_tile(const GroupArgs& g, int group, int
   const int srow = 64 * (wv & 1) + lane;
   const uint32_t so =
       srow < m_rows ? (uint32_t)((gather ? gather[row0 + srow] : srow) * g.ldsa) : kOut;
-  constexpr int kA = MS + 1;  // loads of a wave and slot
-  auto aload = [&](int s) {   // 256 of k
-    const int sc = min(s, ns - 1);
+  auto aload = [&](int s) {  // 256 of k, and two slots' scales with the even one
+    if ((s & 1) == 0)
+      load16_to_lds(sr, lds_sc + ((s >> 1) % 3) * kScSlot + 1024 * (wv & 1),
+                    so + 16 * (uint32_t)(min(s, ns - 1) >> 1));
+    const bool in = 8 * s + lchunk < 4 * nk;  // past K: zeros
 #pragma unroll
     for (int i = 0; i < MS; ++i)
-      load16_to_lds(ar, lds0 + (s % 3) * kSlot + (32 * i + 8 * wv) * 128,
-                    ao[i] + (uint32_t)sc * 128);
-    // two slots' scales with the even one; the odd one fills an area that nothing reads, so that
-    // every slot brings as many loads
-    const bool now = (s & 1) == 0;
-    load16_to_lds(sr, lds_sc + (now ? ((s >> 1) & 1) * kScSlot + 1024 * (wv & 1) : 2 * kScSlot),
-                  so + 16 * (uint32_t)(sc >> 1));
+      load16_to_lds(ar, lds0 + (s & 3) * kSlot + (32 * i + 8 * wv) * 128,
+                    in ? ao[i] + (uint32_t)s * 128 : kOut);
   };
-  u32x4 wb[kDeep + 1][4];
-  uint32_t ws[kDeep + 1];
+  u32x4 wb[D + 1][4];
+  uint32_t ws[D + 1];
   auto wload = [&](int kk, int buf) {
-    const uint8_t* p = wp + (int64_t)min(kk, nk - 1) * kUnit;
+    const int at = min(kk, nk - 1) * kUnit;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) wb[buf][i] = *reinterpret_cast<const u32x4*>(p + i * 1024);
-    ws[buf] = *reinterpret_cast<const uint32_t*>(p + 4096 - lane * 12);
+    for (int i = 0; i < 4; ++i)
+      wb[buf][i] = __builtin_amdgcn_raw_buffer_load_b128(wr, lane * 16 + i * 1024, at, 0);
+    ws[buf] = __builtin_amdgcn_raw_buffer_load_b32(wr, lane * 4, at + 4096, 0);
   };
   f32x16 acc[MS][2];
 #pragma unroll
@@ -161,50 +153,75 @@ __device__ __forceinline__ void mx_group_tile(const GroupArgs& g, int group, int
     for (int n = 0; n < 2; ++n)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[m][n][e] = 0.0f;
+  // operand i = MS u + m of step kk: sub-tile m's codes at instruction u; and its scales
+  constexpr int kF = 2 * MS, kAhead = 3, kN = kAhead + 1;
+  static_assert((D + 1) * kF % kN == 0, "a turn of the loop ends with the register it began with");
+  u32x4 af[kN];
+  uint32_t sa[2][MS];
+  uint32_t fo[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) fo[i] = (uint32_t)at128(fr, 4 * (i >> 1) + 2 * h + (i & 1));
+  auto frag = [&](int kk, int odd, int i, int buf) {  // odd: kk's parity, known to the compiler
+    kk += i / kF;
+    odd ^= i / kF & 1;
+    const int u = i % kF / MS, m = i % MS;
+    af[buf] = lds16(lds0 + ((kk >> 1) & 3) * kSlot + fo[2 * odd + u] + 4096 * m);
+  };
+  auto scale = [&](int kk, int m, int buf) {
+    kk = min(kk, nk - 1);
+    sa[buf][m] = lds2(lds_sc + ((kk >> 2) % 3) * kScSlot + 4 * (kk & 3) + 16 * fr + 2 * h +
+                      512 * m);
+  };
 
-  // the order A(0) W(0) A(1) W(1) W(2), then at each slot's start A(s + 2) and before each step
-  // W(kk + 3): when slot s begins, A(s) and W(2 s) are the oldest, with A(s + 1) and two steps'
-  // weights behind them
+  // The order of loads: A(0) A(1) W(0) .. W(D-1) A(2), then at each slot's start A(s + 3) and
+  // before each step W(kk + D).  A slot is complete in LDS one slot ahead of its turn, so that the
+  // next step's first operands can be read before this one's products are done.
   __syncthreads();  // the previous tile's LDS use is over before the ring is refilled
   aload(0);
-  wload(0, 0);
   aload(1);
-  wload(1, 1);
-  wload(2, 2);
-  for (int kt = 0; kt < nk; kt += kDeep + 1) {
 #pragma unroll
-    for (int j = 0; j <= kDeep; ++j) {
+  for (int j = 0; j < D; ++j) {
+    wload(j, j);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  aload(2);
+  wait_vm<5 * D + MS>();  // A(0), A(1)
+  asm volatile("s_barrier" ::: "memory");
+#pragma unroll
+  for (int m = 0; m < MS; ++m) scale(0, m, 0);
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) frag(0, 0, i, i % kN);
+  for (int kt = 0; kt < nk; kt += D + 1) {
+    // steps past nk - 1 (at most D) multiply by zeros: with conditions in the loop the waits for the
+    // weights would have to suit every way through it
+#pragma unroll
+    for (int j = 0; j <= D; ++j) {
       const int kk = kt + j;
-      if (kk >= nk) break;
-      const int s = kk >> 1;
       if ((j & 1) == 0) {
-        wait_vm<kA + 10>();
-        __syncthreads();
-        aload(s + 2);
+        // A(kk/2 + 1) is complete: behind it are four steps' weights and A(kk/2 + 2)
+        wait_vm<MS + 20>();
+        asm volatile("s_barrier" ::: "memory");
+        aload((kk >> 1) + 3);
       }
-      wload(kk + kDeep, (j + kDeep) % (kDeep + 1));
+      wload(kk + D, (j + D) % (D + 1));
       __builtin_amdgcn_sched_barrier(0);
-      if (!on) continue;
-      const uint32_t a_at = lds0 + (s % 3) * kSlot;
-      const uint32_t s_at =
-          lds_sc + ((s >> 1) & 1) * kScSlot + 8 * (s & 1) + 4 * (j & 1) + 16 * fr + 2 * h;
-      uint32_t sa[MS];
 #pragma unroll
-      for (int m = 0; m < MS; ++m) sa[m] = lds2(s_at + 512 * m);
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const uint32_t off = (uint32_t)at128(fr, 4 * (j & 1) + 2 * h + u);
-#pragma unroll
-        for (int m = 0; m < MS; ++m) {
-          const u32x4 a = lds16(a_at + 32 * m * 128 + off);
-          if (u == 0) {
-            acc[m][0] = mx_mfma32<0, 0>(wb[j][0], a, acc[m][0], ws[j], sa[m]);
-            acc[m][1] = mx_mfma32<2, 0>(wb[j][2], a, acc[m][1], ws[j], sa[m]);
-          } else {
-            acc[m][0] = mx_mfma32<1, 1>(wb[j][1], a, acc[m][0], ws[j], sa[m]);
-            acc[m][1] = mx_mfma32<3, 1>(wb[j][3], a, acc[m][1], ws[j], sa[m]);
-          }
+      for (int i = 0; i < kF; ++i) {
+        const int u = i / MS, m = i % MS, buf = (j * kF + i) % kN;
+        const uint32_t sm = sa[j & 1][m];
+        if (u == 0) {
+          acc[m][0] = mx_mfma32<0, 0>(wb[j][0], af[buf], acc[m][0], ws[j], sm);
+          acc[m][1] = mx_mfma32<2, 0>(wb[j][2], af[buf], acc[m][1], ws[j], sm);
+        } else {
+          acc[m][0] = mx_mfma32<1, 1>(wb[j][1], af[buf], acc[m][0], ws[j], sm);
+          acc[m][1] = mx_mfma32<3, 1>(wb[j][3], af[buf], acc[m][1], ws[j], sm);
         }
+        // the products stay here, with the reads for later ones between them
+        asm volatile("" : "+v"(acc[m][0]), "+v"(acc[m][1]) : : "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        frag(kk, j & 1, i + kAhead, (j * kF + i + kAhead) % kN);
+        if (u == 1) scale(kk + 1, m, (j + 1) & 1);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
   }
@@ -270,42 +287,134 @@ __device__ __forceinline__ void mx_group_tile(const GroupArgs& g, int group, int
   }
 }
 
-template <bool kSwiglu>
-__global__ __launch_bounds__(256, 2) void k_mx_group(GroupArgs g) {
-  __shared__ __attribute__((aligned(1024))) char smem[kRing];
-  __shared__ __attribute__((aligned(16))) char s_sc[2 * kScSlot + 1024];
-  __shared__ int mt_start[kMaxGroups + 1];
-  // the cost prefix is only needed before the first tile's loads overwrite the ring
-  long long* s_cost = reinterpret_cast<long long*>(smem);
-  static_assert(sizeof(long long) * (kMaxGroups + 1) <= kRing, "cost prefix fits the ring");
-  build_schedule(g.offsets, g.NG, kRows, mt_start);
-  const int nt = (g.nblk + 3) / 4;
-  build_costs(g.offsets, mt_start, g.NG, kRows, nt, s_cost);
-  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(smem));
-  const uint32_t lds_sc = __builtin_amdgcn_readfirstlane(lds_offset(s_sc));
-  const int per_xcd = gridDim.x / kXcds;
-  const int xcd = blockIdx.x % kXcds, slot = blockIdx.x / kXcds;
-  const int begin = xcd_boundary(xcd, g.offsets, mt_start, s_cost, g.NG, kRows, nt);
-  const int end = xcd_boundary(xcd + 1, g.offsets, mt_start, s_cost, g.NG, kRows, nt);
-  for (int tile = begin + slot; tile < end; tile += per_xcd) {
-    const Tile tl = decode_tile(tile, mt_start, g.NG, nt);
-    const int group = __builtin_amdgcn_readfirstlane(tl.g);
-    const int n_idx = __builtin_amdgcn_readfirstlane(tl.n_idx);
-    const int m0 = __builtin_amdgcn_readfirstlane(tl.m_idx) * kRows;
-    const int first = g.offsets[group];
-    const int m_rows = min(kRows, g.offsets[group + 1] - first - m0);
-    const int64_t row0 = (int64_t)first + m0;
-    switch ((m_rows + 31) >> 5) {
-      case 1: mx_group_tile<kSwiglu, 1>(g, group, n_idx, row0, m_rows, smem, lds0, lds_sc); break;
-      case 2: mx_group_tile<kSwiglu, 2>(g, group, n_idx, row0, m_rows, smem, lds0, lds_sc); break;
-      case 3: mx_group_tile<kSwiglu, 3>(g, group, n_idx, row0, m_rows, smem, lds0, lds_sc); break;
-      case 4: mx_group_tile<kSwiglu, 4>(g, group, n_idx, row0, m_rows, smem, lds0, lds_sc); break;
-      default: break;
+// The tile of a workgroup.  Tiles are ordered (group, column of blocks, row tile), so that those
+// that share weights or activations are neighbours, and each XCD takes one contiguous range of an
+// eighth of the cost; a tile's cost is kTileCost and one for each 32 rows.
+// Every wave finds its tile by itself, 64 groups at a time, a lane each: no barrier, and one load's
+// latency where there are no more groups than that.
+struct Pick {
+  int group, n_idx, m0, m_rows;
+  int64_t row0;
+};
+constexpr int kTileCost = 12;
+struct Chunk64 {  // of a lane's group: row tiles, cost, and the sums over all groups before it
+  int mt, c, mt0, c0, first, m;
+};
+__device__ __forceinline__ Chunk64 group_chunk(const int32_t* __restrict__ offsets, int NG, int g0,
+                                               int mt_run, int c_run) {
+  const int lane = threadIdx.x & 63, g = g0 + lane;
+  Chunk64 k;
+  k.first = offsets[min(g, NG)];
+  k.m = offsets[min(g + 1, NG)] - k.first;
+  k.mt = (k.m + kRows - 1) / kRows;
+  k.c = kTileCost * k.mt + (k.m + 31) / 32;
+  int a = k.mt, b = k.c;
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) {
+    const int x = __shfl_up(a, d), y = __shfl_up(b, d);
+    if (lane >= d) {
+      a += x;
+      b += y;
     }
+  }
+  k.mt0 = mt_run + a - k.mt;
+  k.c0 = c_run + b - k.c;
+  return k;
+}
+__device__ __forceinline__ int lane_of(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+
+// f(chunk, its first group) over the groups; one chunk is kept where it is all of them
+template <typename F>
+__device__ __forceinline__ void each_chunk(const int32_t* __restrict__ offsets, int NG,
+                                           const Chunk64& all, F f) {
+  if (NG <= kWave) {
+    f(all, 0);
+    return;
+  }
+  int mt_run = 0, c_run = 0;
+  for (int g0 = 0; g0 < NG; g0 += kWave) {
+    const Chunk64 k = group_chunk(offsets, NG, g0, mt_run, c_run);
+    f(k, g0);
+    mt_run = lane_of(k.mt0 + k.mt, 63);
+    c_run = lane_of(k.c0 + k.c, 63);
   }
 }
 
-int group_grid() { return std::max(device_cu_count() * 2 / kXcds, 1) * kXcds; }
+__device__ __forceinline__ bool pick_tile(const int32_t* __restrict__ offsets, int NG, int nt,
+                                          int xcd, int slot, Pick& p) {
+  const Chunk64 all = group_chunk(offsets, NG, 0, 0, 0);
+  int tiles = 0, cost = 0;
+  each_chunk(offsets, NG, all, [&](const Chunk64& k, int) {
+    tiles = lane_of(k.mt0 + k.mt, 63);
+    cost = lane_of(k.c0 + k.c, 63);
+  });
+  int begin = 0, end = tiles * nt;
+  each_chunk(offsets, NG, all, [&](const Chunk64& k, int g0) {
+    // first tile of XCD x: in the last group that begins at or before x eighths of the cost
+    auto bound = [&](int x, int& at) {
+      const int64_t t = (int64_t)cost * nt * x / kXcds;
+      const bool in = g0 + (int)(threadIdx.x & 63) < NG && (int64_t)k.c0 * nt <= t;
+      const uint64_t mask = __ballot(in);
+      if (!mask) return;
+      const int l = 63 - __clzll(mask), c = lane_of(k.c, l), mt = lane_of(k.mt, l);
+      const int64_t past = t - (int64_t)lane_of(k.c0, l) * nt;
+      const int n = nt * mt;  // tiles of this group
+      at = lane_of(k.mt0, l) * nt + (c ? (int)min((double)n, (double)past * mt / (double)c) : 0);
+    };
+    if (xcd > 0) bound(xcd, begin);
+    if (xcd < kXcds - 1) bound(xcd + 1, end);
+  });
+  const int tile = begin + slot;
+  if (tile >= end) return false;
+  each_chunk(offsets, NG, all, [&](const Chunk64& k, int g0) {
+    const uint64_t mask = __ballot(k.mt > 0 && k.mt0 * nt <= tile);
+    if (!mask) return;
+    const int l = 63 - __clzll(mask), mt = lane_of(k.mt, l);
+    const int local = tile - lane_of(k.mt0, l) * nt;
+    p.group = g0 + l;
+    p.n_idx = local / mt;
+    p.m0 = local % mt * kRows;
+    p.m_rows = min(kRows, lane_of(k.m, l) - p.m0);
+    p.row0 = (int64_t)lane_of(k.first, l) + p.m0;
+  });
+  return true;
+}
+
+template <bool kSwiglu>
+__global__ __launch_bounds__(256, 2) void k_mx_group(GroupArgs g) {
+  __shared__ __attribute__((aligned(1024))) char smem[kRing];
+  __shared__ __attribute__((aligned(16))) char s_sc[3 * kScSlot];
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(smem));
+  const uint32_t lds_sc = __builtin_amdgcn_readfirstlane(lds_offset(s_sc));
+  // One tile a workgroup: the hardware hands them out as others end, so that tiles of all costs fill
+  // the chip (a grid of resident ones with a fixed share of the tiles each left it idle for a sixth
+  // of the time).  There are more workgroups than tiles; those past their XCD's range leave.
+  Pick p;
+  if (!pick_tile(g.offsets, g.NG, (g.nblk + 3) / 4, blockIdx.x % kXcds, blockIdx.x / kXcds, p))
+    return;
+  const int group = __builtin_amdgcn_readfirstlane(p.group);
+  const int n_idx = __builtin_amdgcn_readfirstlane(p.n_idx);
+  const int m_rows = __builtin_amdgcn_readfirstlane(p.m_rows);
+  const int64_t row0 = p.row0;
+#define MX_TILE(MS, D) \
+  case MS: mx_group_tile<kSwiglu, MS, D>(g, group, n_idx, row0, m_rows, smem, lds0, lds_sc); break
+  switch ((m_rows + 31) >> 5) {
+    MX_TILE(1, 7);
+    MX_TILE(2, 7);
+    MX_TILE(3, 3);
+    MX_TILE(4, 3);
+    default: break;
+  }
+#undef MX_TILE
+}
+
+// Workgroups that suffice for R rows in NG groups: nt tiles for each of at most mt row tiles, and in
+// an XCD's range, an eighth of the cost, no more than if all of them had the least cost.
+int64_t group_grid(int64_t R, int NG, int nblk) {
+  const int64_t nt = (nblk + 3) / 4, some = std::min<int64_t>(NG, R), mt = some + R / kRows;
+  const int64_t cost = nt * (kTileCost * mt + R / 32 + some);
+  return std::min(nt * mt, cost / kXcds / (kTileCost + 1) + 2) * kXcds;
+}
 
 }  // namespace
 
@@ -323,7 +432,7 @@ hipError_t launch_ffn_up_mxfp4(const Dims& d, const uint8_t* xq, const uint8_t* 
                                uint8_t* hq, uint8_t* hs, int64_t ldhs, hipStream_t st) {
   GroupArgs g{xq, xs, d.H / 2, ldxs, d.T, gather, offsets, w, hq, hs, d.I / 2, ldhs, nullptr,
               d.E + d.S, d.H, 2 * d.I / 64, d.I};
-  hipLaunchKernelGGL(k_mx_group<true>, dim3(group_grid()), dim3(256), 0, st, g);
+  hipLaunchKernelGGL(k_mx_group<true>, dim3((unsigned)group_grid(d.R(), g.NG, g.nblk)), dim3(256), 0, st, g);
   return hipGetLastError();
 }
 
@@ -332,7 +441,7 @@ hipError_t launch_ffn_down_mxfp4(const Dims& d, const uint8_t* hq, const uint8_t
                                  hipStream_t st) {
   GroupArgs g{hq, hs, d.I / 2, ldhs, 0, nullptr, offsets, w, nullptr, nullptr, 0, 0,
               static_cast<uint16_t*>(y), d.E + d.S, d.I, d.H / 64, d.H};
-  hipLaunchKernelGGL(k_mx_group<false>, dim3(group_grid()), dim3(256), 0, st, g);
+  hipLaunchKernelGGL(k_mx_group<false>, dim3((unsigned)group_grid(d.R(), g.NG, g.nblk)), dim3(256), 0, st, g);
   return hipGetLastError();
 }
 

@@ -21,11 +21,10 @@
 namespace moe {
 namespace {
 
-constexpr int kStep = 256;        // of k
-constexpr int kRow = kStep / 2;   // bytes of a row in a stage
+constexpr int kStep = 256;       // of k, of k_mx_gemm_rows
+constexpr int kRow = kStep / 2;  // bytes of a row in a step
 constexpr uint32_t kOut = 0x7ffffff0u;  // an offset past every descriptor's range
 
-__device__ __forceinline__ int at128(int r, int c) { return r * kRow + ((c ^ (r >> 1)) & 7) * 16; }
 __device__ __forceinline__ u32x4 lds16(uint32_t addr) {
   return *reinterpret_cast<const __attribute__((address_space(3))) u32x4*>((uintptr_t)addr);
 }
@@ -38,7 +37,7 @@ struct GemmArgs {
   void* c;  // C, or the partial sums [splits, M, ldc] fp32
   int64_t lda, ldb, ldsa, ldsb, ldc, M, N, K;
   int mt, nt;         // tiles along M and N
-  int splits, steps;  // k is cut into `splits` parts of `steps` steps
+  int splits, steps;  // k is cut into `splits` parts of `steps` stages
   int c_f32, accumulate;
 };
 
@@ -55,14 +54,17 @@ __device__ __forceinline__ void store16(char* p, uint4 v, int n, bool f32, bool 
         const float4 c = *reinterpret_cast<const float4*>(q);
         o = make_float4(c.x + o.x, c.y + o.y, c.z + o.z, c.w + o.w);
       }
-      *reinterpret_cast<float4*>(q) = o;
+      const u32x4 w4 = {__float_as_uint(o.x), __float_as_uint(o.y), __float_as_uint(o.z),
+                        __float_as_uint(o.w)};
+      __builtin_nontemporal_store(w4, reinterpret_cast<u32x4*>(q));
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (i < n) q[i] = accumulate ? q[i] + w[i] : w[i];
     }
   } else if (vec && n >= 8) {
-    *reinterpret_cast<uint4*>(p) = v;
+    const u32x4 w4 = {v.x, v.y, v.z, v.w};
+    __builtin_nontemporal_store(w4, reinterpret_cast<u32x4*>(p));
   } else {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint16_t* q = reinterpret_cast<uint16_t*>(p);
@@ -72,19 +74,32 @@ __device__ __forceinline__ void store16(char* p, uint4 v, int n, bool f32, bool 
   }
 }
 
-template <int BM, int BN, int WM, int WN, int NST>
+// kParts: 128 of k a part, a stage holds one or two of them (rows of 64 or 128 bytes, 16-byte chunks
+// xor-swizzled by the row so that 8 rows read at one chunk lie in different banks)
+template <int kParts>
+__device__ __forceinline__ int chunk_at(int r, int c) {
+  if (kParts == 2) return r * 128 + ((c ^ (r >> 1)) & 7) * 16;
+  return r * 64 + ((c ^ (r >> 2)) & 3) * 16;
+}
+
+template <int BM, int BN, int WM, int WN, int kParts, int NST>
 __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_gemm(GemmArgs g) {
   constexpr int W = WM * WN, SM = BM / WM / 32, SN = BN / WN / 32;
-  constexpr int kStage = (BM + BN) * kRow, kScBuf = (BM + BN) * 16;
-  constexpr int NA = BM / 8 / W, NB = BN / 8 / W;  // code loads of a wave and step
+  constexpr int kChunks = 4 * kParts, kRowB = 16 * kChunks, kStage = (BM + BN) * kRowB;
+  constexpr int kRpi = 1024 / kRowB;  // rows of a load instruction
+  constexpr int kPerSc = 4 / kParts;  // stages of 16 bytes of scales
+  constexpr int kScBuf = (BM + BN) * 16;
+  constexpr int NA = BM / kRpi / W, NB = BN / kRpi / W;      // code loads of a wave and stage
   constexpr int kG = (BM + BN) / 64, NS = (kG + W - 1) / W;  // scale loads: 64 rows each
-  constexpr int kPer = NA + NB + NS;
-  static_assert(BM % (8 * W) == 0 && BN % (8 * W) == 0 && BM % 64 == 0 && BN % 64 == 0,
+  constexpr int kPer = NA + NB, kJ = 2 * kParts;             // kJ products a sub-tile and stage
+  static_assert(BM % (kRpi * W) == 0 && BN % (kRpi * W) == 0 && BM % 64 == 0 && BN % 64 == 0,
                 "whole load instructions");
+  static_assert(NST >= 4, "one stage in use, one complete, two on their way");
   static_assert(W * 32 * (BN / WN) * 4 <= NST * kStage, "output staging fits the ring");
   __shared__ __attribute__((aligned(1024))) char smem[NST * kStage];
-  // the scales of two steps, 16 bytes a row, twice; and what a step that brings none fills
-  __shared__ __attribute__((aligned(16))) char s_sc[2 * kScBuf + 1024];
+  // scales of 512 of k, 16 bytes a row: stage kt + 3's arrive while stage kt's are read
+  constexpr int kScBufs = kParts == 2 ? 3 : 2;
+  __shared__ __attribute__((aligned(16))) char s_sc[kScBufs * kScBuf];
   // tiles in bands of 8 row tiles, column-major inside a band, one contiguous range per XCD
   const int total = g.mt * g.nt * g.splits;
   const int per = (total + kXcds - 1) / kXcds;
@@ -100,7 +115,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_gemm(GemmArgs g) {
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wv / WN, wn = wv % WN, fr = lane & 31, h = lane >> 5;
   const int nb = (int)((g.K + kMxBlock - 1) / kMxBlock);  // blocks of k
-  const int nk = (nb + 7) / 8;
+  const int nk = (nb + kChunks - 1) / kChunks;
   const int k0 = part * g.steps, k1 = min(k0 + g.steps, nk);
   const int m_rows = (int)min((int64_t)BM, g.M - m0), n_rows = (int)min((int64_t)BN, g.N - n0);
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(smem));
@@ -110,38 +125,41 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_gemm(GemmArgs g) {
   const i32x4 br = buffer_rsrc(g.b + n0 * g.ldb, (uint32_t)((n_rows - 1) * g.ldb + 16 * nb));
   const i32x4 sar = buffer_rsrc(g.sa + m0 * g.ldsa, (uint32_t)(m_rows * g.ldsa));
   const i32x4 sbr = buffer_rsrc(g.sb + n0 * g.ldsb, (uint32_t)(n_rows * g.ldsb));
-  // instruction i of wave wv fills rows 8 (i W + wv) .. +7 of the stage (A's, then B's)
-  const int lrow = 8 * wv + (lane >> 3);
-  const int lchunk = (lane & 7) ^ ((4 * (wv & 1) + (lane >> 4)) & 7);
-  uint32_t ao[NA], bo[NB];
+  // instruction i of wave wv fills rows kRpi (i W + wv) .. of the stage (A's, then B's)
+  const int lrow = kRpi * wv + lane / kChunks;
+  const int lchunk = kParts == 2 ? (lane & 7) ^ ((4 * (wv & 1) + (lane >> 4)) & 7)
+                                 : (lane & 3) ^ (lane >> 4);
+  const uint32_t ao = (uint32_t)(lrow * g.lda) + 16 * lchunk;
+  const uint32_t bo = (uint32_t)(lrow * g.ldb) + 16 * lchunk;
+  const uint32_t a_next = (uint32_t)(kRpi * W * g.lda), b_next = (uint32_t)(kRpi * W * g.ldb);
+  uint32_t so[NS];  // scale load i: rows 64 q .. +63 of A, then of B, q = i W + wv
 #pragma unroll
-  for (int i = 0; i < NA; ++i) ao[i] = (uint32_t)((8 * W * i + lrow) * g.lda) + 16 * lchunk;
-#pragma unroll
-  for (int i = 0; i < NB; ++i) bo[i] = (uint32_t)((8 * W * i + lrow) * g.ldb) + 16 * lchunk;
-  // load instruction i (of kPer) of a wave for step kt's stage; past the last step it fetches
-  // what nothing reads
+  for (int i = 0; i < NS; ++i) {
+    const int q = i * W + wv;
+    so[i] = (uint32_t)(q < BM / 64 ? (64 * q + lane) * g.ldsa : (64 * q - BM + lane) * g.ldsb);
+  }
+  // load instruction i (of kPer) of a wave for stage kt; past the last stage it fetches what nothing
+  // reads
   auto load = [&](int kt, int st, int i) {
-    const uint32_t dst = lds0 + st * kStage + 8 * wv * kRow, ko = (uint32_t)kt * kRow;
-    const bool in = 8 * kt + lchunk < nb;
-    if (i < NA) {
-      load16_to_lds(ar, dst + i * 8 * W * kRow, in ? ao[i] + ko : kOut);
-    } else if (i < NA + NB) {
-      load16_to_lds(br, dst + (BM + (i - NA) * 8 * W) * kRow,
-                    in ? bo[i < NA + NB ? i - NA : 0] + ko : kOut);
-    } else {  // the scales of steps kt and kt + 1: rows 64 q .. +63 of A, then of B
-      const int q = (i - NA - NB) * W + wv;
-      const bool now = q < kG && ((kt & 1) == 0 || kt == k0);
-      const bool of_a = q < BM / 64;
-      const int row = 64 * (of_a ? q : q - BM / 64) + lane;
-      load16_to_lds(of_a ? sar : sbr,
-                    lds_sc + (now ? ((kt >> 1) & 1) * kScBuf + 1024 * q : 2 * kScBuf),
-                    now ? (uint32_t)(row * (of_a ? g.ldsa : g.ldsb)) + 16 * (uint32_t)(kt >> 1)
-                        : kOut);
-    }
+    const uint32_t dst = lds0 + st * kStage + wv * 1024, ko = (uint32_t)kt * kRowB;
+    const bool in = kChunks * kt + lchunk < nb;
+    if (i < NA)
+      load16_to_lds(ar, dst + i * W * 1024, in ? ao + (i * a_next + ko) : kOut);
+    else
+      load16_to_lds(br, dst + BM * kRowB + (i - NA) * W * 1024,
+                    in ? bo + ((i - NA) * b_next + ko) : kOut);
   };
-  auto stage = [&](int kt, int st) {
+  // the scales of stage kt and of those that share its 16 bytes, with the first of them
+  auto load_scales = [&](int kt) {
+    if (kt % kPerSc != 0) return;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) load(kt, st, i);
+    for (int i = 0; i < NS; ++i) {
+      const int q = i * W + wv;
+      if (q < kG)
+        load16_to_lds(q < BM / 64 ? sar : sbr,
+                      lds_sc + kt / kPerSc % kScBufs * kScBuf + 1024 * q,
+                      so[i] + 16 * (uint32_t)(kt / kPerSc));
+    }
   };
 
   f32x16 acc[SM][SN];
@@ -152,67 +170,109 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_gemm(GemmArgs g) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[m][n][i] = 0.0f;
 
-#pragma unroll
-  for (int j = 0; j < NST - 1; ++j) stage(k0 + j, j);
-  int st = 0;
-  for (int kt = k0; kt < k1; ++kt) {
-    wait_vm<(NST - 2) * kPer>();
+  // Blocks past K have zero codes (their loads are out of range), and their scales become 2^-127: the
+  // pad may hold the NaN.  Once the last 512 of k's have come, before any is read.
+  auto clear_scales = [&](int kt) {
+    if (nb % 16 == 0 || kt / kPerSc != (nk - 1) / kPerSc) return;
+    char* sc = s_sc + kt / kPerSc % kScBufs * kScBuf;
+    for (int r = tid; r < BM + BN; r += 64 * W)
+      for (int b = nb % 16; b < 16; ++b) sc[16 * r + b] = 0;
     __syncthreads();
-    const int kt_ld = kt + NST - 1, st_ld = st == 0 ? NST - 1 : st - 1;
-    if (kt == nk - 1 && (g.K & (kStep - 1))) {
-      // the last step's blocks past K: their codes are zeros, their scales become 2^-127, not what
-      // the pad holds, which may be the NaN; and the last block's codes past K are cleared in A
-      char* sc = s_sc + ((kt >> 1) & 1) * kScBuf + 8 * (kt & 1);
-      const int left = nb - 8 * kt;  // blocks of this step
-      for (int r = tid; r < BM + BN; r += 64 * W) {
-        for (int b = left; b < 8; ++b) sc[16 * r + b] = 0;
-        const int n = (int)(g.K & (kMxBlock - 1));
-        if (n && r < BM) {
-          uint32_t* p = reinterpret_cast<uint32_t*>(smem + st * kStage + at128(r, left - 1));
+  };
+  // The last block's codes past K are cleared in A, once the last stage has come.
+  auto clear_codes = [&](int kt, int st) {
+    const int n = (int)(g.K & (kMxBlock - 1));
+    if (n == 0 || kt != nk - 1) return;
+    for (int r = tid; r < BM; r += 64 * W) {
+      uint32_t* p = reinterpret_cast<uint32_t*>(smem + st * kStage +
+                                                chunk_at<kParts>(r, nb - 1 - kChunks * kt));
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (n < 8 * i + 8) p[i] = n > 8 * i ? p[i] & ((1u << (4 * (n - 8 * i))) - 1u) : 0u;
+      for (int i = 0; i < 4; ++i)
+        if (n < 8 * i + 8) p[i] = n > 8 * i ? p[i] & ((1u << (4 * (n - 8 * i))) - 1u) : 0u;
+    }
+    __syncthreads();
+  };
+  u32x4 fa[2][SM], fb[2][SN];  // operands of the product at hand and of the next
+  u32x4 qa[SM], qb[SN];        // scales of 512 of k, 4 bytes a part
+  uint32_t sa[SM], sb[SN];     // of the part at hand: the lane's two
+  // operand i (A's, then B's) of product j = 2 s + u of stage st
+  auto frag = [&](int st, int j, int buf, int i) {
+    const uint32_t at = lds0 + st * kStage + chunk_at<kParts>(fr, 4 * (j >> 1) + 2 * h + (j & 1));
+    if (i < SM) fa[buf][i < SM ? i : 0] = lds16(at + (wm * (BM / WM) + 32 * i) * kRowB);
+    else fb[buf][i < SM ? 0 : i - SM] = lds16(at + (BM + wn * (BN / WN) + 32 * (i - SM)) * kRowB);
+  };
+  auto scale = [&](int kt, int i) {  // operand i's scales of the 512 of k with stage kt
+    const uint32_t at = lds_sc + kt / kPerSc % kScBufs * kScBuf + 16 * fr;
+    if (i < SM) qa[i < SM ? i : 0] = lds16(at + 16 * (wm * (BM / WM) + 32 * i));
+    else qb[i < SM ? 0 : i - SM] = lds16(at + 16 * (BM + wn * (BN / WN) + 32 * (i - SM)));
+  };
+  constexpr int kOps = SM + SN, kMul = SM * SN;
+
+#pragma unroll
+  for (int j = 0; j < NST - 1; ++j) {
+    load_scales(k0 + j);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) load(k0 + j, j, i);
+  }
+  wait_vm<(NST - 2) * kPer>();
+  __syncthreads();
+  clear_scales(k0);
+  clear_codes(k0, 0);
+  int st = 0;
+#pragma unroll
+  for (int i = 0; i < kOps; ++i) scale(k0, i);
+#pragma unroll
+  for (int i = 0; i < kOps; ++i) frag(0, 0, 0, i);
+  // k1 - k0 stages, 512 of k a turn of the outer loop (k0 a multiple).  A stage's first
+  // operands are in registers when its turn comes, and the stage after it is complete in LDS behind
+  // its barrier, so that the matrix cores do not run dry at the barriers.
+  for (int kc = k0; kc < k1; kc += kPerSc) {
+#pragma unroll
+    for (int t = 0; t < kPerSc; ++t) {
+      const int kt = kc + t;
+      if (kt >= k1) break;
+      wait_vm<(NST - 3) * kPer>();
+      // nothing but loads fills the ring, and this wave's reads of what is filled next are behind
+      // its products: the barrier alone, without waiting for the reads ahead
+      asm volatile("s_barrier" ::: "memory");
+      const int st1 = st + 1 == NST ? 0 : st + 1, st_ld = st == 0 ? NST - 1 : st - 1;
+      if (t == kPerSc - 1) clear_scales(kt + 1);
+      clear_codes(kt + 1, st1);
+      load_scales(kt + NST - 1);
+#pragma unroll
+      for (int j = 0; j < kJ; ++j) {
+        const int buf = j & 1, part = t * kParts + (j >> 1);  // of the 512 of k
+        if ((j & 1) == 0) {
+#pragma unroll
+          for (int i = 0; i < SM; ++i) sa[i] = qa[i][part] >> (16 * h);
+#pragma unroll
+          for (int i = 0; i < SN; ++i) sb[i] = qb[i][part] >> (16 * h);
+        }
+#pragma unroll
+        for (int p = 0; p < kMul; ++p) {
+          const int m = p % SM, n = p / SM;
+          acc[m][n] = (j & 1) ? mx_mfma32<1, 1>(fb[buf][n], fa[buf][m], acc[m][n], sb[n], sa[m])
+                              : mx_mfma32<0, 0>(fb[buf][n], fa[buf][m], acc[m][n], sb[n], sa[m]);
+          // what follows each product, in this order (left to the compiler, all of a stage's products
+          // sank below its last LDS read): reads for the next product, a load for the ring
+          asm volatile("" : "+a"(acc[m][n]) : : "memory");
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int i = 0; i < kOps; ++i)
+            if (i * kMul / kOps == p) {
+              if (j + 1 < kJ) frag(st, j + 1, buf ^ 1, i);
+              else frag(st1, 0, buf ^ 1, i);
+              // the next 512 of k's scales, once this one's last are taken
+              if ((j & 1) == 0 && part == 3) scale(kt + 1, i);
+            }
+#pragma unroll
+          for (int i = 0; i < kPer; ++i)
+            if (i * kJ * kMul / kPer == j * kMul + p) load(kt + NST - 1, st_ld, i);
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
-      __syncthreads();
+      st = st1;
     }
-    const uint32_t a_at = lds0 + st * kStage + wm * (BM / WM) * kRow;
-    const uint32_t b_at = lds0 + st * kStage + (BM + wn * (BN / WN)) * kRow;
-    const uint32_t sc_at = lds_sc + ((kt >> 1) & 1) * kScBuf + 8 * (kt & 1) + 16 * fr + 2 * h;
-    u32x4 fa[2][SM], fb[2][SN];
-    uint32_t sa[SM], sb[SN];
-    auto frags = [&](int j, int buf) {  // j = 2 s + u
-      const uint32_t off = (uint32_t)at128(fr, 4 * (j >> 1) + 2 * h + (j & 1));
-#pragma unroll
-      for (int m = 0; m < SM; ++m) fa[buf][m] = lds16(a_at + 32 * m * kRow + off);
-#pragma unroll
-      for (int n = 0; n < SN; ++n) fb[buf][n] = lds16(b_at + 32 * n * kRow + off);
-    };
-    auto scales = [&](int s) {
-#pragma unroll
-      for (int m = 0; m < SM; ++m) sa[m] = lds2(sc_at + 16 * (wm * (BM / WM) + 32 * m) + 4 * s);
-#pragma unroll
-      for (int n = 0; n < SN; ++n)
-        sb[n] = lds2(sc_at + 16 * (BM + wn * (BN / WN) + 32 * n) + 4 * s);
-    };
-    frags(0, 0);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if ((j & 1) == 0) scales(j >> 1);
-      if (j < 3) frags(j + 1, (j + 1) & 1);
-      // the next stage's loads go out between the products
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (i * 4 / kPer == j) load(kt_ld, st_ld, i);
-#pragma unroll
-      for (int n = 0; n < SN; ++n)
-#pragma unroll
-        for (int m = 0; m < SM; ++m)
-          acc[m][n] = (j & 1) ? mx_mfma32<1, 1>(fb[j & 1][n], fa[j & 1][m], acc[m][n], sb[n], sa[m])
-                              : mx_mfma32<0, 0>(fb[j & 1][n], fa[j & 1][m], acc[m][n], sb[n], sa[m]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    if (++st == NST) st = 0;
   }
   wait_vm<0>();
   __syncthreads();  // every wave is done with the ring, which now stages the output
@@ -443,7 +503,8 @@ Plan plan(int64_t M, int64_t N, int64_t K) {
     const double step_us = bn == 64 ? 0.55 : 0.69;
     const int64_t tiles = ((M + 127) / 128) * ((N + bn - 1) / bn);
     for (int64_t s = 1; s == 1 || (s * tiles <= 256 && s <= nk / 4); ++s) {
-      const int64_t steps = (nk + s - 1) / s, parts = (nk + steps - 1) / steps;
+      // a part begins at a multiple of 512 of k
+      const int64_t steps = ((nk + s - 1) / s + 1) / 2 * 2, parts = (nk + steps - 1) / steps;
       double us = (double)((tiles * parts + 255) / 256 * steps) * step_us;
       if (parts > 1) us += 3.0 + 2e-6 * (double)(parts * M * N);
       if (us >= best) continue;
@@ -456,12 +517,13 @@ Plan plan(int64_t M, int64_t N, int64_t K) {
   return p;
 }
 
-template <int BM, int BN, int WM, int WN, int NST>
+template <int BM, int BN, int WM, int WN, int kParts, int NST>
 void launch_tile(GemmArgs g, hipStream_t st) {
+  g.steps *= 2 / kParts;
   g.mt = (int)((g.M + BM - 1) / BM);
   g.nt = (int)((g.N + BN - 1) / BN);
   const int per = (g.mt * g.nt * g.splits + kXcds - 1) / kXcds;
-  hipLaunchKernelGGL((k_mx_gemm<BM, BN, WM, WN, NST>), dim3(per * kXcds), dim3(64 * WM * WN), 0, st,
+  hipLaunchKernelGGL((k_mx_gemm<BM, BN, WM, WN, kParts, NST>), dim3(per * kXcds), dim3(64 * WM * WN), 0, st,
                      g);
 }
 
@@ -488,11 +550,11 @@ hipError_t launch_gemm_mxfp4(int64_t M, int64_t N, int64_t K, const uint8_t* a, 
     if (p.bm == 16) hipLaunchKernelGGL((k_mx_gemm_rows<1, 4>), grid, dim3(512), 0, st, g);
     else hipLaunchKernelGGL((k_mx_gemm_rows<2, 4>), grid, dim3(512), 0, st, g);
   } else if (p.bn == 64) {
-    launch_tile<128, 64, 4, 2, 3>(g, st);
+    launch_tile<128, 64, 4, 2, 2, 4>(g, st);
   } else if (p.bn == 128) {
-    launch_tile<128, 128, 4, 2, 3>(g, st);
+    launch_tile<128, 128, 4, 2, 2, 4>(g, st);
   } else {
-    launch_tile<256, 256, 4, 2, 2>(g, st);
+    launch_tile<256, 256, 4, 2, 1, 4>(g, st);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;

@@ -155,6 +155,9 @@ def test_experts(L):
         ("ldhs", 12, "h_q's scales"), ("hq", A, "their own"), ("hs", B, "their own"),
         ("ldxs", 1 << 24, "2^31"), ("ldhs", 1 << 23, "2^22")])
     bad(L, lib.moe_expert_ffn_up_mxfp4(P(L, T=1 << 24), *UP.values()), "2^31")
+    for f, good in ((lib.moe_expert_ffn_up_mxfp4, {**UP, "ldxs": 32}),
+                    (lib.moe_expert_ffn_down_mxfp4, DOWN)):
+        bad(L, f(P(L, T=1 << 26, K=16, M=4, H=128), *good.values()), "2^23")
     wrong(lib.moe_expert_ffn_down_mxfp4, DOWN, [
         ("hq", None, "h_q is NULL"), ("hs", ODD, "h_q's scales"), ("ldhs", 0, "h_q's scales"),
         ("off", None, "offsets"), ("w", None, "w2_packed"), ("y", None, "y_sorted"),
