@@ -192,7 +192,10 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_gemm(GemmArgs g) {
     }
     __syncthreads();
   };
-  u32x4 fa[2][SM], fb[2][SN];  // operands of the product at hand and of the next
+  // Operands of the product at hand and of the next kAhead: one where a wave has many sub-tiles, whose
+  // products cover the LDS's latency, else as many as reach into the next stage.
+  constexpr int kAhead = SM * SN >= 8 || kParts == 1 ? 1 : 3, kBufs = kAhead + 1;
+  u32x4 fa[kBufs][SM], fb[kBufs][SN];
   u32x4 qa[SM], qb[SN];        // scales of 512 of k, 4 bytes a part
   uint32_t sa[SM], sb[SN];     // of the part at hand: the lane's two
   // operand i (A's, then B's) of product j = 2 s + u of stage st
@@ -222,7 +225,9 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_gemm(GemmArgs g) {
 #pragma unroll
   for (int i = 0; i < kOps; ++i) scale(k0, i);
 #pragma unroll
-  for (int i = 0; i < kOps; ++i) frag(0, 0, 0, i);
+  for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+    for (int i = 0; i < kOps; ++i) frag(0, j, j, i);
   // k1 - k0 stages, 512 of k a turn of the outer loop (k0 a multiple).  A stage's first
   // operands are in registers when its turn comes, and the stage after it is complete in LDS behind
   // its barrier, so that the matrix cores do not run dry at the barriers.
@@ -241,7 +246,8 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_gemm(GemmArgs g) {
       load_scales(kt + NST - 1);
 #pragma unroll
       for (int j = 0; j < kJ; ++j) {
-        const int buf = j & 1, part = t * kParts + (j >> 1);  // of the 512 of k
+        const int part = t * kParts + (j >> 1);  // of the 512 of k
+        const int buf = (t * kJ + j) % kBufs, next = (buf + kAhead) % kBufs;
         if ((j & 1) == 0) {
 #pragma unroll
           for (int i = 0; i < SM; ++i) sa[i] = qa[i][part] >> (16 * h);
@@ -260,8 +266,8 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_gemm(GemmArgs g) {
 #pragma unroll
           for (int i = 0; i < kOps; ++i)
             if (i * kMul / kOps == p) {
-              if (j + 1 < kJ) frag(st, j + 1, buf ^ 1, i);
-              else frag(st1, 0, buf ^ 1, i);
+              if (j + kAhead < kJ) frag(st, j + kAhead, next, i);
+              else frag(st1, j + kAhead - kJ, next, i);
               // the next 512 of k's scales, once this one's last are taken
               if ((j & 1) == 0 && part == 3) scale(kt + 1, i);
             }
@@ -322,9 +328,9 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_gemm(GemmArgs g) {
   else store(std::false_type());
 }
 
-// Few rows: a workgroup takes 16 columns and every row of A, its 8 waves every 8th step of k each,
-// with the codes of kU steps on their way from memory straight into registers, and they add their
-// sums in LDS, in order.  B is read once in all, A once a workgroup (from the L2).  The 16 x 16 x
+// Few tiles: a workgroup of 8 waves takes 16 MG rows x 16 NG columns, its waves every 8th step of
+// 256 of k each, with the codes of kU steps on their way from memory straight into registers, and
+// they add their sums in LDS, in order.  Nothing waits for another wave before the end.  The 16 x 16 x
 // 128 instruction: B the first operand, lane l holds block l / 16 of its row, l % 16, and the
 // result's rows 4 (l / 16) .. +3 of B for row l % 16 of A.
 struct Half {  // a row's 128 of k: the lane's block and its scale
@@ -337,55 +343,71 @@ __device__ __forceinline__ f32x4 mul16(const Half& b, const Half& a, const f32x4
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, 0, (int)b.s, 0, (int)a.s);
 }
 
-template <int MG, int kU>
-__global__ __launch_bounds__(512) void k_mx_gemm_rows(GemmArgs g) {
-  constexpr int kW = 8, kM = 16 * MG;
-  __shared__ float s_sum[kW][kM][17];
+template <int MG, int NG, int kU>
+__global__ __launch_bounds__(512, 1) void k_mx_gemm_rows(GemmArgs g) {
+  constexpr int kW = 8, kM = 16 * MG, kN = 16 * NG;
+  __shared__ float s_sum[kW][kM][kN + 1];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, q = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int64_t n0 = (int64_t)(blockIdx.x / g.mt) * kN, m0 = (int64_t)(blockIdx.x % g.mt) * kM;
   const int nb = (int)((g.K + kMxBlock - 1) / kMxBlock), nk = (nb + 7) / 8;
   const int whole = (int)(g.K / kStep);
   // rows past M or N repeat the last one (their results are not stored)
-  const uint8_t *ap[MG], *sap[MG];
+  uint32_t ao[MG], sao[MG], bo[NG], sbo[NG];  // from the tile's first row on
 #pragma unroll
   for (int m = 0; m < MG; ++m) {
-    const int64_t row = min((int64_t)16 * m + r, g.M - 1);
-    ap[m] = g.a + row * g.lda + 16 * q;
-    sap[m] = g.sa + row * g.ldsa;
+    const uint32_t row = (uint32_t)min((int64_t)16 * m + r, g.M - 1 - m0);
+    ao[m] = row * (uint32_t)g.lda + 16 * q;
+    sao[m] = row * (uint32_t)g.ldsa;
   }
-  const int64_t brow = min(n0 + r, g.N - 1);
-  const uint8_t *bp = g.b + brow * g.ldb + 16 * q, *sbp = g.sb + brow * g.ldsb;
+#pragma unroll
+  for (int n = 0; n < NG; ++n) {
+    const uint32_t row = (uint32_t)min((int64_t)16 * n + r, g.N - 1 - n0);
+    bo[n] = row * (uint32_t)g.ldb + 16 * q;
+    sbo[n] = row * (uint32_t)g.ldsb;
+  }
+  const uint8_t *ap = g.a + m0 * g.lda, *sap = g.sa + m0 * g.ldsa;
+  const uint8_t *bp = g.b + n0 * g.ldb, *sbp = g.sb + n0 * g.ldsb;
   struct Step {
-    Half a[MG][2], b[2];
+    Half a[MG][2], b[NG][2];
   };
-  auto scale = [&](const uint8_t* p, int st, Half (&v)[2]) {
-    const uint2 s = *reinterpret_cast<const uint2*>(p + 8 * st);
+  auto scale = [&](const uint8_t* p, Half (&v)[2]) {
+    const uint2 s = *reinterpret_cast<const uint2*>(p);
     v[0].s = s.x >> (8 * q);
     v[1].s = s.y >> (8 * q);
   };
   auto load = [&](Step& v, int st) {  // a whole step
-    const int64_t k = (int64_t)st * kRow;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      v.b[h].q = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(bp + k + 64 * h));
+    for (int n = 0; n < NG; ++n) {
+      const uint8_t* p = bp + st * kRow + bo[n];
 #pragma unroll
-      for (int m = 0; m < MG; ++m)
-        v.a[m][h].q = *reinterpret_cast<const u32x4*>(ap[m] + k + 64 * h);
+      for (int h = 0; h < 2; ++h)
+        v.b[n][h].q = MG == 1 && NG == 1  // B is read once in all
+                          ? __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p + 64 * h))
+                          : *reinterpret_cast<const u32x4*>(p + 64 * h);
+      scale(sbp + 8 * st + sbo[n], v.b[n]);
     }
-    scale(sbp, st, v.b);
 #pragma unroll
-    for (int m = 0; m < MG; ++m) scale(sap[m], st, v.a[m]);
+    for (int m = 0; m < MG; ++m) {
+      const uint8_t* p = ap + st * kRow + ao[m];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) v.a[m][h].q = *reinterpret_cast<const u32x4*>(p + 64 * h);
+      scale(sap + 8 * st + sao[m], v.a[m]);
+    }
   };
-  f32x4 acc[MG];
+  f32x4 acc[MG][NG];
 #pragma unroll
-  for (int m = 0; m < MG; ++m) acc[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int m = 0; m < MG; ++m)
+#pragma unroll
+    for (int n = 0; n < NG; ++n) acc[m][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   auto add = [&](const Step& v) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int m = 0; m < MG; ++m) acc[m] = mul16(v.b[h], v.a[m][h], acc[m]);
+      for (int m = 0; m < MG; ++m)
+#pragma unroll
+        for (int n = 0; n < NG; ++n) acc[m][n] = mul16(v.b[n][h], v.a[m][h], acc[m][n]);
   };
   Step v[kU];
 #pragma unroll
@@ -400,39 +422,41 @@ __global__ __launch_bounds__(512) void k_mx_gemm_rows(GemmArgs g) {
       if (st + kW * kU < whole) load(v[u], st + kW * kU);
     }
   if (whole < nk && whole % kW == wv) {  // the last, partial step
-    const int64_t k = (int64_t)whole * kRow;
     const u32x4 zero = {0, 0, 0, 0};
+    // this lane's block of half h: zeros past K, and in A the codes past K cleared
+    auto partial = [&](const uint8_t* p, const uint8_t* sp, int h, bool clear, Half& v) {
+      const int b = 8 * whole + 4 * h + q;
+      const bool in = b < nb;
+      v.q = in ? *reinterpret_cast<const u32x4*>(p + whole * kRow + 64 * h) : zero;
+      v.s = in ? sp[b] : 0;
+      const int n = clear ? (int)min((int64_t)kMxBlock, g.K - (int64_t)kMxBlock * b) : kMxBlock;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n < 8 * i + 8) v.q[i] = n > 8 * i ? v.q[i] & ((1u << (4 * (n - 8 * i))) - 1u) : 0u;
+    };
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int b = 8 * whole + 4 * h + q;  // this lane's block: zeros past K
-      const bool in = b < nb;
-      const int n = (int)min((int64_t)kMxBlock, g.K - (int64_t)kMxBlock * b);
-      v[0].b[h].q = in ? *reinterpret_cast<const u32x4*>(bp + k + 64 * h) : zero;
-      v[0].b[h].s = in ? sbp[b] : 0;
 #pragma unroll
-      for (int m = 0; m < MG; ++m) {
-        u32x4 w = in ? *reinterpret_cast<const u32x4*>(ap[m] + k + 64 * h) : zero;
+      for (int n = 0; n < NG; ++n) partial(bp + bo[n], sbp + sbo[n], h, false, v[0].b[n][h]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)  // the codes past K: cleared in A
-          if (n < 8 * i + 8) w[i] = n > 8 * i ? w[i] & ((1u << (4 * (n - 8 * i))) - 1u) : 0u;
-        v[0].a[m][h].q = w;
-        v[0].a[m][h].s = in ? sap[m][b] : 0;
-      }
+      for (int m = 0; m < MG; ++m) partial(ap + ao[m], sap + sao[m], h, true, v[0].a[m][h]);
     }
     add(v[0]);
   }
 #pragma unroll
   for (int m = 0; m < MG; ++m)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s_sum[wv][16 * m + r][4 * q + i] = acc[m][i];
+    for (int n = 0; n < NG; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s_sum[wv][16 * m + r][16 * n + 4 * q + i] = acc[m][n][i];
   __syncthreads();
-  for (int e = tid; e < kM * 16; e += 512) {
-    const int m = e >> 4, n = e & 15;
-    if (m >= g.M || n0 + n >= g.N) continue;
+  for (int e = tid; e < kM * kN; e += 512) {
+    const int m = e / kN, n = e % kN;
+    if (m0 + m >= g.M || n0 + n >= g.N) continue;
     float s = s_sum[0][m][n];
 #pragma unroll
     for (int w = 1; w < kW; ++w) s += s_sum[w][m][n];
-    const int64_t at = m * g.ldc + n0 + n;
+    const int64_t at = (m0 + m) * g.ldc + n0 + n;
     if (g.c_f32) {
       float* p = static_cast<float*>(g.c) + at;
       *p = g.accumulate ? *p + s : s;
@@ -483,38 +507,56 @@ struct Plan {
 int64_t up4(int64_t n) { return (n + 3) / 4 * 4; }
 
 // The form, the tile and the split over k, from the sizes.
+//   Few rows, or few outputs: k_mx_gemm_rows in 16 or 32 rows x 16 columns, or in 32 x 32 where that
+//     is one round of workgroups and no long sum (256 x 1024 x 7168 10.7 us, as tiles of 64 x 64 13.1;
+//     300 x 300 x 300 4.3, 5.5; 33 x 7168 x 2048, two rounds, 9.0, 6.0; 40 x 40 x 16384 23.4, 20.8).
+//   Else the tile, whole or split, that is cheapest by what was measured of each: a step of a round
+//     of 256 workgroups, and for a split 3 us of k_mx_join and its partial sums' way out and in at 4
+//     TB/s.  128 x 4096 x 7168: 64 x 64 12.0 us, 128 x 64 14.5, that in four parts 14.9; 512 x 4096 x
+//     4096: 128 x 64 12.0, 64 x 64 16.4, 128 x 128 13.0; 2048 x 4096 x 4096: 128 x 256 26, 128 x 128 29,
+//     256 x 256 33; 4096 x 4096 x 7168: 256 x 256 66, 128 x 256 80, 128 x 128 84.
 Plan plan(int64_t M, int64_t N, int64_t K) {
   const int64_t nk = (K + kStep - 1) / kStep;
   Plan p;
   p.splits = 1;
   p.steps = (int)nk;
-  if (M <= 32) {  // k_mx_gemm_rows
+  if (M <= 32) {
     p.bm = M <= 16 ? 16 : 32;
     p.bn = 16;
     return p;
   }
-  if (M > 128 && N > 128 && ((M + 255) / 256) * ((N + 255) / 256) >= 192) {
-    p.bm = p.bn = 256;
+  const auto tiles = [&](int64_t bm, int64_t bn) { return (M + bm - 1) / bm * ((N + bn - 1) / bn); };
+  if (tiles(32, 32) <= 256 && nk <= 32) {
+    p.bm = p.bn = 32;
     return p;
   }
-  p.bm = 128;
+  static constexpr struct {
+    int bm, bn;
+    double step_us;
+  } kForms[] = {{64, 64, 0.33}, {128, 64, 0.50}, {128, 128, 0.74}, {128, 256, 1.38}, {256, 256, 1.94}};
   double best = 1e30;
-  for (int bn = 64; bn <= 128; bn += 64) {
-    const double step_us = bn == 64 ? 0.55 : 0.69;
-    const int64_t tiles = ((M + 127) / 128) * ((N + bn - 1) / bn);
-    for (int64_t s = 1; s == 1 || (s * tiles <= 256 && s <= nk / 4); ++s) {
+  for (const auto& f : kForms)
+    for (int64_t s = 1; s == 1 || (s * tiles(f.bm, f.bn) <= 256 && s <= nk / 4); ++s) {
       // a part begins at a multiple of 512 of k
-      const int64_t steps = ((nk + s - 1) / s + 1) / 2 * 2, parts = (nk + steps - 1) / steps;
-      double us = (double)((tiles * parts + 255) / 256 * steps) * step_us;
+      const int64_t steps = s == 1 ? nk : ((nk + s - 1) / s + 1) / 2 * 2;
+      const int64_t parts = (nk + steps - 1) / steps;
+      double us = (double)((tiles(f.bm, f.bn) * parts + 255) / 256 * steps) * f.step_us;
       if (parts > 1) us += 3.0 + 2e-6 * (double)(parts * M * N);
       if (us >= best) continue;
       best = us;
-      p.bn = bn;
+      p.bm = f.bm;
+      p.bn = f.bn;
       p.splits = (int)parts;
       p.steps = (int)steps;
     }
-  }
   return p;
+}
+
+template <int MG, int NG, int kU>
+void launch_rows(GemmArgs g, hipStream_t st) {
+  g.mt = (int)((g.M + 16 * MG - 1) / (16 * MG));
+  const int64_t nt = (g.N + 16 * NG - 1) / (16 * NG);
+  hipLaunchKernelGGL((k_mx_gemm_rows<MG, NG, kU>), dim3((unsigned)(g.mt * nt)), dim3(512), 0, st, g);
 }
 
 template <int BM, int BN, int WM, int WN, int kParts, int NST>
@@ -546,15 +588,18 @@ hipError_t launch_gemm_mxfp4(int64_t M, int64_t N, int64_t K, const uint8_t* a, 
     g.ldc = up4(N);
   }
   if (p.bn == 16) {
-    const dim3 grid((unsigned)((N + 15) / 16));
-    if (p.bm == 16) hipLaunchKernelGGL((k_mx_gemm_rows<1, 4>), grid, dim3(512), 0, st, g);
-    else hipLaunchKernelGGL((k_mx_gemm_rows<2, 4>), grid, dim3(512), 0, st, g);
+    if (p.bm == 16) launch_rows<1, 1, 4>(g, st);
+    else launch_rows<2, 1, 4>(g, st);
+  } else if (p.bn == 32) {
+    launch_rows<2, 2, 4>(g, st);
   } else if (p.bn == 64) {
-    launch_tile<128, 64, 4, 2, 2, 4>(g, st);
+    if (p.bm == 64) launch_tile<64, 64, 2, 2, 2, 6>(g, st);
+    else launch_tile<128, 64, 2, 2, 2, 4>(g, st);
   } else if (p.bn == 128) {
     launch_tile<128, 128, 4, 2, 2, 4>(g, st);
   } else {
-    launch_tile<256, 256, 4, 2, 1, 4>(g, st);
+    if (p.bm == 128) launch_tile<128, 256, 2, 4, 1, 4>(g, st);
+    else launch_tile<256, 256, 4, 2, 1, 4>(g, st);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;

@@ -183,7 +183,8 @@ def product(a, b, M, N, K, out, ldc=None, c0=None):
     (1, 1, 1, 0), (1, 16, 32, 0), (1, 700, 2048, 0), (7, 33, 95, 1), (16, 16, 256, 0),
     (17, 100, 300, 0), (32, 130, 1000, 2), (33, 65, 64, 0), (100, 200, 31, 0), (128, 128, 256, 0),
     (129, 127, 257, 1), (130, 300, 4099, 0), (300, 520, 700, 0), (64, 4096, 512, 0),
-    (1000, 70, 2048, 0), (257, 129, 511, 3), (40, 40, 16384, 0)])
+    (1000, 70, 2048, 0), (257, 129, 511, 3), (40, 40, 16384, 0), (70, 300, 9000, 0),
+    (64, 64, 8448, 0)])
 def test_product(M, N, K, pad, out):
     g = torch.Generator().manual_seed(M * 3 + N * 5 + K)
     a = torch.randn((M, K), generator=g) * 2.0 ** torch.randint(-9, 9, (M, 1), generator=g)
@@ -209,10 +210,11 @@ def test_product_accumulates(M, N, K):
 
 
 @pytest.mark.parametrize("out", ["bf16", "f32"])
-def test_product_large(out):
-    """Tiles of 256 x 256 (at least 192 of them), with ragged edges and a partial last step, against
-    rows of the definition."""
-    M, N, K = 3000, 4200, 608
+@pytest.mark.parametrize("M,N,K", [(130, 2100, 600), (600, 2100, 300), (1200, 2100, 300),
+                                   (2500, 2900, 260), (3000, 4200, 608), (3000, 4200, 999)])
+def test_product_large(M, N, K, out):
+    """Every tile, from 64 x 64 to 256 x 256, with ragged edges and a partial last step, against rows
+    of the definition."""
     g = torch.Generator().manual_seed(1)
     a, b = operand(torch.randn((M, K), generator=g)), operand(torch.randn((N, K), generator=g))
     c = product(a, b, M, N, K, out)
