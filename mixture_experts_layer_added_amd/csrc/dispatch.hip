@@ -6,7 +6,8 @@
 // where its expert is not here.  Ranks come from one 64-bit mask per (wave, expert), a lane's bit a
 // pair, so any index may occur any number of times and no order of atomics shows.
 //   k_sort_small: up to 1024 pairs, one workgroup, one launch.
-//   k_sort_count (1024 pairs a workgroup), k_sort_scan (a workgroup an expert), k_sort_place.
+//   k_sort_count (1024 pairs a workgroup), k_sort_scan (a workgroup an expert; up to 64 workgroups of
+//     pairs sum the counts themselves), k_sort_place.
 // Moving: everything goes by token, one read or write of a token's own row and one of each of its
 // rows among the experts':
 //   k_spread: rows[r] = w t;  with the rows' partner given also dw = <t, partner[r]>
@@ -19,7 +20,8 @@
 namespace moe {
 namespace {
 
-constexpr int kPairs = 1024;  // of a sorting workgroup
+constexpr int kPairs = 1024;    // of a sorting workgroup
+constexpr int kFewBlocks = 64;  // workgroups whose counts each of them can sum up by itself
 constexpr int kMostK = 16, kMostE = 512;
 
 __device__ __forceinline__ int local_expert(const int32_t* __restrict__ idx, int64_t p, int64_t n,
@@ -92,7 +94,9 @@ __global__ __launch_bounds__(kPairs) void k_sort_count(const int32_t* __restrict
   const int64_t p = (int64_t)blockIdx.x * kPairs + threadIdx.x;
   const int r = rank_pairs(local_expert(idx, p, n, first, count), count, mask, s);
   if (p < n) row[p] = r;  // the rank in the workgroup, made a row by k_sort_place
-  for (int i = threadIdx.x; i < count; i += kPairs) blocks[i * nb + blockIdx.x] = s[i];
+  // by expert where k_sort_scan sums them, else by workgroup
+  for (int i = threadIdx.x; i < count; i += kPairs)
+    blocks[nb > kFewBlocks ? i * nb + blockIdx.x : (int64_t)blockIdx.x * count + i] = s[i];
 }
 
 // an expert's counts [nb] become the sums of those before, its total goes to totals
@@ -128,9 +132,23 @@ __global__ __launch_bounds__(kPairs) void k_sort_place(const int32_t* __restrict
                                                        int32_t* __restrict__ offsets,
                                                        int32_t* __restrict__ token,
                                                        int32_t* __restrict__ row) {
-  __shared__ int s[kMostE];
+  __shared__ int s[kMostE], s_before[kMostE];
   const int tid = threadIdx.x;
-  if (tid < kMostE) s[tid] = tid < count ? totals[tid] : 0;
+  if (nb > kFewBlocks) {
+    if (tid < kMostE) s[tid] = tid < count ? totals[tid] : 0;
+  } else if (tid < kMostE) {  // a thread an expert: its total, and what lies before this workgroup
+    int sum = 0, before = 0;
+    if (tid < count) {
+#pragma unroll 8
+      for (int b = 0; b < (int)nb; ++b) {
+        const int v = blocks[b * count + tid];
+        sum += v;
+        if (b < (int)blockIdx.x) before += v;
+      }
+    }
+    s[tid] = sum;
+    s_before[tid] = before;
+  }
   __syncthreads();
   scan_experts(s);
   if (blockIdx.x == 0) {
@@ -140,7 +158,8 @@ __global__ __launch_bounds__(kPairs) void k_sort_place(const int32_t* __restrict
   const int64_t p = (int64_t)blockIdx.x * kPairs + tid;
   const int e = local_expert(idx, p, n, first, count);
   if (e < 0) return;
-  const int at = (e ? s[e - 1] : 0) + blocks[e * nb + blockIdx.x] + row[p];
+  const int before = nb > kFewBlocks ? blocks[e * nb + blockIdx.x] : s_before[e];
+  const int at = (e ? s[e - 1] : 0) + before + row[p];
   row[p] = at;
   token[at] = (int)(p / K);
 }
@@ -150,35 +169,30 @@ __global__ void k_no_pairs(int32_t* __restrict__ offsets, int count) {
 }
 
 // ---- moving rows ----
-template <typename T>
-struct Chunk {
-  static constexpr int N = 16 / sizeof(T);
-  float v[N];
-};
-// the chunk at p, n of its elements there (zeros behind)
+// 16 bytes of a row as they lie in memory, n elements of them there (zeros behind)
 template <bool kVec>
-__device__ __forceinline__ void get(const uint16_t* __restrict__ p, int n, Chunk<uint16_t>& c) {
-  if (kVec && n >= 8) {
-    const u32x4 u = *reinterpret_cast<const u32x4*>(p);
+__device__ __forceinline__ u32x4 get(const uint16_t* __restrict__ p, int n) {
+  u32x4 u = {0, 0, 0, 0};
+  if (kVec && n >= 8) return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      c.v[2 * i] = __uint_as_float(u[i] << 16);
-      c.v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) c.v[i] = i < n ? bf16_bits_to_f32(p[i]) : 0.0f;
-  }
+  for (int i = 0; i < 8; ++i)
+    if (i < n) u[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+  return u;
 }
 template <bool kVec>
-__device__ __forceinline__ void get(const float* __restrict__ p, int n, Chunk<float>& c) {
-  if (kVec && n >= 4) {
-    const float4 u = *reinterpret_cast<const float4*>(p);
-    c.v[0] = u.x; c.v[1] = u.y; c.v[2] = u.z; c.v[3] = u.w;
-  } else {
+__device__ __forceinline__ u32x4 get(const float* __restrict__ p, int n) {
+  u32x4 u = {0, 0, 0, 0};
+  if (kVec && n >= 4) return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c.v[i] = i < n ? p[i] : 0.0f;
-  }
+  for (int i = 0; i < 4; ++i)
+    if (i < n) u[i] = __float_as_uint(p[i]);
+  return u;
+}
+__device__ __forceinline__ float value(const u32x4& u, int i, const uint16_t*) {
+  return __uint_as_float(i & 1 ? u[i >> 1] & 0xFFFF0000u : u[i >> 1] << 16);
+}
+__device__ __forceinline__ float value(const u32x4& u, int i, const float*) {
+  return __uint_as_float(u[i]);
 }
 // bf16 bits of a number to nearest even; NaN stays one
 __device__ __forceinline__ uint32_t to_bf16(float f) {
@@ -186,13 +200,12 @@ __device__ __forceinline__ uint32_t to_bf16(float f) {
   return f != f ? (u >> 16 | 0x40u) : (uint32_t)f32_to_bf16_bits(f);
 }
 template <bool kVec>
-__device__ __forceinline__ void put(uint16_t* __restrict__ p, int n, const Chunk<uint16_t>& c) {
-  uint32_t w[4];
+__device__ __forceinline__ void put(uint16_t* __restrict__ p, int n, const float* v) {
+  u32x4 w;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = to_bf16(c.v[2 * i]) | to_bf16(c.v[2 * i + 1]) << 16;
+  for (int i = 0; i < 4; ++i) w[i] = to_bf16(v[2 * i]) | to_bf16(v[2 * i + 1]) << 16;
   if (kVec && n >= 8) {
-    const u32x4 u = {w[0], w[1], w[2], w[3]};
-    __builtin_nontemporal_store(u, reinterpret_cast<u32x4*>(p));
+    __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(p));
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -200,15 +213,15 @@ __device__ __forceinline__ void put(uint16_t* __restrict__ p, int n, const Chunk
   }
 }
 template <bool kVec>
-__device__ __forceinline__ void put(float* __restrict__ p, int n, const Chunk<float>& c) {
+__device__ __forceinline__ void put(float* __restrict__ p, int n, const float* v) {
   if (kVec && n >= 4) {
-    const u32x4 u = {__float_as_uint(c.v[0]), __float_as_uint(c.v[1]), __float_as_uint(c.v[2]),
-                     __float_as_uint(c.v[3])};
+    const u32x4 u = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                     __float_as_uint(v[3])};
     __builtin_nontemporal_store(u, reinterpret_cast<u32x4*>(p));
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (i < n) p[i] = c.v[i];
+      if (i < n) p[i] = v[i];
   }
 }
 
@@ -223,85 +236,87 @@ struct MoveArgs {
   int64_t ld_tok, ld_rows, ld_partner, ld_out;
 };
 
-// dots of the workgroup's 256 threads, one a choice, to dw of token t (0 where there is no row)
+constexpr int kMove = 128;  // threads: 16 bytes each, 1024 bf16 elements a turn
+
+// dots of the workgroup's threads, one a choice, to dw of a token (0 where there is no row)
+template <int kK>
 __device__ __forceinline__ void write_dots(const float* dot, const int* rows, int K, float* dw) {
-  __shared__ float red[4][kMostK];
+  __shared__ float red[2][kK];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
 #pragma unroll
-  for (int k = 0; k < kMostK; ++k) {
+  for (int k = 0; k < kK; ++k) {
     if (k < K) {
       float v = dot[k];
 #pragma unroll
       for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
-      if (lane == 0) red[wv][k] = v;
+      if (lane == 0) red[wv][k] = rows[k] < 0 ? 0.0f : v;
     }
   }
   __syncthreads();
-  if (tid < K)
-    dw[tid] = rows[tid] < 0 ? 0.0f : (red[0][tid] + red[1][tid]) + (red[2][tid] + red[3][tid]);
+  if (tid < K) dw[tid] = red[0][tid] + red[1][tid];
   __syncthreads();
 }
 
 // kSpread: out = rows, tok the tokens' rows, partner (kDot) the experts' rows of the dots.
 // Else (gather): out = the tokens' rows, rows the experts', partner (kDot) the tokens' of the dots.
-// With dots a workgroup takes a token, else a token's slice of 256 chunks of 16 bytes.
-template <typename T, bool kVec, bool kSpread, bool kDot>
-__global__ __launch_bounds__(256) void k_move(MoveArgs g) {
-  constexpr int N = Chunk<T>::N;
-  const int64_t slices = kDot ? 1 : (g.H + 256 * N - 1) / (256 * N);
+// With dots a workgroup takes a token, else a token's slice of kMove chunks of 16 bytes, the slices of
+// a token next to each other, so that its rows' pieces are read together.  All rows' loads of a turn
+// are on their way before the first is used.  kK >= K choices.
+template <typename T, int kK, bool kVec, bool kSpread, bool kDot>
+__global__ __launch_bounds__(kMove) void k_move(MoveArgs g) {
+  constexpr int N = 16 / sizeof(T);
+  const T* type = nullptr;
+  const int64_t slices = kDot ? 1 : (g.H + kMove * N - 1) / (kMove * N);
   const int64_t work = g.T * slices;
   for (int64_t b = blockIdx.x; b < work; b += gridDim.x) {
     const int64_t t = b / slices;
-    int row[kMostK];
-    float w[kMostK], dot[kMostK];
+    int row[kK];
+    float w[kK], dot[kK];
 #pragma unroll
-    for (int k = 0; k < kMostK; ++k) {
+    for (int k = 0; k < kK; ++k) {
       row[k] = k < g.K ? g.row[t * g.K + k] : -1;
       w[k] = k < g.K && g.w ? g.w[t * g.K + k] : 1.0f;
       dot[k] = 0.0f;
     }
-    const int64_t c0 = kDot ? 0 : (b - t * slices) * 256 * N;
-    const int64_t c1 = kDot ? g.H : min(g.H, c0 + 256 * N);
-    for (int64_t c = c0 + threadIdx.x * N; c < c1; c += 256 * N) {
+    const int64_t c0 = kDot ? 0 : (b - t * slices) * kMove * N;
+    const int64_t c1 = kDot ? g.H : min(g.H, c0 + kMove * N);
+    for (int64_t c = c0 + threadIdx.x * N; c < c1; c += kMove * N) {
       const int n = (int)min((int64_t)N, g.H - c);
-      if constexpr (kSpread) {
-        Chunk<T> x;
-        get<kVec>(static_cast<const T*>(g.tok) + t * g.ld_tok + c, n, x);
+      u32x4 u[kK], x = {0, 0, 0, 0};
+      if constexpr (kSpread) x = get<kVec>(static_cast<const T*>(g.tok) + t * g.ld_tok + c, n);
+      else if constexpr (kDot)
+        x = get<kVec>(static_cast<const T*>(g.partner) + t * g.ld_partner + c, n);
+      if constexpr (kDot || !kSpread) {
+        const T* p = static_cast<const T*>(kSpread ? g.partner : g.rows) + c;
+        const int64_t ld = kSpread ? g.ld_partner : g.ld_rows;
 #pragma unroll
-        for (int k = 0; k < kMostK; ++k) {
-          if (row[k] < 0) continue;
-          Chunk<T> o;
-          if constexpr (kDot) {
-            Chunk<T> p;
-            get<kVec>(static_cast<const T*>(g.partner) + row[k] * g.ld_partner + c, n, p);
-#pragma unroll
-            for (int i = 0; i < N; ++i) dot[k] = __builtin_fmaf(x.v[i], p.v[i], dot[k]);
-          }
-#pragma unroll
-          for (int i = 0; i < N; ++i) o.v[i] = w[k] * x.v[i];
-          put<kVec>(static_cast<T*>(g.out) + row[k] * g.ld_out + c, n, o);
-        }
-      } else {
-        Chunk<T> s, x;
-#pragma unroll
-        for (int i = 0; i < N; ++i) s.v[i] = 0.0f;
-        if constexpr (kDot)
-          get<kVec>(static_cast<const T*>(g.partner) + t * g.ld_partner + c, n, x);
-#pragma unroll
-        for (int k = 0; k < kMostK; ++k) {
-          if (row[k] < 0) continue;
-          Chunk<T> p;
-          get<kVec>(static_cast<const T*>(g.rows) + row[k] * g.ld_rows + c, n, p);
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            s.v[i] = __builtin_fmaf(w[k], p.v[i], s.v[i]);
-            if constexpr (kDot) dot[k] = __builtin_fmaf(x.v[i], p.v[i], dot[k]);
-          }
-        }
-        put<kVec>(static_cast<T*>(g.out) + t * g.ld_out + c, n, s);
+        for (int k = 0; k < kK; ++k)
+          if (row[k] >= 0) u[k] = get<kVec>(p + row[k] * ld, n);
       }
+      float s[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) s[i] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kK; ++k) {
+        if (row[k] < 0) continue;
+        if constexpr (kDot) {
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            dot[k] = __builtin_fmaf(value(x, i, type), value(u[k], i, type), dot[k]);
+        }
+        if constexpr (kSpread) {
+          float o[N];
+#pragma unroll
+          for (int i = 0; i < N; ++i) o[i] = w[k] * value(x, i, type);
+          put<kVec>(static_cast<T*>(g.out) + row[k] * g.ld_out + c, n, o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < N; ++i) s[i] = __builtin_fmaf(w[k], value(u[k], i, type), s[i]);
+        }
+      }
+      if constexpr (!kSpread) put<kVec>(static_cast<T*>(g.out) + t * g.ld_out + c, n, s);
     }
-    if constexpr (kDot) write_dots(dot, row, g.K, g.dw + t * g.K);
+    if constexpr (kDot) write_dots<kK>(dot, row, g.K, g.dw + t * g.K);
   }
 }
 
@@ -309,18 +324,22 @@ bool whole16(const void* p, int64_t ld, size_t es) {
   return !p || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld * es % 16 == 0);
 }
 
-template <typename T, bool kSpread>
+template <typename T, int kK, bool kSpread>
 hipError_t move(const MoveArgs& g, hipStream_t st) {
   const bool vec = whole16(g.tok, g.ld_tok, sizeof(T)) && whole16(g.rows, g.ld_rows, sizeof(T)) &&
                    whole16(g.partner, g.ld_partner, sizeof(T)) &&
                    whole16(g.out, g.ld_out, sizeof(T));
-  const int64_t per = 256 * Chunk<T>::N;
+  const int64_t per = kMove * (16 / sizeof(T));
   const int64_t work = g.T * (g.dw ? 1 : (g.H + per - 1) / per);
   const dim3 grid((unsigned)std::min<int64_t>(work, 1 << 20));
-  auto k = g.dw ? (vec ? k_move<T, true, kSpread, true> : k_move<T, false, kSpread, true>)
-                : (vec ? k_move<T, true, kSpread, false> : k_move<T, false, kSpread, false>);
-  hipLaunchKernelGGL(k, grid, dim3(256), 0, st, g);
+  auto k = g.dw ? (vec ? k_move<T, kK, true, kSpread, true> : k_move<T, kK, false, kSpread, true>)
+                : (vec ? k_move<T, kK, true, kSpread, false> : k_move<T, kK, false, kSpread, false>);
+  hipLaunchKernelGGL(k, grid, dim3(kMove), 0, st, g);
   return hipGetLastError();
+}
+template <typename T, bool kSpread>
+hipError_t move(const MoveArgs& g, hipStream_t st) {
+  return g.K <= 8 ? move<T, 8, kSpread>(g, st) : move<T, kMostK, kSpread>(g, st);
 }
 
 }  // namespace
@@ -348,9 +367,11 @@ hipError_t launch_sort_by_expert(int64_t n, int K, const int32_t* idx, int first
                      nb, blocks, row);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(k_sort_scan, dim3(count), dim3(256), 0, st, blocks, nb, totals);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  if (nb > kFewBlocks) {
+    hipLaunchKernelGGL(k_sort_scan, dim3(count), dim3(256), 0, st, blocks, nb, totals);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   hipLaunchKernelGGL(k_sort_place, dim3((unsigned)nb), dim3(kPairs), 0, st, idx, n, K, first, count,
                      nb, blocks, totals, offsets, token, row);
   return hipGetLastError();

@@ -40,15 +40,26 @@ __device__ __forceinline__ uint32_t mx_pack8(const float* v, float s) {
   return mx_pack2<3>(w, v[6], v[7], s);
 }
 
-// Code of v, inv = 1/scale, rounded to one of its two neighbours by a random byte r: up where the
-// fraction between them, in 256ths, passes r + 1/2, so that the mean over all r is v within 1/512
+// Code of v under scale code sc, rounded to one of its two neighbours by a random byte r: up where
+// the fraction between them, in 256ths, passes r + 1/2, so that the mean over all r is v within 1/512
 // of a step.
-__device__ __forceinline__ uint32_t mx_code_random(float v, float inv, uint32_t r) {
-  const float a = __builtin_fabsf(v) * inv;
+// v was fp32: the fraction is formed and compared.
+__device__ __forceinline__ uint32_t mx_code_random(float v, uint32_t sc, uint32_t r, const float*) {
+  const float a = __builtin_fabsf(v) * mx_scale(254 - sc);
   const bool b2 = a >= 2.0f, b4 = a >= 4.0f;
   const float f = a * (b4 ? 0.5f : b2 ? 1.0f : 2.0f), low = __builtin_floorf(f);
   const uint32_t m = (uint32_t)low + ((f - low) * 256.0f > (float)r + 0.5f);
   return (m + (b4 ? 4u : b2 ? 2u : 0u)) | (__float_as_uint(v) >> 31 << 3);
+}
+// v was bf16: |v| 2^-126 over the scale has the code in its bits 24 .. 22 (the codes below 1 lie among
+// fp32's denormals) and the fraction below them, exactly: of v's 8 bits none falls off but from
+// values that no byte rounds up.  With 2^22 (1 - (r + 1/2)/256) - 1 added the code is the upper one where
+// the fraction is larger.  8 operations in place of 16.  r is given as 255 - r.
+__device__ __forceinline__ uint32_t mx_code_random(float v, uint32_t sc, uint32_t r,
+                                                   const uint16_t*) {
+  const uint32_t a = __float_as_uint(__builtin_amdgcn_ldexpf(__builtin_fabsf(v), 1 - (int)sc));
+  const uint32_t w = (r << 14) + a + 8191u;
+  return (w >> 22) | (__float_as_uint(v) >> 31 << 3);
 }
 
 // D += B A over one block of 64 of k: 32 x 32 outputs, lane l holds 32 codes (16 bytes) of row

@@ -46,15 +46,21 @@ __device__ __forceinline__ void read8(const float* __restrict__ p, int n, float*
     for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : 0.0f;
   }
 }
-// 8 random bytes, the first n of them there
+// 8 random bytes, the first n of them there, as mx_code_random takes them
+template <typename T>
 __device__ __forceinline__ uint2 read8r(const uint8_t* __restrict__ p, int n) {
-  if (n >= 8 && (reinterpret_cast<uintptr_t>(p) & 7) == 0)
-    return *reinterpret_cast<const uint2*>(p);
+  constexpr uint32_t kFlip = sizeof(T) == 2 ? 0xffffffffu : 0u;
   uint32_t w[2] = {0, 0};
+  if (n >= 8 && (reinterpret_cast<uintptr_t>(p) & 7) == 0) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    w[0] = u.x;
+    w[1] = u.y;
+  } else {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < n) w[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
-  return make_uint2(w[0], w[1]);
+    for (int i = 0; i < 8; ++i)
+      if (i < n) w[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
+  }
+  return make_uint2(w[0] ^ kFlip, w[1] ^ kFlip);
 }
 
 __device__ __forceinline__ uint32_t max8(const float* v) {
@@ -65,15 +71,16 @@ __device__ __forceinline__ uint32_t max8(const float* v) {
 }
 
 // 8 codes of one block, whose scale code is sc
-template <bool kRandom>
+template <typename T, bool kRandom>
 __device__ __forceinline__ uint32_t codes8(const float* v, uint32_t sc, uint2 r) {
   if (sc == 255) return 0;
   if (!kRandom) return mx_pack8(v, mx_scale(sc));
-  const float inv = mx_scale(254 - sc);
   uint32_t w = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    w |= mx_code_random(v[i], inv, ((i < 4 ? r.x : r.y) >> (8 * (i & 3))) & 255u) << (4 * i);
+    w |= mx_code_random(v[i], sc, ((i < 4 ? r.x : r.y) >> (8 * (i & 3))) & 255u,
+                        static_cast<const T*>(nullptr))
+         << (4 * i);
   return w;
 }
 
@@ -93,12 +100,12 @@ __global__ __launch_bounds__(256) void k_mx_rows(const T* __restrict__ x, int64_
     float v[8];
     read8<kVec>(x + r * ldx + c, n, v);
     uint2 rb = make_uint2(0, 0);
-    if (kRandom) rb = read8r(rnd + r * cols + c, n);
+    if (kRandom) rb = read8r<T>(rnd + r * cols + c, n);
     uint32_t m = max8(v);
     m = max(m, (uint32_t)__shfl_xor((int)m, 1));
     m = max(m, (uint32_t)__shfl_xor((int)m, 2));
     const uint32_t sc = mx_scale_code<kRandom>(m);
-    *reinterpret_cast<uint32_t*>(q + r * ldq + 16 * b + 4 * l) = codes8<kRandom>(v, sc, rb);
+    *reinterpret_cast<uint32_t*>(q + r * ldq + 16 * b + 4 * l) = codes8<T, kRandom>(v, sc, rb);
     if (l == 0) scale[r * lds + b] = (uint8_t)sc;
   }
 }
@@ -158,7 +165,7 @@ __global__ __launch_bounds__(256) void k_mx_tile(const T* __restrict__ x, int64_
       const int nr = r < rows ? n : 0;
       read8<kVec>(x + r * ldx + c0 + 8 * l, nr, v[i]);
       rr[i] = make_uint2(0, 0);
-      if (kRandom) rr[i] = read8r(rnd + r * cols + c0 + 8 * l, nr);
+      if (kRandom) rr[i] = read8r<T>(rnd + r * cols + c0 + 8 * l, nr);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -174,7 +181,7 @@ __global__ __launch_bounds__(256) void k_mx_tile(const T* __restrict__ x, int64_
       if (r < rows && c < cols) {
         const uint32_t sc = mx_scale_code<kRandom>(m);
         *reinterpret_cast<uint32_t*>(q + r * ldq + (c0 + 8 * l) / 2) =
-            codes8<kRandom>(v[i], sc, rr[i]);
+            codes8<T, kRandom>(v[i], sc, rr[i]);
         if ((l & 3) == 0) scale[r * lds + c / kMxBlock] = (uint8_t)sc;
       }
     }
@@ -192,7 +199,8 @@ __global__ __launch_bounds__(256) void k_mx_tile(const T* __restrict__ x, int64_
   const uint32_t sc[2] = {mx_scale_code<kRandom>(m0), mx_scale_code<kRandom>(m1)};
   uint32_t w[2][4];
   if (kRandom) {
-    const float i0 = mx_scale(254 - min(sc[0], 254u)), i1 = mx_scale(254 - min(sc[1], 254u));
+    const uint32_t s0 = min(sc[0], 254u), s1 = min(sc[1], 254u);
+    const T* type = nullptr;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       w[0][j] = w[1][j] = 0;
@@ -201,8 +209,8 @@ __global__ __launch_bounds__(256) void k_mx_tile(const T* __restrict__ x, int64_
         const int k = 8 * j + i;
         const uint32_t r =
             *reinterpret_cast<const uint16_t*>(s_r + (32 * wv + k) * kTile + 2 * lane);
-        w[0][j] |= mx_code_random(P::lo(v[k]), i0, r & 255u) << (4 * i);
-        w[1][j] |= mx_code_random(P::hi(v[k]), i1, r >> 8) << (4 * i);
+        w[0][j] |= mx_code_random(P::lo(v[k]), s0, r & 255u, type) << (4 * i);
+        w[1][j] |= mx_code_random(P::hi(v[k]), s1, r >> 8, type) << (4 * i);
       }
     }
   } else {
@@ -245,54 +253,65 @@ __global__ __launch_bounds__(256) void k_mx_tile(const T* __restrict__ x, int64_
 }
 
 // values of 8 codes: exact in bf16 too (two significant bits, at least 2^-128), NaN for scale 255
-__device__ __forceinline__ void put8(uint16_t* __restrict__ p, const float* v, int n) {
+__device__ __forceinline__ void put8(uint16_t* __restrict__ p, const float* v) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     w[i] = __float_as_uint(v[2 * i]) >> 16 | (__float_as_uint(v[2 * i + 1]) & 0xFFFF0000u);
-  if (n >= 8 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) p[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
-  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ void put8(float* __restrict__ p, const float* v, int n) {
-  if (n >= 8 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) p[i] = v[i];
-  }
+__device__ __forceinline__ void put8(float* __restrict__ p, const float* v) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
 }
+__device__ __forceinline__ void put1(uint16_t* __restrict__ p, float v) {
+  *p = (uint16_t)(__float_as_uint(v) >> 16);
+}
+__device__ __forceinline__ void put1(float* __restrict__ p, float v) { *p = v; }
 
-template <typename T>
+// A lane takes 8 outputs that begin at a multiple of 16 bytes in memory.  kShift: wherever the row
+// begins, so that up to 7 of the first ones lie before it; a lane's codes are then 8 of the 16 around
+// them, and may lie in two blocks.
+template <typename T, bool kShift>
 __global__ __launch_bounds__(256) void k_mx_values(int64_t rows, int64_t cols,
                                                    const uint8_t* __restrict__ q, int64_t ldq,
                                                    const uint8_t* __restrict__ scale, int64_t lds,
                                                    T* __restrict__ out, int64_t ldo) {
-  const int64_t per = (cols + 7) / 8, total = rows * per, stride = (int64_t)gridDim.x * 256;
+  constexpr int kEl = kShift ? 16 / sizeof(T) : 1;  // elements in 16 bytes
+  const int64_t per = (cols + 7 + kEl - 1) / 8, total = rows * per;
+  const int64_t stride = (int64_t)gridDim.x * 256;
   for (int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x; g < total; g += stride) {
     const int64_t r = (uint64_t)total >> 32 ? g / per : (int64_t)((uint32_t)g / (uint32_t)per);
-    const int64_t c = (g - r * per) * 8;
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(q + r * ldq + c / 2);
-    const uint32_t sc = scale[r * lds + c / kMxBlock];
-    const float s = sc == 255 ? __uint_as_float(0x7fc00000u) : mx_scale(sc);
+    T* row = out + r * ldo;
+    const int before = kShift ? (int)(reinterpret_cast<uintptr_t>(row) / sizeof(T) % kEl) : 0;
+    const int64_t c = (g - r * per) * 8 - before;  // the first of the 8, from -(kEl - 1) on
+    if (c >= cols) continue;
+    const int64_t last = (cols + kMxBlock - 1) / kMxBlock * 4 - 1;  // dword of codes
+    const int64_t d = c >> 3;  // rounds down: -1 for what lies before the row
+    const uint32_t* qr = reinterpret_cast<const uint32_t*>(q + r * ldq);
+    const uint32_t lo = qr[max(d, (int64_t)0)], hi = before ? qr[min(d + 1, last)] : 0u;
+    const uint32_t w = before ? (uint32_t)(((uint64_t)hi << 32 | lo) >> (4 * (int)(c & 7))) : lo;
+    const int64_t c0 = max(c, (int64_t)0), c1 = min(c + 7, cols - 1);
+    const uint8_t* sr = scale + r * lds;
+    const uint32_t sc0 = sr[c0 / kMxBlock], sc1 = before ? sr[c1 / kMxBlock] : sc0;
+    const float s0 = sc0 == 255 ? __uint_as_float(0x7fc00000u) : mx_scale(sc0);
+    const float s1 = sc1 == 255 ? __uint_as_float(0x7fc00000u) : mx_scale(sc1);
+    const int turn = before ? kMxBlock - (int)(c & (kMxBlock - 1)) : 8;  // codes of the first block
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    const f32x2 p[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0),
+                        __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1),
+                        __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2),
+                        __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3)};
     float v[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      typedef float f32x2 __attribute__((ext_vector_type(2)));
-      const f32x2 p = i == 0   ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0)
-                      : i == 1 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1)
-                      : i == 2 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2)
-                               : __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
-      v[2 * i] = p.x * s;
-      v[2 * i + 1] = p.y * s;
+    for (int i = 0; i < 8; ++i) v[i] = (i & 1 ? p[i >> 1].y : p[i >> 1].x) * (i < turn ? s0 : s1);
+    if (c >= 0 && c + 8 <= cols) {
+      put8(row + c, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c + i >= 0 && c + i < cols) put1(row + c + i, v[i]);
     }
-    put8(out + r * ldo + c, v, (int)min((int64_t)8, cols - c));
   }
 }
 
@@ -338,14 +357,21 @@ hipError_t launch_quantize_mxfp4(const void* x, int dtype, int64_t rows, int64_t
 hipError_t launch_dequantize_mxfp4(int64_t rows, int64_t cols, const uint8_t* q, int64_t ldq,
                                    const uint8_t* scale, int64_t lds, void* out, int64_t ldo,
                                    int dtype, hipStream_t st) {
-  const int64_t n = rows * ((cols + 7) / 8);
+  const int64_t n = rows * ((cols + 14) / 8);
   const dim3 g((unsigned)std::min<int64_t>((n + 255) / 256, 1 << 20));
-  if (dtype == MOE_BF16)
-    hipLaunchKernelGGL(k_mx_values<uint16_t>, g, dim3(256), 0, st, rows, cols, q, ldq, scale, lds,
-                       static_cast<uint16_t*>(out), ldo);
-  else
-    hipLaunchKernelGGL(k_mx_values<float>, g, dim3(256), 0, st, rows, cols, q, ldq, scale, lds,
-                       static_cast<float*>(out), ldo);
+  const int es = dtype == MOE_BF16 ? 2 : 4;
+  const bool shift = (reinterpret_cast<uintptr_t>(out) & 15) != 0 || ldo * es % 16 != 0;
+#define MX_VALUES(T, S)                                                                          \
+  hipLaunchKernelGGL((k_mx_values<T, S>), g, dim3(256), 0, st, rows, cols, q, ldq, scale, lds, \
+                     static_cast<T*>(out), ldo)
+  if (dtype == MOE_BF16) {
+    if (shift) MX_VALUES(uint16_t, true);
+    else MX_VALUES(uint16_t, false);
+  } else {
+    if (shift) MX_VALUES(float, true);
+    else MX_VALUES(float, false);
+  }
+#undef MX_VALUES
   return hipGetLastError();
 }
 
