@@ -85,6 +85,13 @@ moe_status validate(const moe_problem* p, Dims* d) {
   return MOE_OK;
 }
 
+// the calls that have kernels of their own for this type (moe_..._mxfp4)
+moe_status refuse_mxfp4(const Dims& d, const char* call) {
+  if (d.expert == MOE_MXFP4)
+    return fail(MOE_ERR_UNSUPPORTED, "%s is not built for MXFP4 experts", call);
+  return MOE_OK;
+}
+
 size_t route_ws_bytes(const Dims& d) { return sizeof(float) * (size_t)d.T * d.E; }
 
 #define REQUIRE_PTR(ptr)                                                   \
@@ -238,6 +245,7 @@ moe_status moe_expert_ffn_up(const moe_problem* p, const void* x_sorted,
   Dims d;
   moe_status s = validate(p, &d);
   if (s != MOE_OK) return s;
+  if ((s = refuse_mxfp4(d, "moe_expert_ffn_up")) != MOE_OK) return s;
   REQUIRE_PTR(x_sorted);
   REQUIRE_PTR(w13);
   REQUIRE_PTR(h);
@@ -259,6 +267,7 @@ moe_status moe_expert_ffn_up_gather(const moe_problem* p, const void* x, const f
   Dims d;
   moe_status s = validate(p, &d);
   if (s != MOE_OK) return s;
+  if ((s = refuse_mxfp4(d, "moe_expert_ffn_up_gather")) != MOE_OK) return s;
   REQUIRE_PTR(x);
   REQUIRE_PTR(w13);
   REQUIRE_PTR(h);
@@ -299,6 +308,7 @@ moe_status moe_expert_ffn_down(const moe_problem* p, const void* h, const float*
   Dims d;
   moe_status s = validate(p, &d);
   if (s != MOE_OK) return s;
+  if ((s = refuse_mxfp4(d, "moe_expert_ffn_down")) != MOE_OK) return s;
   REQUIRE_PTR(h);
   REQUIRE_PTR(w2);
   REQUIRE_PTR(y_sorted);
@@ -321,8 +331,7 @@ moe_status moe_expert_ffn(const moe_problem* p, const void* x_sorted,
   Dims d;
   moe_status s = validate(p, &d);
   if (s != MOE_OK) return s;
-  if (d.expert == MOE_MXFP4)
-    return fail(MOE_ERR_UNSUPPORTED, "moe_expert_ffn is not built for MXFP4 experts");
+  if ((s = refuse_mxfp4(d, "moe_expert_ffn")) != MOE_OK) return s;
   REQUIRE_PTR(x_sorted);
   REQUIRE_PTR(w13);
   REQUIRE_PTR(w2);

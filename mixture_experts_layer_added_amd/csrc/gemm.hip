@@ -423,6 +423,7 @@ hipError_t launch_ffn_up(const Dims& d, const void* xs, const float* xs_scale,
                        (int)d.T, ng, d.H, 2 * d.I, d.I, d.I);
     return hipGetLastError();
   }
+  if (d.expert != MOE_FP8_E4M3) return hipErrorNotSupported;
   return launch_fp8_up(d, xs, xs_scale, offsets, gather, w13, w13_scale, h, h_scale, st);
 }
 
@@ -444,6 +445,7 @@ hipError_t launch_ffn_down(const Dims& d, const void* h, const float* h_scale,
                        0);
     return hipGetLastError();
   }
+  if (d.expert != MOE_FP8_E4M3) return hipErrorNotSupported;
   return launch_fp8_down(d, h, h_scale, offsets, w2, w2_scale, ys, st);
 }
 

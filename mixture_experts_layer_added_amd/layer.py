@@ -11,7 +11,7 @@ import torch
 
 from . import _lib as L
 
-_DT = {"f32": L.MOE_F32, "bf16": L.MOE_BF16, "e4m3": L.MOE_FP8_E4M3}
+_DT = {"f32": L.MOE_F32, "bf16": L.MOE_BF16, "e4m3": L.MOE_FP8_E4M3, "mxfp4": L.MOE_MXFP4}
 
 
 @dataclass
@@ -124,6 +124,218 @@ class Fp8Linear:
         self.dw.zero_()
 
 
+def _dtype(t):
+    assert t.dtype in (torch.bfloat16, torch.float32)
+    return L.MOE_F32 if t.dtype == torch.float32 else L.MOE_BF16
+
+
+def _mx_buffers(rows, cols, device):
+    """Codes and scales of an MXFP4 matrix with the smallest row strides that the calls take."""
+    kb = -(-cols // 32)
+    return (torch.empty((rows, 16 * kb), dtype=torch.uint8, device=device),
+            torch.empty((rows, -(-kb // 16) * 16), dtype=torch.uint8, device=device))
+
+
+def quantize_mxfp4(x: torch.Tensor, rows=True, cols=False, random=None):
+    """fp32 or bf16 [n, m] (rows may be strided) -> MXFP4 codes (uint8, 16 a block of 32) and E8M0
+    scales (uint8, rows padded to 16): (q, scale) along the rows, (qt, scale_t) of the transpose;
+    None for a form not asked for.  random: uint8 [n, m], for stochastic rounding.  On the current
+    stream."""
+    assert x.dim() == 2 and x.stride(1) == 1 and x.stride(0) >= x.shape[1]
+    n, m = x.shape
+    assert random is None or (random.dtype == torch.uint8 and random.shape == x.shape)
+    q, scale = _mx_buffers(n, m, x.device) if rows else (None, None)
+    qt, scale_t = _mx_buffers(m, n, x.device) if cols else (None, None)
+    L._ptrs("moe_quantize_mxfp4", x.as_strided((1,), (1,)))  # its device; its rows may be strided
+    L.moe_quantize_mxfp4(x.data_ptr(), _dtype(x), n, m, x.stride(0), q, q.shape[1] if rows else 0,
+                         scale, scale.shape[1] if rows else 0, qt, qt.shape[1] if cols else 0,
+                         scale_t, scale_t.shape[1] if cols else 0, random)
+    return q, scale, qt, scale_t
+
+
+def dequantize_mxfp4(q, scale, cols, dtype=torch.bfloat16):
+    """The values [n, cols] of codes and scales."""
+    out = torch.empty((q.shape[0], cols), dtype=dtype, device=q.device)
+    L.moe_dequantize_mxfp4(q.shape[0], cols, q, q.shape[1], scale, scale.shape[1], out, cols,
+                           _dtype(out))
+    return out
+
+
+def quantize_weights_mxfp4(w: torch.Tensor):
+    """bf16 or fp32 [batch, rows, cols] (cols a multiple of 128) -> codes [batch, rows, cols/2] and
+    scales [batch, rows, cols/32], as MoELayer and ExpertShare take them."""
+    assert w.dim() == 3 and w.is_contiguous() and w.shape[2] % 128 == 0
+    b, r, c = w.shape
+    q, scale, _, _ = quantize_mxfp4(w.view(b * r, c))
+    return q.view(b, r, c // 2), scale[:, :c // 32].contiguous().view(b, r, c // 32)
+
+
+class Fp4Linear:
+    """y = x W^T in MXFP4 with its gradients: W [N, K] bf16 is kept in both orders, blocks of 32
+    along K for y and along N for dx; x and dy are quantised along the dimension that each product
+    sums over.
+
+    forward(x [M, K] bf16) -> y [M, N] bf16; backward(dy [M, N] bf16), of the last forward, -> dx
+    [M, K] bf16 and adds dy^T x to self.dw [N, K] fp32 (zero_grad clears it).  dy is rounded
+    stochastically, so that the gradients' mean over the roundings is that of the unrounded dy:
+    backward draws the bytes, or takes them as random [M, N] uint8; stochastic=False rounds to
+    nearest.  Both run on the current stream; the caller orders the backward's behind the
+    forward's where they differ.
+    """
+
+    def __init__(self, w: torch.Tensor, train=False, stochastic=True):
+        assert w.dtype == torch.bfloat16 and w.dim() == 2
+        self.N, self.K = w.shape
+        self.train, self.stochastic = train, stochastic
+        self.w_q, self.w_scale, self.wt_q, self.wt_scale = quantize_mxfp4(w, True, train)
+        self.dw = torch.zeros((self.N, self.K), dtype=torch.float32,
+                              device=w.device) if train else None
+        self._x = None
+
+    @staticmethod
+    def _gemm(a, a_scale, b, b_scale, M, N, K, out, accumulate=0):
+        n = L.moe_gemm_mxfp4_workspace_bytes(M, N, K)
+        ws = torch.empty((n,), dtype=torch.uint8, device=a.device) if n else None
+        L.moe_gemm_mxfp4(M, N, K, a, a.shape[1], a_scale, a_scale.shape[1], b, b.shape[1], b_scale,
+                         b_scale.shape[1], out, out.shape[1], _dtype(out), accumulate, ws, n)
+        return out
+
+    def forward(self, x):
+        M = x.shape[0]
+        assert x.dtype == torch.bfloat16 and x.shape == (M, self.K)
+        q, scale, qt, scale_t = quantize_mxfp4(x, True, self.train)
+        self._x = (M, qt, scale_t)
+        y = torch.empty((M, self.N), dtype=torch.bfloat16, device=x.device)
+        return self._gemm(q, scale, self.w_q, self.w_scale, M, self.N, self.K, y)
+
+    def backward(self, dy, random=None):
+        assert self.train, "construct the layer with train=True"
+        assert self._x is not None, "call forward first"
+        M, xt, xt_scale = self._x
+        for t in (xt, xt_scale):  # the forward's, perhaps of another stream
+            t.record_stream(torch.cuda.current_stream())
+        assert dy.dtype == torch.bfloat16 and dy.shape == (M, self.N)
+        if random is None and self.stochastic:
+            random = torch.randint(0, 256, dy.shape, dtype=torch.uint8, device=dy.device)
+        q, scale, qt, scale_t = quantize_mxfp4(dy, True, True, random)
+        dx = torch.empty((M, self.K), dtype=torch.bfloat16, device=dy.device)
+        self._gemm(q, scale, self.wt_q, self.wt_scale, M, self.K, self.N, dx)
+        self._gemm(qt, scale_t, xt, xt_scale, self.N, self.K, M, self.dw, 1)
+        return dx
+
+    def zero_grad(self):
+        self.dw.zero_()
+
+
+class ExpertShare:
+    """Experts first .. first+count-1 of a layer, the share of one GPU: the part of the routed
+    output that they give, y[t] = sum over the choices k of token t that are here of
+    gate[t,k] FFN_e(x[t]), and its gradients.  The whole layer's output is the sum of the shares'
+    (an all-reduce of y over the GPUs, plus the shared expert's output); dx likewise, and dgate
+    [T, K] has its entries where the choices are.
+
+    expert "bf16" or "f32": w13 [count, 2I, H] and w2 [count, H, I]; "mxfp4": codes and scales
+    (quantize_weights_mxfp4), forward only.  forward(x [T, H], topk_idx [T, K], gate [T, K]) of any
+    T, also 0; indices of experts that are not here may have any value.  train: backward(dy [T, H])
+    of the last forward returns (dx, dgate) and fills dw13, dw2 (fp32).  Tensors are allocated in
+    each call, on the current stream.
+    """
+
+    def __init__(self, first, w13, w2, w13_scale=None, w2_scale=None, expert="bf16", train=False):
+        assert expert in ("bf16", "f32", "mxfp4")
+        assert expert != "mxfp4" or (w13_scale is not None and w2_scale is not None)
+        assert expert != "mxfp4" or not train, "the backward is built for the bf16 and fp32 paths"
+        self.first, self.count, self.expert, self.train = first, w13.shape[0], expert, train
+        self.I = w13.shape[1] // 2
+        self.H = w2.shape[1]
+        self.act = torch.float32 if expert == "f32" else torch.bfloat16
+        self.w13, self.w2 = w13, w2
+        if expert == "mxfp4":  # only the packed copies are kept
+            self.w13, self.w2 = _pack_mxfp4(self._problem(1), self.count, w13, w13_scale, w2,
+                                            w2_scale)
+        if train:
+            self.dw13 = torch.empty((self.count, 2 * self.I, self.H), device=w13.device)
+            self.dw2 = torch.empty((self.count, self.H, self.I), device=w13.device)
+        self._kept = None
+
+    def _problem(self, rows):
+        act = L.MOE_F32 if self.expert == "f32" else L.MOE_BF16
+        return L.problem(rows, self.H, self.count, 1, 1, 1, 1, self.I, 0, act, _DT[self.expert])
+
+    def _empty(self, shape, dtype=None):
+        return torch.empty(shape, dtype=dtype or self.act, device=self.w13.device)
+
+    def forward(self, x, topk_idx, gate):
+        T, K = topk_idx.shape
+        H, I, R, dt, i32 = self.H, self.I, T * K, _DT["f32" if self.expert == "f32" else "bf16"], \
+            torch.int32
+        assert x.shape == (T, H) and x.dtype == self.act and topk_idx.dtype == i32
+        assert gate.shape == (T, K) and gate.dtype == torch.float32
+        self._kept = None
+        y = self._empty((T, H))
+        if T == 0:
+            if self.train:
+                self._kept = (T, K)
+            return y
+        offsets, token = self._empty((self.count + 1,), i32), self._empty((R,), i32)
+        row = self._empty((T, K), i32)
+        n = L.moe_sort_by_expert_workspace_bytes(T, K, self.count)
+        ws = self._empty((n,), torch.uint8)
+        L.moe_sort_by_expert(T, K, topk_idx, self.first, self.count, offsets, token, row, ws, n)
+        p, ys = self._problem(R), self._empty((R, H))
+        xs = au = h = None
+        if self.expert == "mxfp4":
+            xq, xs_, _, _ = quantize_mxfp4(x)
+            hq, hs = _mx_buffers(R, I, x.device)
+            L.moe_expert_ffn_up_mxfp4(p, xq, xs_, xs_.shape[1], token, offsets, self.w13, hq, hs,
+                                      hs.shape[1])
+            L.moe_expert_ffn_down_mxfp4(p, hq, hs, hs.shape[1], offsets, self.w2, ys)
+        else:
+            xs, h = self._empty((R, H)), self._empty((R, I))
+            L.moe_dispatch(dt, T, K, H, x, H, row, None, xs, H)
+            if self.train:
+                au = self._empty((R, 2 * I))
+                L.moe_expert_ffn_up_save(p, xs, None, offsets, self.w13, h, au)
+            else:
+                L.moe_expert_ffn_up(p, xs, None, offsets, self.w13, None, h)
+            L.moe_expert_ffn_down(p, h, None, offsets, self.w2, None, ys)
+        L.moe_collect(dt, T, K, H, ys, H, row, gate, y, H)
+        if self.train:
+            self._kept = (T, K, p, dt, offsets, row, gate, xs, au, h, ys)
+        return y
+
+    def backward(self, dy):
+        assert self.train, "construct the share with train=True"
+        assert self._kept is not None, "call forward first"
+        T = self._kept[0]
+        assert dy.shape == (T, self.H) and dy.dtype == self.act
+        if T == 0:
+            self.dw13.zero_()
+            self.dw2.zero_()
+            return self._empty((0, self.H)), self._empty((0, self._kept[1]), torch.float32)
+        _, K, p, dt, offsets, row, gate, xs, au, h, ys = self._kept
+        for t in (offsets, row, gate, xs, au, h, ys):  # the forward's, perhaps of another stream
+            t.record_stream(torch.cuda.current_stream())
+        H, I, R = self.H, self.I, T * K
+        dys, dau, dxs = self._empty((R, H)), self._empty((R, 2 * I)), self._empty((R, H))
+        dgate, dx = self._empty((T, K), torch.float32), self._empty((T, H))
+        L.moe_collect_backward(dt, T, K, H, dy, H, row, gate, ys, H, dys, H, dgate)
+        L.moe_expert_ffn_backward_input(p, offsets, self.w13, self.w2, au, dys, dau, dxs)
+        L.moe_expert_ffn_backward_weight(p, xs, None, offsets, h, dys, dau, self.dw13, self.dw2)
+        L.moe_dispatch_backward(dt, T, K, H, dxs, H, row, None, None, H, dx, H)
+        return dx, dgate
+
+
+def _pack_mxfp4(p, groups, w13, w13_scale, w2, w2_scale):
+    """Packed copies of MXFP4 expert weights."""
+    def out(w):
+        n = L.moe_mxfp4_packed_bytes(groups, w.shape[1], 2 * w.shape[2])
+        return torch.empty((n,), dtype=torch.uint8, device=w.device)
+    p13, p2 = out(w13), out(w2)
+    L.moe_pack_expert_weights_mxfp4(p, w13, w13_scale, w2, w2_scale, p13, p2)
+    return p13, p2
+
+
 # batches up to this mean load per routed expert use the packed-weight GEMMs by default
 PACKED_MAX_MEAN_ROWS = 160
 
@@ -133,7 +345,8 @@ class MoELayer:
 
     Weights: w_router [E,H] fp32, bias [E] fp32 (updated in place by bias_step),
     w13 [E+S,2I,H] and w2 [E+S,H,I] in the expert dtype (uint8 E4M3 codes with
-    w13_scale / w2_scale for the FP8 path).
+    w13_scale / w2_scale for the FP8 path; for expert "mxfp4" the codes and scales of
+    quantize_weights_mxfp4, of which only packed copies are kept: forward only, rows gathered).
 
     gather=False: permute writes x_sorted and the gate/up GEMM reads it.
     gather=True:  permute writes the index maps only (FP8: plus one quantisation of x
@@ -163,7 +376,9 @@ class MoELayer:
         self._seq_offsets = None  # of the balance loss of the last forward
         self._buffers = {}
         self.shape = shape
-        self.gather = gather
+        mx = shape.expert == "mxfp4"
+        assert not (mx and train), "the backward is built for the bf16 and fp32 paths"
+        self.gather = gather = gather or mx
         self.train = train
         can_pack = shape.act == "bf16" and shape.expert in ("bf16", "e4m3")
         if packed is None:
@@ -176,6 +391,10 @@ class MoELayer:
         self.w_router, self.bias = w_router, bias
         self.w13, self.w2, self.w13_scale, self.w2_scale = w13, w2, w13_scale, w2_scale
         self.w13p = self.w2p = self.w13tp = self.w2tp = None
+        if mx:
+            self.w13p, self.w2p = _pack_mxfp4(self.p, shape.E + shape.S, w13, w13_scale, w2,
+                                              w2_scale)
+            self.w13 = self.w2 = self.w13_scale = self.w2_scale = None
         if self.packed:
             self.w13p, self.w2p = torch.empty_like(w13), torch.empty_like(w2)
             L.moe_pack_expert_weights(self.p, w13, w2, self.w13p, self.w2p)
@@ -203,7 +422,10 @@ class MoELayer:
             self.x_scale = None
         if not gather:
             self.x_sorted = self.x_q
-        if shape.expert == "e4m3":
+        if mx:
+            self.x_q, self.x_scale = _mx_buffers(T, H, dev)
+            self.h, self.h_scale = _mx_buffers(R, shape.I, dev)
+        elif shape.expert == "e4m3":
             self.h = torch.empty((R, shape.I), dtype=torch.uint8, device=dev)
             self.h_scale = torch.empty((R, shape.I // 128), dtype=torch.float32, device=dev)
         else:
@@ -269,6 +491,10 @@ class MoELayer:
                           self.inv_perm, None, None, ws, n, stream)
             if self.shape.expert == "e4m3":
                 L.moe_quantize_act_fp8(self.p, x, self.x_q, self.x_scale, stream)
+            elif self.shape.expert == "mxfp4":
+                T, H = self.shape.T, self.shape.H
+                L.moe_quantize_mxfp4(x, L.MOE_BF16, T, H, H, self.x_q, H // 2, self.x_scale,
+                                     self.x_scale.shape[1], stream=stream)
             self._x = x
         else:
             L.moe_permute(self.p, x, self.topk_idx, self.offsets, self.sorted_token,
@@ -276,7 +502,11 @@ class MoELayer:
             self._xin = x
 
     def expert_ffn_up(self, stream=None):
-        if self.packed:
+        if self.shape.expert == "mxfp4":
+            L.moe_expert_ffn_up_mxfp4(self.p, self.x_q, self.x_scale, self.x_scale.shape[1],
+                                      self.sorted_token, self.offsets, self.w13p, self.h,
+                                      self.h_scale, self.h_scale.shape[1], stream)
+        elif self.packed:
             if self.shape.expert == "e4m3":
                 xin, st = (self.x_q, self.sorted_token) if self.gather else (self.x_sorted, None)
             else:
@@ -300,6 +530,10 @@ class MoELayer:
             L.moe_checkpoint_save(self.p, self.au, self.au_q, self.au_scale, stream)
 
     def expert_ffn_down(self, stream=None):
+        if self.shape.expert == "mxfp4":
+            L.moe_expert_ffn_down_mxfp4(self.p, self.h, self.h_scale, self.h_scale.shape[1],
+                                        self.offsets, self.w2p, self.y_sorted, stream)
+            return
         if self.packed:
             L.moe_expert_ffn_down_packed(self.p, self.h, self.h_scale, self.offsets, self.w2p,
                                          self.w2_scale, self.y_sorted, stream)

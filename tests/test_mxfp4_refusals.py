@@ -174,6 +174,9 @@ def test_other_calls_refuse_mxfp4_experts(L):
     bad(L, lib.moe_permute(p, A, A, A, A, A, A, A, A, 1 << 30, None), "x_sorted", U)
     bad(L, lib.moe_permute_noalloc(p, A, A, A, A, A, A, A, None), "x_sorted", U)
     bad(L, lib.moe_expert_ffn(p, A, A, A, A, A, A, A, A, A, 1 << 30, None), "MXFP4", U)
+    bad(L, lib.moe_expert_ffn_up(p, A, A, A, A, A, A, A, None), "MXFP4", U)
+    bad(L, lib.moe_expert_ffn_up_gather(p, A, A, A, A, A, A, A, A, None), "MXFP4", U)
+    bad(L, lib.moe_expert_ffn_down(p, A, A, A, A, A, A, None), "MXFP4", U)
     assert L.moe_workspace_bytes(L.problem(**GOOD), L.MOE_CALL_EXPERT_FFN) == 0
     assert "MXFP4" in L.last_error()
     bad(L, lib.moe_combine_backward(p, A, A, A, A, A, A, None), "backward", U)
@@ -190,16 +193,7 @@ def test_other_calls_refuse_mxfp4_experts(L):
                  (lib.moe_expert_ffn_backward_input_checkpoint, 9)):
         rc = f(p, *[ctypes.c_void_p(4096 * (i + 1)) for i in range(n)], None)
         assert rc in (L.MOE_ERR_UNSUPPORTED, L.MOE_ERR_INVALID_ARG), f
-
-
-def test_unbuilt_forward_calls(L, no_gpu):
-    """The natural-layout forward calls have no kernel for the type; with no GPU they end at the
-    device check, which comes first."""
-    lib, p = L.lib(), P(L)
-    for rc in (lib.moe_expert_ffn_up(p, A, A, A, A, A, A, A, None),
-               lib.moe_expert_ffn_down(p, A, A, A, A, A, A, None),
-               lib.moe_expert_ffn_up_gather(p, A, A, A, A, A, A, A, A, None)):
-        assert rc in (L.MOE_ERR_UNSUPPORTED, L.MOE_ERR_HIP)
+        assert "not gfx950" not in L.last_error()  # refused before the device is looked at
 
 
 SORT = dict(T=300, K=8, idx=A, first=3, count=20, off=B, tok=C, row=D, ws=E, ws_bytes=1 << 20,
