@@ -553,7 +553,7 @@ moe_status moe_gemm_fp8(int64_t M, int64_t N, int64_t K, const void* a, int64_t 
  *                1.5 on already, so that no element lies past 6.  The mean over all bytes is off
  *                by at most 1/512 of a step.  Both forms use an element's one byte.
  * Codes of a last block past cols are 0.  Limits (checked): rows, cols >= 1, ldx >= cols, x aligned
- * to its element, fewer than 2^31 blocks of 128 x 128, with qt fewer than 2^24. */
+ * to its element, fewer than 2^31 blocks of 128 x 128, with qt fewer than 2^23. */
 moe_status moe_quantize_mxfp4(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ldx,
                               void* q, int64_t ldq, void* scale, int64_t lds, void* qt,
                               int64_t ldqt, void* scale_t, int64_t ldst, const void* random,

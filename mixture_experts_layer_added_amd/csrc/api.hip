@@ -955,8 +955,8 @@ moe_status moe_quantize_mxfp4(const void* x, int32_t dtype, int64_t rows, int64_
   constexpr int64_t kMost = (int64_t)1 << 40;
   if (rows < 1 || cols < 1 || rows > kMost || cols > kMost)
     return fail(MOE_ERR_INVALID_ARG, "rows and cols must be in [1, 2^40]");
-  // the transpose takes a workgroup of 256 threads a block, and a launch holds fewer than 2^32
-  if (((rows + 127) / 128) * (double)((cols + 127) / 128) >= (qt ? 16777216.0 : 2147483648.0))
+  // the transpose takes two workgroups of 256 threads a block, and a launch holds fewer than 2^32
+  if (((rows + 127) / 128) * (double)((cols + 127) / 128) >= (qt ? 8388608.0 : 2147483648.0))
     return fail(MOE_ERR_INVALID_ARG, "too many 128x128 blocks");
   if (ldx < cols) return fail(MOE_ERR_INVALID_ARG, "ldx=%lld < cols", (long long)ldx);
   if (!x || (reinterpret_cast<uintptr_t>(x) & (dtype == MOE_F32 ? 3 : 1)))

@@ -4,8 +4,7 @@
 // (1/2, 1, 2 are the steps of 0 .. 2, 2 .. 4, 4 .. 6), a quarter of the scale below.
 // Each element is read once and each code written once.
 //   k_mx_rows: 4 lanes take a block of 32 columns, 8 elements a lane.
-//   k_mx_tile: a workgroup takes 128 x 128 elements through LDS; a wave's lane forms two whole
-//     blocks of 32 rows, of two adjacent columns, without its neighbours.
+//   k_mx_tile: a workgroup takes 128 x 64 elements through LDS and writes both orders.
 //   k_mx_values: 8 values a lane.
 #include <algorithm>
 
@@ -14,7 +13,7 @@
 namespace moe {
 namespace {
 
-constexpr int kTile = 128;
+constexpr int kTileR = 128, kTileC = 64;  // of k_mx_tile
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
@@ -68,6 +67,13 @@ __device__ __forceinline__ uint32_t max8(const float* v) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
   return m;
+}
+
+// the larger of the magnitudes of two pairs, a pair's each by itself, as bits
+__device__ __forceinline__ uint32_t pair_max(uint32_t a, uint32_t b) {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  const u16x2 x = __builtin_bit_cast(u16x2, a), y = __builtin_bit_cast(u16x2, b & 0x7fff7fffu);
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(x, y));
 }
 
 // 8 codes of one block, whose scale code is sc
@@ -137,8 +143,10 @@ __device__ __forceinline__ void keep8(float* p, const float* v) {
   *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
 }
 
-// 128 x 128 elements a workgroup.  Rows: 16 lanes a row, 8 elements a lane, which also go to LDS
-// as they are.  Columns: lane l of wave w takes columns 2 l and 2 l + 1 of rows 32 w .. +31.
+// 128 x 64 elements a workgroup.  Rows: 8 lanes a row, 8 elements a lane, which also go to LDS as
+// they are.  Columns: half h of wave w takes rows 32 w + 16 h .. +15, a lane two adjacent columns; the
+// halves share a block's maximum.  Row r lies at r ^ (r / 16 & 1), so that the halves' rows lie in
+// different banks.
 template <typename T, bool kVec, bool kRandom>
 __global__ __launch_bounds__(256) void k_mx_tile(const T* __restrict__ x, int64_t rows,
                                                  int64_t cols, int64_t ldx,
@@ -149,79 +157,96 @@ __global__ __launch_bounds__(256) void k_mx_tile(const T* __restrict__ x, int64_
                                                  uint8_t* __restrict__ scale_t, int64_t ldst,
                                                  int64_t nb) {
   typedef Pair<T> P;
-  __shared__ __attribute__((aligned(16))) T tile[kTile * kTile];
-  __shared__ __attribute__((aligned(16))) uint8_t s_r[kRandom ? kTile * kTile : 16];
-  const int tid = threadIdx.x, l = tid & 15;
+  __shared__ __attribute__((aligned(16))) T tile[kTileR * kTileC];
+  __shared__ __attribute__((aligned(16))) uint8_t s_r[kRandom ? kTileR * kTileC : 16];
+  __shared__ __attribute__((aligned(4))) uint8_t s_sc[kTileC][4];  // scales of the columns' blocks
+  const int tid = threadIdx.x, l = tid & 7;
   const int64_t rb = blockIdx.x / nb, cb = blockIdx.x - rb * nb;
-  const int64_t r0 = rb * kTile, c0 = cb * kTile;
+  const int64_t r0 = rb * kTileR, c0 = cb * kTileC;
   const int n = (int)max((int64_t)0, min((int64_t)8, cols - c0 - 8 * l));
+  float v[4][8];
+  uint2 rr[4];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    float v[4][8];
-    uint2 rr[4];
+  for (int i = 0; i < 4; ++i) {
+    const int64_t r = r0 + 32 * i + (tid >> 3);
+    const int nr = r < rows ? n : 0;
+    read8<kVec>(x + r * ldx + c0 + 8 * l, nr, v[i]);
+    rr[i] = make_uint2(0, 0);
+    if (kRandom) rr[i] = read8r<T>(rnd + r * cols + c0 + 8 * l, nr);
+  }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t r = r0 + 64 * h + 16 * i + (tid >> 4);
-      const int nr = r < rows ? n : 0;
-      read8<kVec>(x + r * ldx + c0 + 8 * l, nr, v[i]);
-      rr[i] = make_uint2(0, 0);
-      if (kRandom) rr[i] = read8r<T>(rnd + r * cols + c0 + 8 * l, nr);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int at = 64 * h + 16 * i + (tid >> 4);
-      const int64_t r = r0 + at;
-      keep8(tile + at * kTile + 8 * l, v[i]);
-      if (kRandom) *reinterpret_cast<uint2*>(s_r + at * kTile + 8 * l) = rr[i];
-      if (!q) continue;
-      uint32_t m = max8(v[i]);
-      m = max(m, (uint32_t)__shfl_xor((int)m, 1));
-      m = max(m, (uint32_t)__shfl_xor((int)m, 2));
-      const int64_t c = c0 + 8 * (l & ~3);  // the block's first column
-      if (r < rows && c < cols) {
-        const uint32_t sc = mx_scale_code<kRandom>(m);
-        *reinterpret_cast<uint32_t*>(q + r * ldq + (c0 + 8 * l) / 2) =
-            codes8<T, kRandom>(v[i], sc, rr[i]);
-        if ((l & 3) == 0) scale[r * lds + c / kMxBlock] = (uint8_t)sc;
-      }
+  for (int i = 0; i < 4; ++i) {
+    const int at = 32 * i + (tid >> 3), to = at ^ (at >> 4 & 1);
+    const int64_t r = r0 + at;
+    keep8(tile + to * kTileC + 8 * l, v[i]);
+    if (kRandom) *reinterpret_cast<uint2*>(s_r + to * kTileC + 8 * l) = rr[i];
+    if (!q) continue;
+    uint32_t m = max8(v[i]);
+    m = max(m, (uint32_t)__shfl_xor((int)m, 1));
+    m = max(m, (uint32_t)__shfl_xor((int)m, 2));
+    const int64_t c = c0 + 8 * (l & ~3);  // the block's first column
+    if (r < rows && c < cols) {
+      const uint32_t sc = mx_scale_code<kRandom>(m);
+      *reinterpret_cast<uint32_t*>(q + r * ldq + (c0 + 8 * l) / 2) =
+          codes8<T, kRandom>(v[i], sc, rr[i]);
+      // both blocks' scales in one store (lds is a multiple of 16, the first block even)
+      const uint32_t next = (uint32_t)__shfl_down((int)sc, 4);
+      uint8_t* to_scale = scale + r * lds + c / kMxBlock;
+      if (l == 0 && c + kMxBlock < cols)
+        *reinterpret_cast<uint16_t*>(to_scale) = (uint16_t)(sc | next << 8);
+      else if (l == 0)
+        *to_scale = (uint8_t)sc;
     }
   }
   __syncthreads();
-  const int lane = tid & 63, wv = tid >> 6;
-  typename P::type v[32];
-  uint32_t m0 = 0, m1 = 0;
+  const int lane = tid & 63, wv = tid >> 6, p = lane & 31, h = lane >> 5;
+  typename P::type u[16];
+  uint32_t m0 = 0, m1 = 0, both = 0;
+  auto row_of = [&](int k) {
+    const int r = 32 * wv + 16 * h + k;
+    return r ^ (r >> 4 & 1);
+  };
 #pragma unroll
-  for (int k = 0; k < 32; ++k) {
-    v[k] = *reinterpret_cast<const typename P::type*>(tile + (32 * wv + k) * kTile + 2 * lane);
-    m0 = max(m0, abs_bits(P::lo(v[k])));
-    m1 = max(m1, abs_bits(P::hi(v[k])));
+  for (int k = 0; k < 16; ++k) {
+    u[k] = *reinterpret_cast<const typename P::type*>(tile + row_of(k) * kTileC + 2 * p);
+    if constexpr (sizeof(T) == 2) {
+      both = pair_max(both, u[k]);
+    } else {
+      m0 = max(m0, abs_bits(P::lo(u[k])));
+      m1 = max(m1, abs_bits(P::hi(u[k])));
+    }
   }
+  if constexpr (sizeof(T) == 2) {
+    m0 = both << 16;
+    m1 = both & 0xffff0000u;
+  }
+  m0 = max(m0, (uint32_t)__shfl_xor((int)m0, 32));
+  m1 = max(m1, (uint32_t)__shfl_xor((int)m1, 32));
   const uint32_t sc[2] = {mx_scale_code<kRandom>(m0), mx_scale_code<kRandom>(m1)};
-  uint32_t w[2][4];
+  uint32_t w[2][2];
   if (kRandom) {
     const uint32_t s0 = min(sc[0], 254u), s1 = min(sc[1], 254u);
     const T* type = nullptr;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 2; ++j) {
       w[0][j] = w[1][j] = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int k = 8 * j + i;
-        const uint32_t r =
-            *reinterpret_cast<const uint16_t*>(s_r + (32 * wv + k) * kTile + 2 * lane);
-        w[0][j] |= mx_code_random(P::lo(v[k]), s0, r & 255u, type) << (4 * i);
-        w[1][j] |= mx_code_random(P::hi(v[k]), s1, r >> 8, type) << (4 * i);
+        const uint32_t r = *reinterpret_cast<const uint16_t*>(s_r + row_of(k) * kTileC + 2 * p);
+        w[0][j] |= mx_code_random(P::lo(u[k]), s0, r & 255u, type) << (4 * i);
+        w[1][j] |= mx_code_random(P::hi(u[k]), s1, r >> 8, type) << (4 * i);
       }
     }
   } else {
     const float s0 = mx_scale(sc[0]), s1 = mx_scale(sc[1]);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 2; ++j) {
       float a[8], b[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        a[i] = P::lo(v[8 * j + i]);
-        b[i] = P::hi(v[8 * j + i]);
+        a[i] = P::lo(u[8 * j + i]);
+        b[i] = P::hi(u[8 * j + i]);
       }
       w[0][j] = mx_pack8(a, s0);
       w[1][j] = mx_pack8(b, s1);
@@ -231,25 +256,23 @@ __global__ __launch_bounds__(256) void k_mx_tile(const T* __restrict__ x, int64_
   // every wave has its part of the tile in registers: the tile's memory now takes the codes, 64
   // bytes a column (16-byte chunks swizzled by the column's pair), so that 4 lanes write 64 bytes
   char* codes = reinterpret_cast<char*>(tile);
-  const int64_t blk = r0 / kMxBlock + wv;  // this wave's block of rows
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int cc = 2 * lane + h;
-    const bool nan = sc[h] == 255;
-    *reinterpret_cast<uint4*>(codes + cc * 64 + ((wv ^ (lane & 3)) << 4)) =
-        make_uint4(nan ? 0 : w[h][0], nan ? 0 : w[h][1], nan ? 0 : w[h][2], nan ? 0 : w[h][3]);
-    if (c0 + cc < cols && blk * kMxBlock < rows) scale_t[(c0 + cc) * ldst + blk] = (uint8_t)sc[h];
+  for (int j = 0; j < 2; ++j) {
+    const int cc = 2 * p + j;
+    const bool nan = sc[j] == 255;
+    *reinterpret_cast<uint2*>(codes + cc * 64 + ((wv ^ (p & 3)) << 4) + 8 * h) =
+        make_uint2(nan ? 0 : w[j][0], nan ? 0 : w[j][1]);
+    if (h == j) s_sc[cc][wv] = (uint8_t)sc[j];
   }
   __syncthreads();
-  const int ch = tid & 3;
-  if (r0 + kMxBlock * ch >= rows) return;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int cc = 64 * i + (tid >> 2);
-    if (c0 + cc >= cols) continue;
-    *reinterpret_cast<uint4*>(qt + (c0 + cc) * ldqt + r0 / 2 + 16 * ch) =
-        *reinterpret_cast<const uint4*>(codes + cc * 64 + ((ch ^ ((cc >> 1) & 3)) << 4));
-  }
+  const int ch = tid & 3, cc = tid >> 2;
+  if (r0 + kMxBlock * ch >= rows || c0 + cc >= cols) return;
+  // four blocks' scales in one store
+  uint8_t* to_scale = scale_t + (c0 + cc) * ldst + r0 / kMxBlock;
+  if (r0 + 3 * kMxBlock >= rows) to_scale[ch] = s_sc[cc][ch];
+  else if (ch == 0) *reinterpret_cast<uint32_t*>(to_scale) = *reinterpret_cast<uint32_t*>(s_sc[cc]);
+  *reinterpret_cast<uint4*>(qt + (c0 + cc) * ldqt + r0 / 2 + 16 * ch) =
+      *reinterpret_cast<const uint4*>(codes + cc * 64 + ((ch ^ ((cc >> 1) & 3)) << 4));
 }
 
 // values of 8 codes: exact in bf16 too (two significant bits, at least 2^-128), NaN for scale 255
@@ -322,7 +345,7 @@ hipError_t quantize(const T* x, int64_t rows, int64_t cols, int64_t ldx, const u
   // 16-byte loads need every row to start at a multiple of 16 bytes
   const bool vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && ldx * sizeof(T) % 16 == 0;
   if (qt) {
-    const int64_t nb = (cols + kTile - 1) / kTile, nr = (rows + kTile - 1) / kTile;
+    const int64_t nb = (cols + kTileC - 1) / kTileC, nr = (rows + kTileR - 1) / kTileR;
     auto k = vec ? k_mx_tile<T, true, kRandom> : k_mx_tile<T, false, kRandom>;
     hipLaunchKernelGGL(k, dim3((unsigned)(nb * nr)), dim3(256), 0, st, x, rows, cols, ldx, rnd, q,
                        ldq, scale, lds, qt, ldqt, scale_t, ldst, nb);

@@ -66,7 +66,7 @@ def test_quantize(L):
         ("st", F, "their own")])
     none = {**QUANT, "q": None, "qt": None}
     bad(L, f(*none.values()), "both NULL")
-    big = {**QUANT, "rows": 128 << 20, "cols": 128 << 4, "ldx": 128 << 4, "ldq": 1024, "lds": 64,
+    big = {**QUANT, "rows": 128 << 20, "cols": 128 << 3, "ldx": 128 << 3, "ldq": 512, "lds": 32,
            "ldqt": 64 << 20, "ldst": 4 << 20}
     bad(L, f(*big.values()), "blocks")
 
