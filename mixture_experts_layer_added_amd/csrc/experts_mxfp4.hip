@@ -97,8 +97,10 @@ struct GroupArgs {
   int NG, Kd, nblk, n_out;
 };
 
-// one tile of MS sub-tiles of 32 rows, D weight steps on their way
-template <bool kSwiglu, int MS, int D>
+// One tile of MS sub-tiles of 32 rows, D weight steps on their way.  kOnce: no other tile reads these
+// weights, and they pass the L2 by (16 tokens over 32 + 1 experts: 134 us, through the L2 145; weights
+// that several row tiles share lose by it, 4096 tokens 1126 us, 963).
+template <bool kSwiglu, int MS, int D, bool kOnce>
 __device__ __forceinline__ void mx_group_tile(const GroupArgs& g, int group, int n_idx,
                                               int64_t row0, int m_rows, char* smem, uint32_t lds0,
                                               uint32_t lds_sc) {
@@ -141,10 +143,11 @@ __device__ __forceinline__ void mx_group_tile(const GroupArgs& g, int group, int
   uint32_t ws[D + 1];
   auto wload = [&](int kk, int buf) {
     const int at = min(kk, nk - 1) * kUnit;
+    constexpr int kNt = kOnce ? 2 : 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      wb[buf][i] = __builtin_amdgcn_raw_buffer_load_b128(wr, lane * 16 + i * 1024, at, 0);
-    ws[buf] = __builtin_amdgcn_raw_buffer_load_b32(wr, lane * 4, at + 4096, 0);
+      wb[buf][i] = __builtin_amdgcn_raw_buffer_load_b128(wr, lane * 16 + i * 1024, at, kNt);
+    ws[buf] = __builtin_amdgcn_raw_buffer_load_b32(wr, lane * 4, at + 4096, kNt);
   };
   f32x16 acc[MS][2];
 #pragma unroll
@@ -294,6 +297,7 @@ __device__ __forceinline__ void mx_group_tile(const GroupArgs& g, int group, int
 // latency where there are no more groups than that.
 struct Pick {
   int group, n_idx, m0, m_rows;
+  bool once;  // the group's only row tile
   int64_t row0;
 };
 constexpr int kTileCost = 12;
@@ -373,8 +377,11 @@ __device__ __forceinline__ bool pick_tile(const int32_t* __restrict__ offsets, i
     const int local = tile - lane_of(k.mt0, l) * nt;
     p.group = g0 + l;
     p.n_idx = local / mt;
-    p.m0 = local % mt * kRows;
-    p.m_rows = min(kRows, lane_of(k.m, l) - p.m0);
+    // a group's row tiles are of even height (140 rows: 96 and 44, not 128 and 12)
+    const int m = lane_of(k.m, l), high = ((m + mt - 1) / mt + 31) / 32 * 32;
+    p.m0 = local % mt * high;
+    p.m_rows = min(high, m - p.m0);
+    p.once = mt == 1;
     p.row0 = (int64_t)lane_of(k.first, l) + p.m0;
   });
   return true;
@@ -396,8 +403,14 @@ __global__ __launch_bounds__(256, 2) void k_mx_group(GroupArgs g) {
   const int n_idx = __builtin_amdgcn_readfirstlane(p.n_idx);
   const int m_rows = __builtin_amdgcn_readfirstlane(p.m_rows);
   const int64_t row0 = p.row0;
-#define MX_TILE(MS, D) \
-  case MS: mx_group_tile<kSwiglu, MS, D>(g, group, n_idx, row0, m_rows, smem, lds0, lds_sc); break
+  const bool once = __builtin_amdgcn_readfirstlane(p.once);
+#define MX_TILE(MS, D)                                                                           \
+  case MS:                                                                                       \
+    if (once)                                                                                    \
+      mx_group_tile<kSwiglu, MS, D, true>(g, group, n_idx, row0, m_rows, smem, lds0, lds_sc);    \
+    else                                                                                         \
+      mx_group_tile<kSwiglu, MS, D, false>(g, group, n_idx, row0, m_rows, smem, lds0, lds_sc);   \
+    break
   switch ((m_rows + 31) >> 5) {
     MX_TILE(1, 7);
     MX_TILE(2, 7);
