@@ -176,19 +176,21 @@ __device__ __forceinline__ void mx_group_tile(const GroupArgs& g, int group, int
                       512 * m);
   };
 
-  // The order of loads: A(0) A(1) W(0) .. W(D-1) A(2), then at each slot's start A(s + 3) and
+  // The order of loads: A(0) A(1) A(2) W(0) .. W(D-1), then at each slot's start A(s + 3) and
   // before each step W(kk + D).  A slot is complete in LDS one slot ahead of its turn, so that the
-  // next step's first operands can be read before this one's products are done.
-  __syncthreads();  // the previous tile's LDS use is over before the ring is refilled
+  // next step's first operands can be read before this one's products are done.  The loop's count
+  // holds for the slots that it asks for itself, A(3) and on: the first three are waited for here.
+  __syncthreads();  // the ring is refilled only when the LDS is free
   aload(0);
   aload(1);
+  aload(2);
+  __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
   for (int j = 0; j < D; ++j) {
     wload(j, j);
     __builtin_amdgcn_sched_barrier(0);
   }
-  aload(2);
-  wait_vm<5 * D + MS>();  // A(0), A(1)
+  wait_vm<5 * D>();  // A(0), A(1), A(2)
   asm volatile("s_barrier" ::: "memory");
 #pragma unroll
   for (int m = 0; m < MS; ++m) scale(0, m, 0);
@@ -201,7 +203,7 @@ __device__ __forceinline__ void mx_group_tile(const GroupArgs& g, int group, int
     for (int j = 0; j <= D; ++j) {
       const int kk = kt + j;
       if ((j & 1) == 0) {
-        // A(kk/2 + 1) is complete: behind it are four steps' weights and A(kk/2 + 2)
+        // A(kk/2 + 1) is complete: behind it are four steps' weights and A(kk/2 + 2) (kk >= 4)
         wait_vm<MS + 20>();
         asm volatile("s_barrier" ::: "memory");
         aload((kk >> 1) + 3);
@@ -377,10 +379,8 @@ __device__ __forceinline__ bool pick_tile(const int32_t* __restrict__ offsets, i
     const int local = tile - lane_of(k.mt0, l) * nt;
     p.group = g0 + l;
     p.n_idx = local / mt;
-    // a group's row tiles are of even height (140 rows: 96 and 44, not 128 and 12)
-    const int m = lane_of(k.m, l), high = ((m + mt - 1) / mt + 31) / 32 * 32;
-    p.m0 = local % mt * high;
-    p.m_rows = min(high, m - p.m0);
+    p.m0 = local % mt * kRows;
+    p.m_rows = min(kRows, lane_of(k.m, l) - p.m0);
     p.once = mt == 1;
     p.row0 = (int64_t)lane_of(k.first, l) + p.m0;
   });
