@@ -6,7 +6,7 @@
 
 #include <mutex>
 
-#include "common.h"
+#include "launch_added.h"
 
 namespace moe {
 

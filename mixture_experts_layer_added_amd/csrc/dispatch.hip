@@ -15,7 +15,7 @@
 // Sums and dots in fp32, in the order of the choices; a row is rounded once.
 #include <algorithm>
 
-#include "common.h"
+#include "launch_added.h"
 
 namespace moe {
 namespace {

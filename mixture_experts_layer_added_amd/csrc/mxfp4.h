@@ -2,7 +2,7 @@
 // 1.5, 2, 3, 4, 6), two a byte with the even element in the low four bits, and one E8M0 scale,
 // 2^(code - 127), per 32 elements; scale code 255 is NaN and makes its whole block NaN.
 #pragma once
-#include "common.h"
+#include "launch_added.h"
 
 namespace moe {
 
