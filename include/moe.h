@@ -41,7 +41,8 @@
  * 32-bit byte offsets); 1 <= E <= 512, E % G == 0, 1 <= G <= 64,
  * 1 <= M <= G, 1 <= J <= min(E/G, 8), 1 <= K <= min(M*E/G, 16); S in {0, 1}.
  * Dtypes: act_dtype F32 with expert_dtype F32, or act_dtype BF16 with expert_dtype
- * BF16 or FP8_E4M3.  Inputs must be finite, but where a call says what becomes of others.
+ * BF16, FP8_E4M3 or (the calls that say so) MXFP4.  Inputs must be finite, but where a call says
+ * what becomes of others.
  */
 #ifndef MOE_H
 #define MOE_H
@@ -133,7 +134,7 @@ moe_status moe_route(const moe_problem* p, const void* x, const float* w_router,
  *   x_sorted_scale [R,H/128] fp32 out (FP8 only, else NULL)
  *   ws           >= moe_workspace_bytes(p, MOE_CALL_PERMUTE) bytes
  * x_sorted = NULL: only offsets, sorted_token and inv_perm are written (x and
- * x_sorted_scale are then not used), for moe_expert_ffn_up_gather.
+ * x_sorted_scale are then not used), for moe_expert_ffn_up_gather; with MXFP4 experts always.
  * Deterministic: every output is a pure function of the inputs. */
 moe_status moe_permute(const moe_problem* p, const void* x, const int32_t* topk_idx,
                        int32_t* offsets, int32_t* sorted_token, int32_t* inv_perm,

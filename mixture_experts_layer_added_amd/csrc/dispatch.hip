@@ -8,11 +8,16 @@
 //   k_sort_small: up to 1024 pairs, one workgroup, one launch.
 //   k_sort_count (1024 pairs a workgroup), k_sort_scan (a workgroup an expert; up to 64 workgroups of
 //     pairs sum the counts themselves), k_sort_place.
+//   512 pairs 3.3 us, 18,822 pairs 8 in two launches: latency, of the barriers of ranking and
+//   scanning in the one, of the second launch in the other.
 // Moving: everything goes by token, one read or write of a token's own row and one of each of its
 // rows among the experts':
 //   k_spread: rows[r] = w t;  with the rows' partner given also dw = <t, partner[r]>
 //   k_gather: t = sum w rows[r];  with the token's partner given also dw = <partner, rows[r]>
 // Sums and dots in fp32, in the order of the choices; a row is rounded once.
+// Memory bounds them: T = 4096, K = 8, H = 7168 in bf16, k_gather 86 us (6.1 TB/s of 529 MB, mostly
+// reads), k_spread with dots 208 us (4.8 TB/s of 1 GB; a copy reaches 5.0).  T = 3137, K = 6, H = 2000
+// in fp32, half of the pairs here: 22 us, with dots 28.5.
 #include <algorithm>
 
 #include "launch_added.h"

@@ -13,10 +13,18 @@
 // block's 32 columns share one scale of h; down: 64 b + 32 n + c.
 //
 // Kernel.  A workgroup of 4 waves takes up to 128 rows of one group x 4 blocks, a wave one block
-// and every row: weights go from memory to the operand registers, three steps ahead, and are used
-// for all rows; activations (gathered through sorted_token, or in order) go by direct-to-LDS
-// loads into a three-slot ring, 256 of k (a 128-byte line a row) a slot, their scales 16 bytes a
-// row, 512 of k, at a time.  Two workgroups share a CU.
+// and every row: weights go from memory to the operand registers, three steps ahead (seven where up
+// to 64 rows leave the registers for it), and are used for all rows; activations (gathered through
+// sorted_token, or in order) go by direct-to-LDS loads into a ring of four slots, 256 of k (a
+// 128-byte line a row) a slot, their scales 16 bytes a row, 512 of k, at a time.  Two workgroups
+// share a CU.
+// 32 + 1 experts of H = 7168, I = 2048, both products and the quantiser, 8 choices a token:
+//   16 tokens: 126 to 134 us, 5.8 to 6.1 TB/s of 771 MB.  The weights' way from memory bounds it.
+//   512 tokens (a tile or two of up to 128 rows a group): 212 us, up 131 to 138, down 72.  Tiles of
+//   128 rows x 256 columns do not fill whole rounds of the chip, and a group with two row tiles reads
+//   its weights from the L2 the second time.
+//   4096 tokens: 940 to 980 us, 3.3 to 3.4 PFLOP/s, up 556 to 642.  The card's power bounds it: the
+//   matrix cores are busy 51% of the cycles at 1.5 GHz.
 #include <algorithm>
 
 #include "mxfp4.h"
