@@ -20,10 +20,10 @@
 // share a CU.
 // 32 + 1 experts of H = 7168, I = 2048, both products and the quantiser, 8 choices a token:
 //   16 tokens: 126 to 134 us, 5.8 to 6.1 TB/s of 771 MB.  The weights' way from memory bounds it.
-//   512 tokens (a tile or two of up to 128 rows a group): 212 us, up 131 to 138, down 72.  Tiles of
+//   512 tokens (a tile or two of up to 128 rows a group): 212 to 223 us, up 131 to 138, down 72.  Tiles of
 //   128 rows x 256 columns do not fill whole rounds of the chip, and a group with two row tiles reads
 //   its weights from the L2 the second time.
-//   4096 tokens: 940 to 980 us, 3.3 to 3.4 PFLOP/s, up 556 to 642.  The card's power bounds it: the
+//   4096 tokens: 940 to 1015 us by card, 3.2 to 3.4 PFLOP/s, up 556 to 642.  The card's power bounds it: the
 //   matrix cores are busy 51% of the cycles at 1.5 GHz.
 #include <algorithm>
 

@@ -12,7 +12,7 @@
 // that a lane's two scales of a part are adjacent bytes.  B is the instruction's first operand: a
 // lane's results lie in one row of C.  Split over k (few tiles): fp32 partial sums to the
 // workspace, k_mx_join adds them in order.
-//   4096 x 4096 x 7168, bf16 out, 256 x 256 tiles: 65 us, 3.7 PFLOP/s.  A round of 128 of k takes
+//   4096 x 4096 x 7168, bf16 out, 256 x 256 tiles: 65 to 73 us by card, 3.3 to 3.7 PFLOP/s.  A round of 128 of k takes
 //   0.97 us; its matrix instructions alone take 0.79, because the card's power lets the clock drop to
 //   1.6 GHz under random codes (5.9 to 6.2 PFLOP/s with nothing else, dense).  12 to 14 us do not
 //   grow with K: the first loads, and 7 to 8 for the 34 MB of C that all 256 workgroups store at

@@ -43,23 +43,37 @@ __device__ __forceinline__ uint32_t mx_pack8(const float* v, float s) {
 // Code of v under scale code sc, rounded to one of its two neighbours by a random byte r: up where
 // the fraction between them, in 256ths, passes r + 1/2, so that the mean over all r is v within 1/512
 // of a step.
-// v was fp32: the fraction is formed and compared.
-__device__ __forceinline__ uint32_t mx_code_random(float v, uint32_t sc, uint32_t r, const float*) {
+__device__ __forceinline__ uint32_t mx_code_random(float v, uint32_t sc, uint32_t r) {
   const float a = __builtin_fabsf(v) * mx_scale(254 - sc);
   const bool b2 = a >= 2.0f, b4 = a >= 4.0f;
   const float f = a * (b4 ? 0.5f : b2 ? 1.0f : 2.0f), low = __builtin_floorf(f);
   const uint32_t m = (uint32_t)low + ((f - low) * 256.0f > (float)r + 0.5f);
   return (m + (b4 ? 4u : b2 ? 2u : 0u)) | (__float_as_uint(v) >> 31 << 3);
 }
-// v was bf16: |v| 2^-126 over the scale has the code in its bits 24 .. 22 (the codes below 1 lie among
-// fp32's denormals) and the fraction below them, exactly: of v's 8 bits none falls off but from
-// values that no byte rounds up.  With 2^22 (1 - (r + 1/2)/256) - 1 added the code is the upper one where
-// the fraction is larger.  8 operations in place of 16.  r is given as 255 - r.
-__device__ __forceinline__ uint32_t mx_code_random(float v, uint32_t sc, uint32_t r,
-                                                   const uint16_t*) {
-  const uint32_t a = __float_as_uint(__builtin_amdgcn_ldexpf(__builtin_fabsf(v), 1 - (int)sc));
-  const uint32_t w = (r << 14) + a + 8191u;
-  return (w >> 22) | (__float_as_uint(v) >> 31 << 3);
+// Eight codes at once, for v that were bf16 (those below 1 need no more than 22 bits of fraction).  The
+// conversion adds the seed to the fraction below the code and cuts: with 255 - r in the seed's top
+// byte and 0x7fffff behind it the code is the upper one where the fraction passes r + 1/2.  Compared
+// with the definition for every finite bf16 inside the range of every scale, and every byte.  Of
+// each conversion only the low four bits are used: the second value of a pair takes other bits of the
+// seed, and what the register held before is not kept.  r is given as 255 - r.
+__device__ __forceinline__ uint32_t mx_pack8_random(const float* v, uint32_t sc, uint2 r) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  const float s = mx_scale(sc);
+  auto code = [&](float x, uint32_t bytes, uint32_t i) {
+    const f32x2 p = {x, x};
+    const uint32_t seed = __builtin_amdgcn_perm(bytes, 0x007fffffu, (4 + i) << 24 | 0x020100u);
+    return (uint32_t)__builtin_amdgcn_cvt_scalef32_sr_pk_fp4_f32(
+        0u, __builtin_shufflevector(p, p, 0, -1), seed, s, 0);
+  };
+  auto join = [&](int first) {  // codes first, first + 2, + 4, + 6 in the low halves of four bytes
+    const uint32_t a = __builtin_amdgcn_perm(code(v[first + 2], r.x, first + 2),
+                                             code(v[first], r.x, first), 0x0c0c0400u);
+    const uint32_t b = __builtin_amdgcn_perm(code(v[first + 6], r.y, first + 2),
+                                             code(v[first + 4], r.y, first), 0x0c0c0400u);
+    return __builtin_amdgcn_perm(b, a, 0x05040100u);
+  };
+  const uint32_t even = join(0), odd = join(1) << 4;
+  return (even & 0x0f0f0f0fu) | (odd & 0xf0f0f0f0u);
 }
 
 // D += B A over one block of 64 of k: 32 x 32 outputs, lane l holds 32 codes (16 bytes) of row

@@ -6,9 +6,10 @@
 //   k_mx_rows: 4 lanes take a block of 32 columns, 8 elements a lane.  128 x 7168 bf16: 3.0 us, a
 //     launch and one round of loads (its 2.3 MB would take 0.5).
 //   k_mx_tile: a workgroup takes 128 x 64 elements through LDS and writes both orders.  4099 x 7168
-//     bf16 with random bytes: 45 us, 2.65 TB/s of its 119 MB (24 us at a copy's rate).  It is bound
-//     by the vector unit, two stochastic roundings of 8 operations an element, and by the waits
-//     between its passes through LDS; tiles of 64 x 64 took 50.
+//     bf16 with random bytes: 43 us, 2.8 TB/s of its 119 MB (24 us at a copy's rate).  The waits
+//     between its passes bind it (memory, LDS, LDS, memory) with 6 workgroups to a CU by their LDS;
+//     the vector unit is busy for under half of the time.  Stochastic rounding an element at a time,
+//     8 operations where the conversion takes 4, took 45, tiles of 64 x 64 50.
 //   k_mx_values: 8 values a lane.  7168 x 4099 to bf16, rows at odd 2-byte starts: 20.5 us for 74 MB;
 //     4099 x 7168, rows at 16 bytes: 14.8, 5.0 TB/s.
 #include <algorithm>
@@ -81,17 +82,22 @@ __device__ __forceinline__ uint32_t pair_max(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(x, y));
 }
 
+// the bytes that sel takes of r[0], r[1] and of r[2], r[3]
+__device__ __forceinline__ uint32_t bytes_of(const uint32_t* r, uint32_t sel) {
+  return __builtin_amdgcn_perm(__builtin_amdgcn_perm(r[3], r[2], sel),
+                               __builtin_amdgcn_perm(r[1], r[0], sel), 0x05040100u);
+}
+
 // 8 codes of one block, whose scale code is sc
 template <typename T, bool kRandom>
 __device__ __forceinline__ uint32_t codes8(const float* v, uint32_t sc, uint2 r) {
   if (sc == 255) return 0;
   if (!kRandom) return mx_pack8(v, mx_scale(sc));
+  if (sizeof(T) == 2) return mx_pack8_random(v, sc, r);
   uint32_t w = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    w |= mx_code_random(v[i], sc, ((i < 4 ? r.x : r.y) >> (8 * (i & 3))) & 255u,
-                        static_cast<const T*>(nullptr))
-         << (4 * i);
+    w |= mx_code_random(v[i], sc, ((i < 4 ? r.x : r.y) >> (8 * (i & 3))) & 255u) << (4 * i);
   return w;
 }
 
@@ -231,17 +237,22 @@ __global__ __launch_bounds__(256) void k_mx_tile(const T* __restrict__ x, int64_
   uint32_t w[2][2];
   if (kRandom) {
     const uint32_t s0 = min(sc[0], 254u), s1 = min(sc[1], 254u);
-    const T* type = nullptr;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      w[0][j] = w[1][j] = 0;
+      uint32_t r[8];  // bytes of the two columns
+      float a[8], b[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int k = 8 * j + i;
-        const uint32_t r = *reinterpret_cast<const uint16_t*>(s_r + row_of(k) * kTileC + 2 * p);
-        w[0][j] |= mx_code_random(P::lo(u[k]), s0, r & 255u, type) << (4 * i);
-        w[1][j] |= mx_code_random(P::hi(u[k]), s1, r >> 8, type) << (4 * i);
+        r[i] = *reinterpret_cast<const uint16_t*>(s_r + row_of(k) * kTileC + 2 * p);
+        a[i] = P::lo(u[k]);
+        b[i] = P::hi(u[k]);
       }
+      uint2 ra, rb;
+      ra = make_uint2(bytes_of(r, 0x0c0c0400u), bytes_of(r + 4, 0x0c0c0400u));
+      rb = make_uint2(bytes_of(r, 0x0c0c0501u), bytes_of(r + 4, 0x0c0c0501u));
+      w[0][j] = codes8<T, true>(a, s0, ra);
+      w[1][j] = codes8<T, true>(b, s1, rb);
     }
   } else {
     const float s0 = mx_scale(sc[0]), s1 = mx_scale(sc[1]);
