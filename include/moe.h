@@ -585,7 +585,9 @@ moe_status moe_gemm_mxfp4(int64_t M, int64_t N, int64_t K, const void* a, int64_
 /* ---------------- experts in MXFP4 (act_dtype MOE_BF16, expert_dtype MOE_MXFP4) ----------------
  * h = mx(silu(x W1^T) (x W3^T)), y = h W2^T per group, mx the quantisation above along a row: 0.53
  * bytes a weight in place of 1 or 2.  moe_route, moe_permute (x_sorted NULL), moe_combine and
- * moe_bias_update go with it; the other expert calls and the backward refuse this type.
+ * moe_bias_update go with it; the other expert calls and the backward refuse this type.  In the
+ * three calls below K <= 16 may pass M*E/G: a share of the experts (next section) is described by
+ * its tokens and their K choices, of which any number may lie in it.
  *
  * Offline: w13 [E+S, 2I, H/2] and w13_scale [E+S, 2I, H/32], w2 [E+S, H, I/2] and w2_scale
  * [E+S, H, I/32] (contiguous, as moe_quantize_mxfp4 writes them with the smallest strides where

@@ -51,7 +51,9 @@ moe_status check_device(int* cus) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-moe_status validate(const moe_problem* p, Dims* d) {
+// share: for calls that take the experts as they come, without routing to them; a token of a share
+// of the experts may have more choices than the share has experts
+moe_status validate(const moe_problem* p, Dims* d, bool share = false) {
   if (!p) return fail(MOE_ERR_INVALID_ARG, "problem is NULL");
   if (p->T < 1) return fail(MOE_ERR_INVALID_ARG, "T=%lld must be >= 1", (long long)p->T);
   if (p->K < 1 || p->K > 16) return fail(MOE_ERR_INVALID_ARG, "K=%d must be in [1,16]", p->K);
@@ -71,7 +73,8 @@ moe_status validate(const moe_problem* p, Dims* d) {
   if (p->M < 1 || p->M > p->G) return fail(MOE_ERR_INVALID_ARG, "M=%d must be in [1,G]", p->M);
   if (p->J < 1 || p->J > gs || p->J > 8)
     return fail(MOE_ERR_INVALID_ARG, "J=%d must be in [1,min(E/G,8)]", p->J);
-  if (p->K > p->M * gs) return fail(MOE_ERR_INVALID_ARG, "K=%d exceeds M*E/G=%d", p->K, p->M * gs);
+  if (!share && p->K > p->M * gs)
+    return fail(MOE_ERR_INVALID_ARG, "K=%d exceeds M*E/G=%d", p->K, p->M * gs);
   if (p->S != 0 && p->S != 1) return fail(MOE_ERR_INVALID_ARG, "S=%d must be 0 or 1", p->S);
   const bool ok_dtypes = (p->act_dtype == MOE_F32 && p->expert_dtype == MOE_F32) ||
                          (p->act_dtype == MOE_BF16 &&
@@ -1056,7 +1059,7 @@ moe_status moe_pack_expert_weights_mxfp4(const moe_problem* p, const void* w13,
                                          const void* w2_scale, void* w13_packed, void* w2_packed,
                                          void* stream) {
   Dims d;
-  moe_status s = validate(p, &d);
+  moe_status s = validate(p, &d, true);
   if (s != MOE_OK) return s;
   if ((s = require_mxfp4(d, "moe_pack_expert_weights_mxfp4")) != MOE_OK) return s;
   if (!w13_packed && !w2_packed)
@@ -1091,7 +1094,7 @@ moe_status moe_expert_ffn_up_mxfp4(const moe_problem* p, const void* x_q, const 
                                    const int32_t* offsets, const void* w13_packed, void* h_q,
                                    void* h_scale, int64_t ldhs, void* stream) {
   Dims d;
-  moe_status s = validate(p, &d);
+  moe_status s = validate(p, &d, true);
   if (s != MOE_OK) return s;
   if ((s = require_mxfp4(d, "moe_expert_ffn_up_mxfp4")) != MOE_OK) return s;
   if ((s = check_mx_tiles(d)) != MOE_OK) return s;
@@ -1120,7 +1123,7 @@ moe_status moe_expert_ffn_down_mxfp4(const moe_problem* p, const void* h_q, cons
                                      int64_t ldhs, const int32_t* offsets, const void* w2_packed,
                                      void* y_sorted, void* stream) {
   Dims d;
-  moe_status s = validate(p, &d);
+  moe_status s = validate(p, &d, true);
   if (s != MOE_OK) return s;
   if ((s = require_mxfp4(d, "moe_expert_ffn_down_mxfp4")) != MOE_OK) return s;
   if ((s = check_mx_tiles(d)) != MOE_OK) return s;

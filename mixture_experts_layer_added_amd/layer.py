@@ -251,16 +251,16 @@ class ExpertShare:
         self.act = torch.float32 if expert == "f32" else torch.bfloat16
         self.w13, self.w2 = w13, w2
         if expert == "mxfp4":  # only the packed copies are kept
-            self.w13, self.w2 = _pack_mxfp4(self._problem(1), self.count, w13, w13_scale, w2,
+            self.w13, self.w2 = _pack_mxfp4(self._problem(1, 1), self.count, w13, w13_scale, w2,
                                             w2_scale)
         if train:
             self.dw13 = torch.empty((self.count, 2 * self.I, self.H), device=w13.device)
             self.dw2 = torch.empty((self.count, self.H, self.I), device=w13.device)
         self._kept = None
 
-    def _problem(self, rows):
+    def _problem(self, T, K):
         act = L.MOE_F32 if self.expert == "f32" else L.MOE_BF16
-        return L.problem(rows, self.H, self.count, 1, 1, 1, 1, self.I, 0, act, _DT[self.expert])
+        return L.problem(T, self.H, self.count, 1, 1, K, 1, self.I, 0, act, _DT[self.expert])
 
     def _empty(self, shape, dtype=None):
         return torch.empty(shape, dtype=dtype or self.act, device=self.w13.device)
@@ -282,7 +282,9 @@ class ExpertShare:
         n = L.moe_sort_by_expert_workspace_bytes(T, K, self.count)
         ws = self._empty((n,), torch.uint8)
         L.moe_sort_by_expert(T, K, topk_idx, self.first, self.count, offsets, token, row, ws, n)
-        p, ys = self._problem(R), self._empty((R, H))
+        # MXFP4: the T tokens, whose rows are gathered; else the T*K rows that dispatch writes
+        p = self._problem(T, K) if self.expert == "mxfp4" else self._problem(R, 1)
+        ys = self._empty((R, H))
         xs = au = h = None
         if self.expert == "mxfp4":
             xq, xs_, _, _ = quantize_mxfp4(x)

@@ -1,0 +1,39 @@
+"""ExpertShare with MXFP4 experts at the ends of its range.  Exact: a token's rows do not depend on
+the other tokens of the call."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from mixture_experts_layer_added_amd import _lib
+    _lib.lib()
+
+
+@pytest.mark.parametrize("T,K,H,count", [(130, 16, 256, 2), (4104, 16, 65536, 2)])
+def test_all_tokens_at_once_and_in_halves(T, K, H, count):
+    """More choices than experts; in the second case T*K*H/2 passes 2^31, T*H/2 does not."""
+    from mixture_experts_layer_added_amd.layer import ExpertShare, quantize_weights_mxfp4
+    g = torch.Generator(device="cuda").manual_seed(T)
+    I = 128
+
+    def rnd(*shape):
+        return torch.randn(shape, generator=g, device="cuda").bfloat16()
+    (a, sa), (b, sb) = (quantize_weights_mxfp4(rnd(count, 2 * I, H) / 64),
+                        quantize_weights_mxfp4(rnd(count, H, I)))
+    share = ExpertShare(3, a, b, sa, sb, "mxfp4")
+    x = rnd(T, H)
+    idx = torch.randint(0, 40, (T, K), generator=g, device="cuda", dtype=torch.int32)
+    gate = torch.rand((T, K), generator=g, device="cuda")
+    y = share.forward(x, idx, gate)
+    half = T // 2
+    parts = [share.forward(x[r].contiguous(), idx[r].contiguous(), gate[r].contiguous())
+             for r in (slice(0, half), slice(half, T))]
+    torch.cuda.synchronize()
+    here = ((idx >= 3) & (idx < 3 + count)).any(1)
+    assert bool(y[here].any(1).all()) and not bool(y[~here].any())
+    assert torch.equal(y, torch.cat(parts))
