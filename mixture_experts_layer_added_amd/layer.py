@@ -48,14 +48,23 @@ def quantize_weights_fp8(w: torch.Tensor, stream=None):
     return q, s
 
 
+def _row_stride(x):
+    """Elements between the rows of a matrix whose rows lie in memory one element after the other; a
+    single row or column may come with any stride."""
+    n, m = x.shape
+    ld = x.stride(0) if n > 1 else m
+    assert (m == 1 or x.stride(1) == 1) and ld >= m, "rows overlap or are not contiguous"
+    return ld
+
+
 def quantize_fp8(x: torch.Tensor, rows=True, cols=False):
     """fp32 or bf16 [n, m] (rows may be strided) -> E4M3 codes (uint8, row length padded to 16)
     and fp32 scales per 128: (q [n, .], scale [n, ceil(m/128)]) along the rows, (qt [m, .],
     scale_t [m, ceil(n/128)]) of the transpose; None for a form not asked for.  On the current
     stream."""
-    assert x.dim() == 2 and x.stride(1) == 1 and x.stride(0) >= x.shape[1]
+    assert x.dim() == 2
     assert x.dtype in (torch.bfloat16, torch.float32)
-    n, m = x.shape
+    (n, m), ld = x.shape, _row_stride(x)
 
     def out(r, c):
         return (torch.empty((r, -(-c // 16) * 16), dtype=torch.uint8, device=x.device),
@@ -64,7 +73,7 @@ def quantize_fp8(x: torch.Tensor, rows=True, cols=False):
     qt, scale_t = out(m, n) if cols else (None, None)
     L._ptrs("moe_quantize_fp8", x.as_strided((1,), (1,)))  # its device; its rows may be strided
     L.moe_quantize_fp8(x.data_ptr(), L.MOE_F32 if x.dtype == torch.float32 else L.MOE_BF16, n, m,
-                       x.stride(0), q, q.shape[1] if rows else 0, scale, qt,
+                       ld, q, q.shape[1] if rows else 0, scale, qt,
                        qt.shape[1] if cols else 0, scale_t)
     return q, scale, qt, scale_t
 
@@ -141,13 +150,13 @@ def quantize_mxfp4(x: torch.Tensor, rows=True, cols=False, random=None):
     scales (uint8, rows padded to 16): (q, scale) along the rows, (qt, scale_t) of the transpose;
     None for a form not asked for.  random: uint8 [n, m], for stochastic rounding.  On the current
     stream."""
-    assert x.dim() == 2 and x.stride(1) == 1 and x.stride(0) >= x.shape[1]
-    n, m = x.shape
+    assert x.dim() == 2
+    (n, m), ld = x.shape, _row_stride(x)
     assert random is None or (random.dtype == torch.uint8 and random.shape == x.shape)
     q, scale = _mx_buffers(n, m, x.device) if rows else (None, None)
     qt, scale_t = _mx_buffers(m, n, x.device) if cols else (None, None)
     L._ptrs("moe_quantize_mxfp4", x.as_strided((1,), (1,)))  # its device; its rows may be strided
-    L.moe_quantize_mxfp4(x.data_ptr(), _dtype(x), n, m, x.stride(0), q, q.shape[1] if rows else 0,
+    L.moe_quantize_mxfp4(x.data_ptr(), _dtype(x), n, m, ld, q, q.shape[1] if rows else 0,
                          scale, scale.shape[1] if rows else 0, qt, qt.shape[1] if cols else 0,
                          scale_t, scale_t.shape[1] if cols else 0, random)
     return q, scale, qt, scale_t
