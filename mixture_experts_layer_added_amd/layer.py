@@ -185,7 +185,7 @@ class Fp4Linear:
     sums over.
 
     forward(x [M, K] bf16) -> y [M, N] bf16; backward(dy [M, N] bf16), of the last forward, -> dx
-    [M, K] bf16 and adds dy^T x to self.dw [N, K] fp32 (zero_grad clears it).  dy is rounded
+    [M, K] bf16 and adds dy^T x to self.dw [N, K] fp32 (zero_grad clears it).  M may be 0.  dy is rounded
     stochastically, so that the gradients' mean over the roundings is that of the unrounded dy:
     backward draws the bytes, or takes them as random [M, N] uint8; stochastic=False rounds to
     nearest.  Both run on the current stream; the caller orders the backward's behind the
@@ -212,6 +212,9 @@ class Fp4Linear:
     def forward(self, x):
         M = x.shape[0]
         assert x.dtype == torch.bfloat16 and x.shape == (M, self.K)
+        if M == 0:
+            self._x = (0, None, None)
+            return torch.empty((0, self.N), dtype=torch.bfloat16, device=x.device)
         q, scale, qt, scale_t = quantize_mxfp4(x, True, self.train)
         self._x = (M, qt, scale_t)
         y = torch.empty((M, self.N), dtype=torch.bfloat16, device=x.device)
@@ -221,9 +224,11 @@ class Fp4Linear:
         assert self.train, "construct the layer with train=True"
         assert self._x is not None, "call forward first"
         M, xt, xt_scale = self._x
+        assert dy.dtype == torch.bfloat16 and dy.shape == (M, self.N)
+        if M == 0:
+            return torch.empty((0, self.K), dtype=torch.bfloat16, device=dy.device)
         for t in (xt, xt_scale):  # the forward's, perhaps of another stream
             t.record_stream(torch.cuda.current_stream())
-        assert dy.dtype == torch.bfloat16 and dy.shape == (M, self.N)
         if random is None and self.stochastic:
             random = torch.randint(0, 256, dy.shape, dtype=torch.uint8, device=dy.device)
         q, scale, qt, scale_t = quantize_mxfp4(dy, True, True, random)
