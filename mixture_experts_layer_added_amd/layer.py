@@ -163,7 +163,9 @@ def quantize_mxfp4(x: torch.Tensor, rows=True, cols=False, random=None):
 
 
 def dequantize_mxfp4(q, scale, cols, dtype=torch.bfloat16):
-    """The values [n, cols] of codes and scales."""
+    """The values [n, cols] of codes [n, .] and scales [n, .], as quantize_mxfp4 returns them."""
+    assert q.dim() == scale.dim() == 2 and q.shape[0] == scale.shape[0], "a row of scales a row"
+    assert q.dtype == scale.dtype == torch.uint8
     out = torch.empty((q.shape[0], cols), dtype=dtype, device=q.device)
     L.moe_dequantize_mxfp4(q.shape[0], cols, q, q.shape[1], scale, scale.shape[1], out, cols,
                            _dtype(out))
