@@ -266,7 +266,12 @@ class ExpertShare:
         self.H = w2.shape[1]
         self.act = torch.float32 if expert == "f32" else torch.bfloat16
         self.w13, self.w2 = w13, w2
-        if expert == "mxfp4":  # only the packed copies are kept
+        if expert != "mxfp4":
+            assert w13.shape == (self.count, 2 * self.I, self.H), "w13 is [count, 2I, H]"
+            assert w2.shape == (self.count, self.H, self.I), "w2 is [count, H, I]"
+            assert w13.dtype == w2.dtype == self.act and w13.device == w2.device
+            assert w13.is_contiguous() and w2.is_contiguous()
+        else:  # only the packed copies are kept
             self.w13, self.w2 = _pack_mxfp4(self._problem(1, 1), self.count, w13, w13_scale, w2,
                                             w2_scale)
         if train:
@@ -346,6 +351,11 @@ class ExpertShare:
 
 def _pack_mxfp4(p, groups, w13, w13_scale, w2, w2_scale):
     """Packed copies of MXFP4 expert weights."""
+    for w, rows, cols in ((w13, 2 * p.I, p.H // 2), (w13_scale, 2 * p.I, p.H // 32),
+                          (w2, p.H, p.I // 2), (w2_scale, p.H, p.I // 32)):
+        assert w.dtype == torch.uint8 and w.shape == (groups, rows, cols), \
+            f"codes and scales of quantize_weights_mxfp4: [{groups}, {rows}, {cols}]"
+
     def out(w):
         n = L.moe_mxfp4_packed_bytes(groups, w.shape[1], 2 * w.shape[2])
         return torch.empty((n,), dtype=torch.uint8, device=w.device)
