@@ -1170,8 +1170,8 @@ moe_status moe_sort_by_expert(int64_t T, int32_t K, const int32_t* topk_idx, int
     return fail(MOE_ERR_INVALID_ARG, "topk_idx, sorted_token and pair_row are required");
   if (T && (topk_idx == pair_row || topk_idx == sorted_token || sorted_token == pair_row))
     return fail(MOE_ERR_INVALID_ARG, "topk_idx, sorted_token and pair_row need buffers of their own");
-  moe_status s = check_ws("moe_sort_by_expert", ws, ws_bytes, need);
-  if (s != MOE_OK) return s;
+  moe_status s = MOE_OK;
+  if (T && (s = check_ws("moe_sort_by_expert", ws, ws_bytes, need)) != MOE_OK) return s;
   if ((s = check_device(nullptr)) != MOE_OK) return s;
   const hipError_t e = launch_sort_by_expert(T * K, K, topk_idx, first, count, offsets,
                                              sorted_token, pair_row, ws,

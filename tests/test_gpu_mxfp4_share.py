@@ -37,3 +37,10 @@ def test_all_tokens_at_once_and_in_halves(T, K, H, count):
     here = ((idx >= 3) & (idx < 3 + count)).any(1)
     assert bool(y[here].any(1).all()) and not bool(y[~here].any())
     assert torch.equal(y, torch.cat(parts))
+
+
+def test_sort_of_no_tokens_without_workspace():
+    from mixture_experts_layer_added_amd import _lib as L
+    off = torch.full((9,), 7, dtype=torch.int32, device="cuda")
+    L.moe_sort_by_expert(0, 4, None, 0, 8, off, None, None, None, 0)
+    assert off.tolist() == [0] * 9

@@ -53,3 +53,10 @@ def test_rows_of_x_are_the_tokens(L, no_gpu):
     fine(L, L.lib().moe_expert_ffn_up_mxfp4, {"p": P(L, **big), **UP, "ldxs": 2048})
     bad(L, L.lib().moe_expert_ffn_up_mxfp4(P(L, **{**big, "T": 65536}), *{**UP, "ldxs": 2048}.values()),
         "2^31")
+
+
+def test_sort_of_no_tokens_needs_offsets_alone(L, no_gpu):
+    from test_mxfp4_refusals import SORT
+    none = {**SORT, "T": 0, "idx": None, "tok": None, "row": None, "ws": None, "ws_bytes": 0}
+    fine(L, L.lib().moe_sort_by_expert, none)
+    bad(L, L.lib().moe_sort_by_expert(*{**none, "off": None}.values()), "offsets")
