@@ -44,3 +44,44 @@ def test_sort_of_no_tokens_without_workspace():
     off = torch.full((9,), 7, dtype=torch.int32, device="cuda")
     L.moe_sort_by_expert(0, 4, None, 0, 8, off, None, None, None, 0)
     assert off.tolist() == [0] * 9
+
+
+@pytest.mark.parametrize("expert", ["bf16", "f32"])
+def test_training_step_captured(expert):
+    """Forward and backward of a share in a graph, replayed on new tokens, choices and gradients, with
+    eager steps of another share of the same weights in between: the same bits."""
+    from mixture_experts_layer_added_amd.layer import ExpertShare
+    g = torch.Generator().manual_seed(11)
+    T, K, E, H, I, count = 70, 3, 10, 256, 128, 4
+    dt = torch.float32 if expert == "f32" else torch.bfloat16
+
+    def rnd(*shape):
+        return torch.randn(shape, generator=g).to(dt).cuda()
+    w13, w2 = rnd(count, 2 * I, H) * 0.05, rnd(count, H, I) * 0.05
+    share, eager = (ExpertShare(3, w13, w2, expert=expert, train=True) for _ in range(2))
+    x, dy = rnd(T, H), rnd(T, H)
+    idx = torch.randint(0, E, (T, K), generator=g, dtype=torch.int32).cuda()
+    gate = torch.rand((T, K), generator=g).cuda()
+
+    def step(s):
+        y = s.forward(x, idx, gate)
+        return y, *s.backward(dy)
+
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        step(share)
+    torch.cuda.current_stream().wait_stream(st)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(share)
+    for n in (E, 5, 2 ** 20, E):  # half of the choices here, most, none
+        x.copy_(torch.randn(x.shape, generator=g))
+        dy.copy_(torch.randn(dy.shape, generator=g))
+        idx.copy_(torch.randint(0, n, idx.shape, generator=g, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (*out, share.dw13, share.dw2)]
+        want = [*step(eager), eager.dw13, eager.dw2]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
