@@ -23,8 +23,12 @@
 //   512 tokens (a tile or two of up to 128 rows a group): 212 to 223 us, up 131 to 138, down 72.  Tiles of
 //   128 rows x 256 columns do not fill whole rounds of the chip, and a group with two row tiles reads
 //   its weights from the L2 the second time.
-//   4096 tokens: 940 to 1015 us by card, 3.2 to 3.4 PFLOP/s, up 556 to 642.  The card's power bounds it: the
-//   matrix cores are busy 51% of the cycles at 1.5 GHz.
+//   4096 tokens: 940 to 1015 us by card, 3.2 to 3.4 PFLOP/s, up 556 to 642.  The matrix cores are busy 50%
+//   (up) and 39% (down) of the cycles, at 1.55 and 1.63 GHz (2.4 unloaded): half is the clock that the
+//   card's power leaves, half are waits; up also fetches 1970 MB, weights and rows read again for row
+//   tiles and columns, and a tenth of the cycles are LDS conflicts.
+// 256 + 1 experts, the groups found over five rounds of 64: 128 tokens, 230 groups with rows, 915 us, 5.9
+// TB/s of weights as with 32 + 1.
 #include <algorithm>
 
 #include "mxfp4.h"

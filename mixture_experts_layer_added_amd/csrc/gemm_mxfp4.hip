@@ -12,11 +12,13 @@
 // that a lane's two scales of a part are adjacent bytes.  B is the instruction's first operand: a
 // lane's results lie in one row of C.  Split over k (few tiles): fp32 partial sums to the
 // workspace, k_mx_join adds them in order.
-//   4096 x 4096 x 7168, bf16 out, 256 x 256 tiles: 65 to 73 us by card, 3.3 to 3.7 PFLOP/s.  A round of 128 of k takes
-//   0.97 us; its matrix instructions alone take 0.79, because the card's power lets the clock drop to
-//   1.6 GHz under random codes (5.9 to 6.2 PFLOP/s with nothing else, dense).  12 to 14 us do not
-//   grow with K: the first loads, and 7 to 8 for the 34 MB of C that all 256 workgroups store at
-//   once.  2048 x 7168 x 4099, fp32 out: 49 us, 12 of them the 59 MB of C.
+//   4096 x 4096 x 7168, bf16 out, 256 x 256 tiles: 65 to 73 us by card, 3.3 to 3.7 PFLOP/s.  A round of
+//   128 of k takes 0.97 us; its 4.3 GFLOP take 0.66 at the rate of a loop of the matrix instruction
+//   alone on random codes (6.5 PFLOP/s: the card's power holds that loop's clock at 1.7 GHz; on zeros it
+//   runs 9.7 at 2.4).  What is between them is LDS reads, loads and the barrier.  12 to 14 us do not
+//   grow with K: the first loads, and 7 to 8 for the 34 MB of C that all 256 workgroups store at once,
+//   with one workgroup a CU and nothing to run beside them.  2048 x 7168 x 4099, fp32 out: 49 us, 12 of
+//   them the 59 MB of C.
 //   128 x 4096 x 7168, 64 x 64 tiles: 11.7 us, of 28 dependent steps at 0.33 and the first loads.
 // Read and stored once: C goes past the caches, operands through them (they are read again by the
 // other tiles of their band).
@@ -35,9 +37,6 @@ constexpr uint32_t kOut = 0x7ffffff0u;  // an offset past every descriptor's ran
 
 __device__ __forceinline__ u32x4 lds16(uint32_t addr) {
   return *reinterpret_cast<const __attribute__((address_space(3))) u32x4*>((uintptr_t)addr);
-}
-__device__ __forceinline__ uint32_t lds2(uint32_t addr) {
-  return *reinterpret_cast<const __attribute__((address_space(3))) uint16_t*>((uintptr_t)addr);
 }
 
 struct GemmArgs {

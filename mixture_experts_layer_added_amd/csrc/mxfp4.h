@@ -53,9 +53,10 @@ __device__ __forceinline__ uint32_t mx_code_random(float v, uint32_t sc, uint32_
 // Eight codes at once, for v that were bf16 (those below 1 need no more than 22 bits of fraction).  The
 // conversion adds the seed to the fraction below the code and cuts: with 255 - r in the seed's top
 // byte and 0x7fffff behind it the code is the upper one where the fraction passes r + 1/2.  Compared
-// with the definition for every finite bf16 inside the range of every scale, and every byte.  Of
-// each conversion only the low four bits are used: the second value of a pair takes other bits of the
-// seed, and what the register held before is not kept.  r is given as 255 - r.
+// with the definition for every finite bf16 inside the range of every scale, and every byte
+// (tests/test_gpu_mxfp4_random_all.py).  Of each conversion only the low four bits are used: the
+// second value of a pair takes other bits of the seed, and what the register held before is not kept.
+// r is given as 255 - r.
 __device__ __forceinline__ uint32_t mx_pack8_random(const float* v, uint32_t sc, uint2 r) {
   typedef float f32x2 __attribute__((ext_vector_type(2)));
   const float s = mx_scale(sc);

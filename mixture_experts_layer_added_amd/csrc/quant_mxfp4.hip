@@ -4,12 +4,17 @@
 // (1/2, 1, 2 are the steps of 0 .. 2, 2 .. 4, 4 .. 6), a quarter of the scale below.
 // Each element is read once and each code written once.
 //   k_mx_rows: 4 lanes take a block of 32 columns, 8 elements a lane.  128 x 7168 bf16: 3.0 us, a
-//     launch and one round of loads (its 2.3 MB would take 0.5).
+//     launch and one round of loads (its 2.3 MB would take 0.5).  4099 x 7168: 17 us, 4.3 TB/s of 74
+//     MB; with random bytes 24, 4.3 TB/s.
 //   k_mx_tile: a workgroup takes 128 x 64 elements through LDS and writes both orders.  4099 x 7168
 //     bf16 with random bytes: 43 us, 2.8 TB/s of its 119 MB (24 us at a copy's rate).  The waits
 //     between its passes bind it (memory, LDS, LDS, memory) with 6 workgroups to a CU by their LDS;
 //     the vector unit is busy for under half of the time.  Stochastic rounding an element at a time,
-//     8 operations where the conversion takes 4, took 45, tiles of 64 x 64 50.
+//     8 operations where the conversion takes 4, took 45, tiles of 64 x 64 50.  To the nearest 32; the
+//     transposed form alone 22, with random bytes 32.
+//   Rows that do not begin at multiples of 16 bytes are read element by element (random bytes whose row
+//     does not begin at a multiple of 8 one by one): rows of 7169 elements, 40 us for the rows, 50 for
+//     the transposed form, 58 for both, with random bytes 44, 62 and 73.
 //   k_mx_values: 8 values a lane.  7168 x 4099 to bf16, rows at odd 2-byte starts: 20.5 us for 74 MB;
 //     4099 x 7168, rows at 16 bytes: 14.8, 5.0 TB/s.
 #include <algorithm>

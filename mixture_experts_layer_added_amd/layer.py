@@ -254,7 +254,8 @@ class ExpertShare:
     (quantize_weights_mxfp4), forward only.  forward(x [T, H], topk_idx [T, K], gate [T, K]) of any
     T, also 0; indices of experts that are not here may have any value.  train: backward(dy [T, H])
     of the last forward returns (dx, dgate) and fills dw13, dw2 (fp32).  Tensors are allocated in
-    each call, on the current stream.
+    each call, on the current stream, for all T*K choices, which could all be here: the backward's
+    limit T*K*max(H, 2I) < 2^30 (bf16; 2^29 in fp32) counts them all.
     """
 
     def __init__(self, first, w13, w2, w13_scale=None, w2_scale=None, expert="bf16", train=False):
