@@ -19,7 +19,7 @@
 // 128-byte line a row) a slot, their scales 16 bytes a row, 512 of k, at a time.  Two workgroups
 // share a CU.
 // 32 + 1 experts of H = 7168, I = 2048, both products and the quantiser, 8 choices a token:
-//   16 tokens: 126 to 134 us, 5.8 to 6.1 TB/s of 771 MB.  The weights' way from memory bounds it.
+//   16 tokens: 126 to 139 us by card, 5.5 to 6.1 TB/s of 771 MB.  The weights' way from memory bounds it.
 //   512 tokens (a tile or two of up to 128 rows a group): 212 to 223 us, up 131 to 138, down 72.  Tiles of
 //   128 rows x 256 columns do not fill whole rounds of the chip, and a group with two row tiles reads
 //   its weights from the L2 the second time.
